@@ -521,6 +521,161 @@ awq_status awq_gemm_w8(const void* x_f16, const uint32_t* qweight,
                        void* y_f16, int path, void* workspace,
                        size_t workspace_bytes, void* stream);
 
+/*
+ * A paged 8-bit key / value cache, the second tensor a decode step streams
+ * beside the weights: quantized as it is written, with the symmetric map of
+ * aissn.com 对称/非对称量化 (zero-point 0) and one fp32 scale per page (a
+ * block of page_size consecutive tokens of one sequence) and head, for keys
+ * and for values (the granularity of xxmr.cn §1.4, a block in place of a
+ * weight group).
+ *
+ *   format       AWQ_KV_INT8: code = rint(v / s) in -127..127, stored as the
+ *                byte code + 128; s = max|v| / 127
+ *                AWQ_KV_E4M3: the OCP fp8 (1-4-3) value of v / s, rounded to
+ *                nearest even; s = max|v| / 448
+ *   n_pages      pages the tensors hold, 1 .. 2^31 - 1
+ *   n_kv_heads   1 .. 65535
+ *   page_size    32, 64, 128 or 256 tokens
+ *   head_dim     64, 96, 128, 192 or 256 channels
+ *   k_codes      device, uint8 [n_pages, n_kv_heads, head_dim / 16, page_size,
+ *                16]: 16 consecutive channels of a token are adjacent
+ *   v_codes      device, uint8 [n_pages, n_kv_heads, page_size / 16, head_dim,
+ *                16]: 16 consecutive tokens of a channel are adjacent
+ *   k_scales, v_scales   device, fp32 [n_pages, n_kv_heads], finite and >= 0
+ * Codes 16-byte aligned, scales 4-byte aligned. A page need not be
+ * initialised before the first write to it.
+ */
+enum { AWQ_KV_INT8 = 0, AWQ_KV_E4M3 = 1 };
+typedef struct {
+    void* k_codes;
+    void* v_codes;
+    float* k_scales;
+    float* v_scales;
+    int64_t n_pages;
+    int n_kv_heads;
+    int page_size;
+    int head_dim;
+    int format;
+} awq_kv_cache;
+
+/*
+ * A batch of sequences over such a cache. Sequence b holds kv_len[b] tokens;
+ * token j is slot j % page_size of page block_table[b, j / page_size]. The
+ * rows cu_tokens[b] .. cu_tokens[b + 1] - 1 of a call's token tensors are
+ * its newest tokens: row cu_tokens[b] + i is position
+ * kv_len[b] - (cu_tokens[b + 1] - cu_tokens[b]) + i. The same descriptor
+ * serves awq_kv_write (kv_len counts the tokens being written),
+ * awq_kv_attention (the queries) and awq_kv_read (the tokens to read).
+ *
+ *   block_table  device, int32 [n_seqs, table_stride], the first max_pages
+ *                entries of a row used. An entry outside [0, n_pages) marks
+ *                a page the cache does not hold: nothing is written to it,
+ *                its tokens read as 0 and attention does not see them.
+ *   cu_tokens    device, int32 [n_seqs + 1], ascending from 0
+ *   kv_len       device, int32 [n_seqs]; lengths past max_pages * page_size
+ *                count as that
+ *   n_seqs       0 .. 32767
+ *   max_tokens   at least every cu_tokens[b + 1] - cu_tokens[b]
+ *   max_len      at least every kv_len[b]
+ * max_tokens and max_len only size the launch (the lengths themselves are
+ * read on the device, so a captured graph can be replayed with new ones).
+ * Whatever the arrays hold, no access leaves the tensors: a kv_len past
+ * max_len counts as max_len, and new tokens past max_tokens (from a
+ * sequence's first new one on, rounded up to whole pages) are not processed.
+ */
+typedef struct {
+    const int32_t* block_table;
+    const int32_t* cu_tokens;
+    const int32_t* kv_len;
+    int64_t table_stride;
+    int max_pages;
+    int n_seqs;
+    int64_t max_tokens;
+    int64_t max_len;
+} awq_kv_seqs;
+
+/*
+ * awq_kv_write - quantizes new keys and values into the cache.
+ * With top = 127 (int8) or 448 (e4m3), for every page p that new tokens
+ * fall into, per head, for keys and values each, in float32:
+ *   a   = max(max |x| over the page's new tokens, 1e-5)
+ *   s   = a / top                    if the page's first token is new,
+ *         max(old scale, a / top)    otherwise
+ *   new codes  = round(x * (1 / s))
+ *   if s grew: old codes of the page = round(q * (old scale * (1 / s)))
+ * (round-half-to-even; 1 / s rounded once). A value thus carries at most
+ * half a step of the page's final scale for its own rounding and for each
+ * later growth of its page's scale (int8; relative 2^-4 each in e4m3); a
+ * prompt written in one call is rounded once.
+ * NaN is stored as 0, an infinity as +-65504.
+ *
+ *   k_f16, v_f16     device, fp16 [n_tokens, n_kv_heads, head_dim], the
+ *                    channels contiguous, 16-byte aligned
+ *   *_token_stride, *_head_stride   in halves, non-negative multiples of 8
+ *   n_tokens         rows of k and v; rows outside [0, n_tokens) and
+ *                    positions below 0 are skipped
+ * A page shared by several sequences may be read by all, but written through
+ * one of them only in a call. Asynchronous on `stream`; results are the same
+ * on every run.
+ */
+awq_status awq_kv_write(const awq_kv_cache* cache, const awq_kv_seqs* seqs,
+                        const void* k_f16, int64_t k_token_stride, int64_t k_head_stride,
+                        const void* v_f16, int64_t v_token_stride, int64_t v_head_stride,
+                        int64_t n_tokens, void* stream);
+
+/*
+ * awq_kv_read - the sequences' newest tokens (all of a sequence when
+ * cu_tokens counts kv_len tokens for it) back as fp16(code * scale).
+ *
+ *   k_f16, v_f16     device, fp16 [n_tokens, n_kv_heads, head_dim], packed,
+ *                    16-byte aligned (outputs). Either may be NULL. Rows of
+ *                    no sequence are left as they were; rows at positions
+ *                    below 0 or in pages the cache does not hold become 0.
+ * Asynchronous on `stream`.
+ */
+awq_status awq_kv_read(const awq_kv_cache* cache, const awq_kv_seqs* seqs,
+                       void* k_f16, void* v_f16, int64_t n_tokens, void* stream);
+
+/*
+ * awq_kv_attention - softmax attention of the newest tokens over the cache,
+ * the keys and values dequantized inside the products:
+ *   o[i, h] = sum_j softmax_j(scale * q[i, h] . K[j, h / r]) V[j, h / r],
+ *   r = n_heads / n_kv_heads,
+ * over the positions j the query at position p sees: all of its sequence, or
+ * with causal != 0 those with j <= p, and with window > 0 only the last
+ * `window` of them (j > p - window). A query that sees no position gets
+ * o = 0 and lse = -infinity. Logits, softmax statistics and sums are fp32;
+ * the weights enter the second product rounded to fp16.
+ *
+ *   q_f16        device, fp16 [n_tokens, n_heads, head_dim], channels
+ *                contiguous, 16-byte aligned, strides in halves, multiples
+ *                of 8
+ *   n_heads      a multiple of n_kv_heads
+ *   scale        finite
+ *   causal       0 or 1; window 0 (none) or > 0 (causal only)
+ *   out_f16      device, fp16 [n_tokens, n_heads, head_dim] (output, same
+ *                rules as q; must not alias the inputs). Rows of no sequence
+ *                are left as they were.
+ *   lse          device, fp32 [n_tokens, n_heads] or NULL (output): the
+ *                natural logarithm of the softmax denominator
+ *   workspace    device memory of at least
+ *                awq_kv_attention_workspace_bytes(...) bytes, 256-byte
+ *                aligned, for splitting long sequences over the GPU, or NULL
+ *                (no split, slower on few sequences). It must be zero-filled
+ *                before its first use; every call leaves it ready for the
+ *                next, of any sizes that fit it. Calls that may run at the
+ *                same time must not share one.
+ * Results do not depend on run-to-run scheduling. Asynchronous on `stream`.
+ * The size query returns 0 for arguments the call would refuse.
+ */
+size_t awq_kv_attention_workspace_bytes(const awq_kv_cache* cache, const awq_kv_seqs* seqs,
+                                        int n_heads);
+awq_status awq_kv_attention(const awq_kv_cache* cache, const awq_kv_seqs* seqs,
+                            const void* q_f16, int64_t q_token_stride, int64_t q_head_stride,
+                            int64_t n_tokens, int n_heads, float scale, int causal, int64_t window,
+                            void* out_f16, int64_t out_token_stride, int64_t out_head_stride,
+                            float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -11,6 +11,9 @@ Entry points (same names as the C ABI in include/awq.h):
         (awq_gemm_ex when a workspace from gemm_workspace(M, N, K) is given)
     awq_activation_absmean(x) -> m
     awq_scale_search(w, x, group_size=128, alphas=None) -> losses, best_index, best_scales
+    awq_kv_write(cache, seqs, k, v), awq_kv_read(cache, seqs) -> k, v
+    awq_kv_attention(q, cache, seqs) -> out
+        (a paged 8-bit cache, KVCache, and a batch of sequences over it, KVSeqs)
 """
 
 from __future__ import annotations
@@ -31,7 +34,21 @@ STATUS_NAMES = {
 PATH_AUTO, PATH_GEMV, PATH_GEMM, PATH_SKINNY, PATH_COLTILE = 0, 1, 2, 3, 4
 QUANT_ASYMMETRIC, QUANT_SYMMETRIC = 0, 1
 
+KV_FORMATS = {"int8": 0, "e4m3": 1}
+
 _lib = None
+
+
+class _KVCacheStruct(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("n_kv_heads", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("head_dim", ctypes.c_int), ("format", ctypes.c_int)]
+
+
+class _KVSeqsStruct(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("cu_tokens", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("max_pages", ctypes.c_int), ("n_seqs", ctypes.c_int),
+                ("max_tokens", ctypes.c_int64), ("max_len", ctypes.c_int64)]
 
 
 class AwqError(RuntimeError):
@@ -108,6 +125,15 @@ def load() -> ctypes.CDLL:
     L.awq_quantize_w8.argtypes = [c_vp, c_vp, c_i64, c_i64, c_int, c_int, c_vp, c_vp, c_vp, c_vp]
     L.awq_gemm_w8.restype = c_int
     L.awq_gemm_w8.argtypes = [c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_int, c_vp, c_int, c_vp, c_sz, c_vp]
+    L.awq_kv_write.restype = c_int
+    L.awq_kv_write.argtypes = [c_vp, c_vp, c_vp, c_i64, c_i64, c_vp, c_i64, c_i64, c_i64, c_vp]
+    L.awq_kv_read.restype = c_int
+    L.awq_kv_read.argtypes = [c_vp, c_vp, c_vp, c_vp, c_i64, c_vp]
+    L.awq_kv_attention_workspace_bytes.restype = c_sz
+    L.awq_kv_attention_workspace_bytes.argtypes = [c_vp, c_vp, c_int]
+    L.awq_kv_attention.restype = c_int
+    L.awq_kv_attention.argtypes = [c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_int, ctypes.c_float, c_int, c_i64,
+                                   c_vp, c_i64, c_i64, c_vp, c_vp, c_sz, c_vp]
     _lib = L
     return L
 
@@ -544,3 +570,217 @@ def awq_gemm_w8(x, qweight, scales, zeros, group_size: int = 128, path: int = PA
                             _ptr(workspace), nbytes, _stream(x.device))
     _check("awq_gemm_w8", st)
     return y
+
+
+# ---------------------------------------------------------------- the paged 8-bit key / value cache
+
+class KVCache:
+    """A paged 8-bit key / value cache (awq_kv_cache): the caller's tensors
+    k_codes uint8 [pages, heads, D / 16, page, 16], v_codes uint8 [pages,
+    heads, page / 16, D, 16], k_scales and v_scales fp32 [pages, heads];
+    fmt "int8" or "e4m3". KVCache.empty allocates them."""
+
+    def __init__(self, k_codes, v_codes, k_scales, v_scales, fmt: str = "int8"):
+        torch = _torch()
+        if fmt not in KV_FORMATS:
+            raise ValueError(f"fmt must be one of {sorted(KV_FORMATS)}")
+        _need_gpu("k_codes", k_codes, torch.uint8)
+        _need_gpu("v_codes", v_codes, torch.uint8)
+        _need_gpu("k_scales", k_scales, torch.float32)
+        _need_gpu("v_scales", v_scales, torch.float32)
+        if k_codes.dim() != 5 or k_codes.shape[4] != 16:
+            raise ValueError("k_codes must be [pages, heads, D / 16, page, 16]")
+        pages, heads, dc, page, _ = k_codes.shape
+        if tuple(v_codes.shape) != (pages, heads, page // 16, dc * 16, 16) or page % 16:
+            raise ValueError(f"v_codes must be [{pages}, {heads}, page / 16, {dc * 16}, 16]")
+        if tuple(k_scales.shape) != (pages, heads) or tuple(v_scales.shape) != (pages, heads):
+            raise ValueError(f"k_scales and v_scales must be [{pages}, {heads}]")
+        if len({t.device for t in (k_codes, v_codes, k_scales, v_scales)}) != 1:
+            raise ValueError("the cache's tensors must be on one device")
+        self.k_codes, self.v_codes, self.k_scales, self.v_scales, self.fmt = k_codes, v_codes, k_scales, v_scales, fmt
+        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = pages, heads, page, dc * 16
+        self.device = k_codes.device
+        self._struct = _KVCacheStruct(_ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), pages, heads, page,
+                                      dc * 16, KV_FORMATS[fmt])
+        self._ref = ctypes.addressof(self._struct)
+
+    @classmethod
+    def empty(cls, n_pages: int, n_kv_heads: int, head_dim: int, page_size: int = 64, fmt: str = "int8", device=None):
+        """A cache of n_pages pages that hold nothing yet."""
+        torch = _torch()
+        dev = device or "cuda"
+        return cls(torch.empty((n_pages, n_kv_heads, head_dim // 16, page_size, 16), dtype=torch.uint8, device=dev),
+                   torch.empty((n_pages, n_kv_heads, page_size // 16, head_dim, 16), dtype=torch.uint8, device=dev),
+                   torch.zeros((n_pages, n_kv_heads), dtype=torch.float32, device=dev),
+                   torch.zeros((n_pages, n_kv_heads), dtype=torch.float32, device=dev), fmt)
+
+
+class KVSeqs:
+    """A batch of sequences over a cache (awq_kv_seqs): block_table int32
+    [B, pages], cu_tokens int32 [B + 1], kv_len int32 [B] on the GPU.
+    max_tokens and max_len bound the new tokens and the length of any
+    sequence; without them they are read from the tensors (a
+    synchronisation). The tensors may be changed in place between calls,
+    within those bounds."""
+
+    def __init__(self, block_table, cu_tokens, kv_len, max_tokens: int | None = None, max_len: int | None = None):
+        torch = _torch()
+        for name, t in (("block_table", block_table), ("cu_tokens", cu_tokens), ("kv_len", kv_len)):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name} must be a torch.Tensor")
+            if t.device.type != "cuda":
+                raise ValueError(f"{name} must be a GPU tensor (no CPU path exists)")
+            if t.dtype != torch.int32:
+                raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
+        n = kv_len.numel()
+        if kv_len.dim() != 1 or cu_tokens.dim() != 1 or cu_tokens.numel() != n + 1:
+            raise ValueError("kv_len must be [B] and cu_tokens [B + 1]")
+        if block_table.dim() != 2 or block_table.shape[0] != n:
+            raise ValueError("block_table must be [B, pages]")
+        if not kv_len.is_contiguous() or not cu_tokens.is_contiguous() or \
+                (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+            raise ValueError("kv_len, cu_tokens and the rows of block_table must be contiguous")
+        if not (block_table.device == cu_tokens.device == kv_len.device):
+            raise ValueError("the batch's tensors must be on one device")
+        if max_tokens is None:
+            max_tokens = int((cu_tokens[1:] - cu_tokens[:-1]).max()) if n else 0
+        if max_len is None:
+            max_len = int(kv_len.max()) if n else 0
+        self.block_table, self.cu_tokens, self.kv_len = block_table, cu_tokens, kv_len
+        self.max_tokens, self.max_len, self.n_seqs = int(max_tokens), int(max_len), n
+        self.device = kv_len.device
+        stride = block_table.stride(0) if n > 1 else block_table.shape[1]
+        self._struct = _KVSeqsStruct(_ptr(block_table), _ptr(cu_tokens), _ptr(kv_len), stride, block_table.shape[1], n,
+                                     self.max_tokens, self.max_len)
+        self._ref = ctypes.addressof(self._struct)
+
+
+def _on_device(device, fn, *args):
+    """fn(*args, stream) with `device` current, on its current stream."""
+    torch = _torch()
+    if torch.cuda.current_device() == device.index:
+        return fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    with torch.cuda.device(device):
+        return fn(*args, torch.cuda.current_stream(device).cuda_stream)
+
+
+def _need_tokens(name: str, t, cache, heads: int | None) -> None:
+    """fp16 [T, heads, D] with contiguous channels on the cache's device."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.float16:
+        raise TypeError(f"{name} must be torch.float16, got {t.dtype}")
+    if t.device != cache.device:
+        raise ValueError(f"{name} must be on {cache.device}")
+    if t.dim() != 3 or t.shape[2] != cache.head_dim or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [tokens, {'heads' if heads is None else heads}, {cache.head_dim}]")
+    if t.stride(2) != 1:
+        raise ValueError(f"{name}'s channels must be contiguous")
+
+
+def _strides(t):
+    """Token and head strides; an extent of one has none."""
+    return t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0
+
+
+def _need_seqs(cache, seqs) -> None:
+    if seqs.device != cache.device:
+        raise ValueError(f"seqs must be on {cache.device}")
+
+
+def awq_kv_write(cache: KVCache, seqs: KVSeqs, k, v) -> None:
+    """awq_kv_write: quantizes the batch's new tokens k, v (fp16 [T, heads, D],
+    any token and head strides that are multiples of 8) into the cache."""
+    _need_seqs(cache, seqs)
+    _need_tokens("k", k, cache, cache.n_kv_heads)
+    _need_tokens("v", v, cache, cache.n_kv_heads)
+    T = k.shape[0]
+    if v.shape[0] != T:
+        raise ValueError("k and v must hold the same tokens")
+    st = _on_device(cache.device, load().awq_kv_write, cache._ref, seqs._ref, k.data_ptr(), *_strides(k),
+                    v.data_ptr(), *_strides(v), T)
+    if st != AWQ_OK:
+        _check("awq_kv_write", st)
+
+
+def awq_kv_read(cache: KVCache, seqs: KVSeqs, n_tokens: int | None = None, out=None):
+    """awq_kv_read: the sequences' newest tokens as (k, v), fp16
+    [n_tokens, heads, D] each, rows as seqs.cu_tokens says (n_tokens defaults
+    to its last entry, read with a synchronisation). out: the two tensors to
+    fill, either of them None to leave it out; rows of no sequence stay."""
+    torch = _torch()
+    _need_seqs(cache, seqs)
+    if out is None:
+        T = int(seqs.cu_tokens[-1]) if n_tokens is None else int(n_tokens)
+        out = tuple(torch.zeros((T, cache.n_kv_heads, cache.head_dim), dtype=torch.float16, device=cache.device)
+                    for _ in range(2))
+    k, v = out
+    T = None
+    for name, t in (("k", k), ("v", v)):
+        if t is None:
+            continue
+        _need_tokens(name, t, cache, cache.n_kv_heads)
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if T is not None and t.shape[0] != T:
+            raise ValueError("k and v must hold the same tokens")
+        T = t.shape[0]
+    if T is None:
+        return k, v
+    if n_tokens is not None and n_tokens != T:
+        raise ValueError(f"out must hold {n_tokens} tokens")
+    st = _on_device(cache.device, load().awq_kv_read, cache._ref, seqs._ref, _ptr(k), _ptr(v), T)
+    if st != AWQ_OK:
+        _check("awq_kv_read", st)
+    return k, v
+
+
+def kv_attention_workspace_bytes(cache: KVCache, seqs: KVSeqs, n_heads: int) -> int:
+    return int(load().awq_kv_attention_workspace_bytes(cache._ref, seqs._ref, n_heads))
+
+
+def kv_attention_workspace(cache: KVCache, seqs: KVSeqs, n_heads: int):
+    """A zero-filled uint8 GPU tensor for awq_kv_attention calls of these
+    bounds (max_tokens, max_len) and heads, and of any that need no more.
+    Each call leaves it ready for the next, without clearing."""
+    torch = _torch()
+    nbytes = kv_attention_workspace_bytes(cache, seqs, n_heads)
+    if nbytes == 0:
+        raise AwqError("awq_kv_attention_workspace_bytes", 4, "the call cannot take these arguments")
+    return torch.zeros(nbytes, dtype=torch.uint8, device=cache.device)
+
+
+def awq_kv_attention(q, cache: KVCache, seqs: KVSeqs, scale: float | None = None, causal: bool = True, window: int = 0,
+                     out=None, lse=None, workspace=None):
+    """awq_kv_attention: softmax attention of the batch's newest tokens q (fp16
+    [T, heads, D], heads a multiple of the cache's) over the cache. scale
+    defaults to D ** -0.5; lse, when given, is fp32 [T, heads] and receives
+    the softmax denominators' logarithms. Without `out` the rows of no
+    sequence are 0."""
+    torch = _torch()
+    _need_seqs(cache, seqs)
+    _need_tokens("q", q, cache, None)
+    T, heads, D = q.shape
+    if out is None:
+        out = torch.zeros((T, heads, D), dtype=torch.float16, device=q.device)
+    else:
+        _need_tokens("out", out, cache, heads)
+        if out.shape[0] != T:
+            raise ValueError(f"out must be [{T}, {heads}, {D}]")
+    if lse is not None:
+        _need_gpu("lse", lse, torch.float32)
+        if tuple(lse.shape) != (T, heads) or lse.device != q.device:
+            raise ValueError(f"lse must be [{T}, {heads}] on {q.device}")
+    nbytes = 0
+    if workspace is not None:
+        _need_gpu("workspace", workspace, torch.uint8)
+        if workspace.device != q.device:
+            raise ValueError(f"workspace must be on {q.device}")
+        nbytes = workspace.numel()
+    st = _on_device(cache.device, load().awq_kv_attention, cache._ref, seqs._ref, q.data_ptr(), *_strides(q), T,
+                    heads, D ** -0.5 if scale is None else scale, 1 if causal else 0, window, out.data_ptr(),
+                    *_strides(out), _ptr(lse), _ptr(workspace), nbytes)
+    if st != AWQ_OK:
+        _check("awq_kv_attention", st)
+    return out

@@ -5,7 +5,7 @@
 #include <mutex>
 #include <vector>
 
-#include "awq_internal.h"
+#include "kv_internal.h"
 
 using namespace awq;
 
@@ -735,6 +735,154 @@ awq_status awq_gemm_w8(const void* x_f16, const uint32_t* qweight, const void* s
     a.K = K;
     a.y16 = y;
     return launch_gemm(a, GemmB::kInt8, GemmOut::kF16, as_stream(stream), workspace);
+}
+
+}  // extern "C"
+
+// ---- the paged 8-bit cache ----
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Checks a cache and a batch and lays them out for the kernels. *empty is set
+// when there is nothing to do (no sequence, no token).
+awq_status kv_pages(const awq_kv_cache* cache, const awq_kv_seqs* seqs, int64_t n_tokens, KvPages* out, bool* empty) {
+    if (!cache || !seqs) return AWQ_ERR_NULL;
+    if (cache->format != AWQ_KV_INT8 && cache->format != AWQ_KV_E4M3) return AWQ_ERR_CONFIG;
+    const int page = cache->page_size, dim = cache->head_dim;
+    if (page != 32 && page != 64 && page != 128 && page != 256) return AWQ_ERR_CONFIG;
+    if (dim != 64 && dim != 96 && dim != 128 && dim != 192 && dim != 256) return AWQ_ERR_CONFIG;
+    if (cache->n_pages < 1 || cache->n_pages > INT32_MAX || cache->n_kv_heads < 1 || cache->n_kv_heads > 65535)
+        return AWQ_ERR_SHAPE;
+    if (seqs->n_seqs < 0 || seqs->n_seqs > 32767 || seqs->max_pages < 0 || seqs->table_stride < seqs->max_pages ||
+        seqs->max_tokens < 0 || seqs->max_tokens > INT32_MAX || seqs->max_len < 0 || seqs->max_len > INT32_MAX - 256 ||
+        n_tokens < 0 || n_tokens > INT32_MAX)
+        return AWQ_ERR_SHAPE;
+    *empty = seqs->n_seqs == 0 || seqs->max_tokens == 0 || n_tokens == 0;
+    if (*empty) return AWQ_OK;
+    if (!cache->k_codes || !cache->v_codes || !cache->k_scales || !cache->v_scales || !seqs->cu_tokens ||
+        !seqs->kv_len || (seqs->max_pages > 0 && !seqs->block_table))
+        return AWQ_ERR_NULL;
+    if (!aligned16(cache->k_codes) || !aligned16(cache->v_codes) || !aligned4(cache->k_scales) ||
+        !aligned4(cache->v_scales) || !aligned4(seqs->block_table) || !aligned4(seqs->cu_tokens) ||
+        !aligned4(seqs->kv_len))
+        return AWQ_ERR_ALIGN;
+    out->k_codes = static_cast<uint8_t*>(cache->k_codes);
+    out->v_codes = static_cast<uint8_t*>(cache->v_codes);
+    out->k_scales = cache->k_scales;
+    out->v_scales = cache->v_scales;
+    out->table = seqs->block_table;
+    out->cu = seqs->cu_tokens;
+    out->len = seqs->kv_len;
+    out->table_stride = seqs->table_stride;
+    out->max_pages = seqs->max_pages;
+    out->n_pages = static_cast<int>(cache->n_pages);
+    out->heads = cache->n_kv_heads;
+    out->log2_page = 31 - __builtin_clz(static_cast<unsigned>(page));
+    out->n_tokens = static_cast<int>(n_tokens);
+    out->max_len = static_cast<int>(seqs->max_len);
+    return AWQ_OK;
+}
+
+// strides of a token tensor: whole 16-byte pieces, not negative
+bool strides_ok(int64_t token, int64_t head) {
+    return token >= 0 && head >= 0 && token % 8 == 0 && head % 8 == 0 && token <= kMaxDim && head <= kMaxDim;
+}
+
+}  // namespace
+
+extern "C" {
+
+awq_status awq_kv_write(const awq_kv_cache* cache, const awq_kv_seqs* seqs, const void* k_f16, int64_t k_token_stride,
+                        int64_t k_head_stride, const void* v_f16, int64_t v_token_stride, int64_t v_head_stride,
+                        int64_t n_tokens, void* stream) {
+    KvWriteArgs a{};
+    bool empty = false;
+    const awq_status st = kv_pages(cache, seqs, n_tokens, &a.c, &empty);
+    if (st != AWQ_OK) return st;
+    if (!strides_ok(k_token_stride, k_head_stride) || !strides_ok(v_token_stride, v_head_stride)) return AWQ_ERR_SHAPE;
+    if (empty || seqs->max_pages == 0) return AWQ_OK;
+    if (!k_f16 || !v_f16) return AWQ_ERR_NULL;
+    if (!aligned16(k_f16) || !aligned16(v_f16)) return AWQ_ERR_ALIGN;
+    a.k = static_cast<const half_t*>(k_f16);
+    a.v = static_cast<const half_t*>(v_f16);
+    a.k_token = k_token_stride;
+    a.k_head = k_head_stride;
+    a.v_token = v_token_stride;
+    a.v_head = v_head_stride;
+    a.head_dim = cache->head_dim;
+    a.n_seqs = seqs->n_seqs;
+    a.format = cache->format;
+    a.max_tokens = std::min(seqs->max_tokens, n_tokens);
+    return launch_kv_write(a, as_stream(stream));
+}
+
+awq_status awq_kv_read(const awq_kv_cache* cache, const awq_kv_seqs* seqs, void* k_f16, void* v_f16, int64_t n_tokens,
+                       void* stream) {
+    KvReadArgs a{};
+    bool empty = false;
+    const awq_status st = kv_pages(cache, seqs, n_tokens, &a.c, &empty);
+    if (st != AWQ_OK) return st;
+    if (empty || (!k_f16 && !v_f16)) return AWQ_OK;
+    if (!aligned16(k_f16) || !aligned16(v_f16)) return AWQ_ERR_ALIGN;
+    a.k = static_cast<half_t*>(k_f16);
+    a.v = static_cast<half_t*>(v_f16);
+    a.head_dim = cache->head_dim;
+    a.n_seqs = seqs->n_seqs;
+    a.format = cache->format;
+    a.max_tokens = std::min(seqs->max_tokens, n_tokens);
+    return launch_kv_read(a, as_stream(stream));
+}
+
+size_t awq_kv_attention_workspace_bytes(const awq_kv_cache* cache, const awq_kv_seqs* seqs, int n_heads) {
+    KvPages c{};
+    bool empty = false;
+    if (kv_pages(cache, seqs, 1, &c, &empty) != AWQ_OK) return 0;
+    if (n_heads < 1 || n_heads % cache->n_kv_heads != 0) return 0;
+    if (empty) return 256;
+    return kv_attention_workspace_bytes(seqs->n_seqs, cache->n_kv_heads, n_heads / cache->n_kv_heads, cache->head_dim,
+                                        seqs->max_tokens, seqs->max_len);
+}
+
+awq_status awq_kv_attention(const awq_kv_cache* cache, const awq_kv_seqs* seqs, const void* q_f16,
+                            int64_t q_token_stride, int64_t q_head_stride, int64_t n_tokens, int n_heads, float scale,
+                            int causal, int64_t window, void* out_f16, int64_t out_token_stride,
+                            int64_t out_head_stride, float* lse, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+    KvAttentionArgs a{};
+    bool empty = false;
+    const awq_status st = kv_pages(cache, seqs, n_tokens, &a.c, &empty);
+    if (st != AWQ_OK) return st;
+    if (n_heads < 1 || n_heads % cache->n_kv_heads != 0 || n_tokens * n_heads > INT32_MAX) return AWQ_ERR_SHAPE;
+    if (!strides_ok(q_token_stride, q_head_stride) || !strides_ok(out_token_stride, out_head_stride))
+        return AWQ_ERR_SHAPE;
+    if (!std::isfinite(scale) || (causal != 0 && causal != 1) || window < 0 || (window > 0 && !causal))
+        return AWQ_ERR_CONFIG;
+    if (empty) return AWQ_OK;
+    if (!q_f16 || !out_f16) return AWQ_ERR_NULL;
+    if (!aligned16(q_f16) || !aligned16(out_f16) || !aligned4(lse)) return AWQ_ERR_ALIGN;
+    a.q = static_cast<const half_t*>(q_f16);
+    a.out = static_cast<half_t*>(out_f16);
+    a.lse = lse;
+    a.q_token = q_token_stride;
+    a.q_head = q_head_stride;
+    a.out_token = out_token_stride;
+    a.out_head = out_head_stride;
+    a.head_dim = cache->head_dim;
+    a.n_seqs = seqs->n_seqs;
+    a.format = cache->format;
+    a.ratio = n_heads / cache->n_kv_heads;
+    a.max_tokens = std::min(seqs->max_tokens, n_tokens);
+    a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    a.causal = causal != 0;
+    a.window = static_cast<int>(std::min<int64_t>(window, INT32_MAX));
+    if (workspace) {
+        if (reinterpret_cast<uintptr_t>(workspace) & 255) return AWQ_ERR_ALIGN;
+        if (workspace_bytes < kv_attention_workspace_bytes(a.n_seqs, a.c.heads, a.ratio, a.head_dim, a.max_tokens,
+                                                           a.c.max_len))
+            return AWQ_ERR_WORKSPACE;
+    }
+    return launch_kv_attention(a, workspace, as_stream(stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,716 @@
+// Softmax attention of a batch's newest tokens over the paged 8-bit cache
+// (include/awq.h, awq_kv_attention).
+//
+// Mathematics. A tile of keys gives logits t = ks * (q . kc) * scale * log2 e
+// from the exact fp16 numbers kc of the stored bytes; with the running
+// maximum m the weights are p = 2^(t - m), and sums and outputs carried from
+// earlier tiles are multiplied by 2^(m_old - m). The values' page scale vs
+// goes into the weights: the outputs are kept in units of r, the largest vs
+// so far, and p * (vs / r) * 2^14 is rounded to fp16 for the second product
+// (vs / r <= 1, so it stays below 2^14, and the 2^14 keeps a page of a
+// scale far below the largest out of fp16's subnormal range).
+//
+// Both kernels compute the transposed products: S^T = K . Q^T and
+// O^T = V^T . P^T. A lane then owns one query (a column), so the softmax's
+// statistics are a few registers per lane, and S^T's accumulator layout is
+// P^T's operand layout once the tile's tokens are dealt to S^T's rows so
+// that a lane's registers hold the 16 consecutive tokens of one piece of the
+// stored values. Nothing moves between lanes but the row maxima.
+//
+// Rows. The query rows of a kv head are its tokens times the r query heads
+// that share it (row = token * ratio + head), so grouped heads read each key
+// once.
+#include <algorithm>
+
+#include "kv_internal.h"
+
+namespace awq {
+namespace {
+
+constexpr float kNone = -1.0e38f;       // running maximum before any visible key
+constexpr float kWeightUnit = 16384.0f; // 2^14, the unit of the rounded weights
+constexpr float kTinyScale = 1.0e-20f;  // scales at or below it count as it
+constexpr int kSc1 = 16;                // cache-policy bit sc1 (device scope)
+constexpr float kLn2 = 0.69314718056f;
+
+// Splits of the keys over blocks: split s takes positions
+// [s * tokens, (s + 1) * tokens).
+struct Split {
+    int tokens;
+    float* partials;    // per (row tile, split): [rows][D] outputs, [rows] maxima, [rows] sums
+    int* counters;      // per row tile, zero between launches
+};
+
+__device__ inline __amdgpu_buffer_rsrc_t rsrc(const void* p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), static_cast<short>(0), static_cast<int>(bytes),
+                                             0x00020000);
+}
+
+// The positions rows [row0, row0 + rows) of a kv head see.
+struct Span {
+    int begin, end;             // any of them
+    int all_begin, all_end;     // every one of them
+};
+__device__ inline void visible(const KvAttentionArgs& a, const KvSeq& sq, int token, int& lo, int& hi) {
+    const int p = sq.start + token;
+    hi = a.causal ? min(sq.len, p + 1) : sq.len;
+    lo = a.window > 0 ? max(0, max(p, -1) - a.window + 1) : 0;
+}
+__device__ inline Span row_span(const KvAttentionArgs& a, const KvSeq& sq, int row0, int rows) {
+    const int first = row0 / a.ratio;
+    const int last = min(sq.n - 1, (row0 + rows - 1) / a.ratio);
+    Span s;
+    visible(a, sq, first, s.begin, s.all_end);
+    visible(a, sq, last, s.all_begin, s.end);
+    return s;
+}
+
+// The output of one row: o (in true units) / sum, and its lse.
+__device__ inline void store_lse(const KvAttentionArgs& a, const KvSeq& sq, int kv_head, int row, float m, float sum) {
+    if (a.lse == nullptr) return;
+    const int token = row / a.ratio, head = kv_head * a.ratio + row % a.ratio;
+    a.lse[(static_cast<int64_t>(sq.row0) + token) * (static_cast<int64_t>(a.c.heads) * a.ratio) + head] =
+        sum > 0.f ? (m + __builtin_amdgcn_logf(sum)) * kLn2 : -__builtin_huge_valf();
+}
+__device__ inline half_t* out_row(const KvAttentionArgs& a, const KvSeq& sq, int kv_head, int row) {
+    const int token = row / a.ratio, head = kv_head * a.ratio + row % a.ratio;
+    return a.out + (static_cast<int64_t>(sq.row0) + token) * a.out_token + head * a.out_head;
+}
+
+// A block's rows are complete: so [ROWS][D] outputs in true units, sm and sl
+// their maxima and sums, all in LDS. With one split they are divided and
+// stored; otherwise parked, and the last of the tile's blocks to arrive adds
+// the splits in order (deterministic; nobody waits on anybody).
+template <int D, int ROWS, int NT>
+__device__ inline void finish_rows(const KvAttentionArgs& a, const KvSeq& sq, const Split& sp, int kv_head, int row0,
+                                   int rows, int tile, int split, int n_splits, int first_split, int last_split,
+                                   const float* so, int so_stride, const float* sm, const float* sl, int* s_flag) {
+    const int tid = threadIdx.x;
+    if (first_split >= last_split) {
+        for (int i = tid; i < rows * (D / 4); i += NT) {
+            const int r = i / (D / 4), d = i % (D / 4) * 4;
+            const float inv = sl[r] > 0.f ? 1.0f / sl[r] : 0.f;
+            typedef half_t half4_t __attribute__((ext_vector_type(4)));
+            half4_t v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = static_cast<half_t>(so[r * so_stride + d + j] * inv);
+            *reinterpret_cast<half4_t*>(out_row(a, sq, kv_head, row0 + r) + d) = v;
+        }
+        for (int r = tid; r < rows; r += NT) store_lse(a, sq, kv_head, row0 + r, sm[r], sl[r]);
+        return;
+    }
+    constexpr int kFloats = ROWS * D + 2 * ROWS;
+    float* mine = sp.partials + static_cast<int64_t>(tile) * n_splits * kFloats;
+    const auto rs = rsrc(mine, static_cast<uint32_t>(n_splits) * kFloats * 4u);
+    const int base = split * kFloats * 4;
+    for (int i = tid; i < rows * (D / 4); i += NT) {
+        const int r = i / (D / 4), d = i % (D / 4) * 4;
+        const float4_t v = *reinterpret_cast<const float4_t*>(so + r * so_stride + d);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(kv_u32x4, v), rs, (r * D + d) * 4, base, kSc1);
+    }
+    for (int r = tid; r < rows; r += NT) {
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, sm[r]), rs, (ROWS * D + r) * 4, base, kSc1);
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, sl[r]), rs, (ROWS * D + ROWS + r) * 4, base,
+                                              kSc1);
+    }
+    // sc1 stores and loads go past the per-XCD L2s; every store is complete
+    // before the counter moves, and the loads are issued after it is read
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    if (tid == 0)
+        *s_flag = __hip_atomic_fetch_add(&sp.counters[tile], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                  last_split - first_split;
+    __syncthreads();
+    if (!*s_flag) return;
+    auto part = [&](int s, int word) {
+        return __builtin_bit_cast(float,
+                                  __builtin_amdgcn_raw_buffer_load_b32(rs, word * 4, s * (kFloats * 4), kSc1));
+    };
+    for (int i = tid; i < rows * (D / 4); i += NT) {
+        const int r = i / (D / 4), d = i % (D / 4) * 4;
+        float m = kNone;
+        for (int s = first_split; s <= last_split; ++s) m = fmaxf(m, part(s, ROWS * D + r));
+        float sum = 0.f;
+        float4_t o = {0.f, 0.f, 0.f, 0.f};
+        for (int s = first_split; s <= last_split; ++s) {
+            const float w = __builtin_amdgcn_exp2f(part(s, ROWS * D + r) - m);
+            sum += w * part(s, ROWS * D + ROWS + r);
+            const float4_t v = __builtin_bit_cast(
+                float4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, (r * D + d) * 4, s * (kFloats * 4), kSc1));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[j] += w * v[j];
+        }
+        const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+        typedef half_t half4_t __attribute__((ext_vector_type(4)));
+        half4_t h;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[j] = static_cast<half_t>(o[j] * inv);
+        *reinterpret_cast<half4_t*>(out_row(a, sq, kv_head, row0 + r) + d) = h;
+        if (d == 0) store_lse(a, sq, kv_head, row0 + r, m, sum);
+    }
+    if (tid == 0) __hip_atomic_store(&sp.counters[tile], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// ---------------------------------------------------------------- few rows
+
+// Decode: up to 16 query rows per block. The four waves walk the split's
+// 64-token tiles in turn, each on its own (no LDS in the loop), straight from
+// the cache into MFMA operands, and are joined in LDS at the end.
+// v_mfma_f32_16x16x32_f16: lane l supplies row / column l % 16 and k-slots
+// 8 (l / 16) .. + 7, and holds results 4 (l / 16) + e of column l % 16.
+// S^T row r of sub-tile s4 (0 .. 3) is token 16 (r / 4) + 4 s4 + r % 4 of the
+// tile: quarter q of the wave then holds the 16 tokens 16 q .. of its query,
+// whose values are one 16-byte piece per channel.
+constexpr int kDecodeRows = 16;
+constexpr int kDecodeWaves = 4;
+constexpr int kTile = 64;
+
+// NP: pages a 64-token tile spans (2 for pages of 32, else 1)
+template <int D, int FORMAT, int NP>
+__global__ __launch_bounds__(kDecodeWaves* kWave) void kv_decode_kernel(KvAttentionArgs a, Split sp, int n_splits) {
+    constexpr int DC = D / 16;              // channel pieces of a key
+    constexpr int KC = (DC + 3) / 4;        // of them per lane
+    constexpr int DT = D / 16;              // 16-channel tiles of the output
+    constexpr int NT = kDecodeWaves * kWave;
+    constexpr int SO = D + 4;
+    __shared__ __attribute__((aligned(16))) float so[kDecodeWaves][kDecodeRows][SO];
+    __shared__ float sm[kDecodeWaves][kDecodeRows], sl[kDecodeWaves][kDecodeRows];
+    __shared__ int s_flag;
+
+    const KvPages& c = a.c;
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int col = lane & 15, quarter = lane >> 4;
+    const int split = blockIdx.x;
+    const int b = blockIdx.z;
+    const int kv_head = blockIdx.y % c.heads;
+    const int row0 = blockIdx.y / c.heads * kDecodeRows;
+    const KvSeq sq = kv_seq(c, b);
+    const int all_rows = sq.n * a.ratio;
+    if (row0 >= all_rows) return;
+    const int rows = min(kDecodeRows, all_rows - row0);
+    const Span span = row_span(a, sq, row0, rows);
+    // the splits that hold a visible position; none at all: split 0 writes zeros
+    const int first_split = span.begin < span.end ? span.begin / sp.tokens : 0;
+    const int last_split = span.begin < span.end ? (span.end - 1) / sp.tokens : 0;
+    if (split < first_split || split > last_split) return;
+
+    // ---- queries: k-slots of step 2 i + h are channels 16 (quarter + 4 i) + 8 h .. + 7 ----
+    const int row = row0 + col;
+    int lo = 0, hi = 0;
+    half8_t qf[2 * KC];
+#pragma unroll
+    for (int i = 0; i < 2 * KC; ++i) qf[i] = half8_t{};
+    if (col < rows) {
+        const int token = row / a.ratio;
+        visible(a, sq, token, lo, hi);
+        const half_t* q = a.q + (static_cast<int64_t>(sq.row0) + token) * a.q_token +
+                          (kv_head * a.ratio + row % a.ratio) * a.q_head;
+#pragma unroll
+        for (int i = 0; i < KC; ++i)
+            if (quarter + 4 * i < DC) {
+                qf[2 * i] = *reinterpret_cast<const half8_t*>(q + 16 * (quarter + 4 * i));
+                qf[2 * i + 1] = *reinterpret_cast<const half8_t*>(q + 16 * (quarter + 4 * i) + 8);
+            }
+    }
+
+    float m = kNone, sum = 0.f, unit = 0.f;
+    float4_t acc[DT];
+#pragma unroll
+    for (int t = 0; t < DT; ++t) acc[t] = float4_t{0.f, 0.f, 0.f, 0.f};
+
+    const int page_mask = (1 << c.log2_page) - 1;
+    const int64_t page_bytes = static_cast<int64_t>(D) << c.log2_page;
+    const int from = max(span.begin, split * sp.tokens) / kTile;
+    const int to = (min(static_cast<int64_t>(span.end), (static_cast<int64_t>(split) + 1) * sp.tokens) + kTile - 1) / kTile;
+    for (int tile = from + wave; tile < to; tile += kDecodeWaves) {
+        const int tb = tile * kTile;
+        // ---- this tile's pages ----
+        int64_t block[NP];
+        bool held[NP];
+        float ks[NP], vs[NP];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int p = (tb >> c.log2_page) + i;
+            // a page past the sequence's end counts as not held, whatever its entry
+            const int id = (p << c.log2_page) < sq.len ? kv_page(c, b, p) : -1;
+            held[i] = id >= 0;
+            block[i] = static_cast<int64_t>(max(id, 0)) * c.heads + kv_head;
+            ks[i] = held[i] ? c.k_scales[block[i]] : 0.f;
+            vs[i] = held[i] ? fmaxf(c.v_scales[block[i]], kTinyScale) : kTinyScale;
+        }
+        const int kp = NP == 2 ? col >> 3 : 0, vp = NP == 2 ? quarter >> 1 : 0;
+        const uint8_t* kbase = c.k_codes + (kp ? block[NP - 1] : block[0]) * page_bytes;
+        const uint8_t* vbase = c.v_codes + (vp ? block[NP - 1] : block[0]) * page_bytes;
+        const int slot0 = NP == 2 ? 16 * ((col >> 2) & 1) + (col & 3) : (tb & page_mask) + 16 * (col >> 2) + (col & 3);
+        const int piece0 = NP == 2 ? quarter & 1 : ((tb & page_mask) >> 4) + quarter;
+        kv_u32x4 kr[4][KC], vr[DT];
+#pragma unroll
+        for (int s4 = 0; s4 < 4; ++s4)
+#pragma unroll
+            for (int i = 0; i < KC; ++i) {
+                const int piece = min(quarter + 4 * i, DC - 1);     // past D: the queries' slots are 0
+                kr[s4][i] = *reinterpret_cast<const kv_u32x4*>(
+                    kbase + ((piece << c.log2_page) + slot0 + 4 * s4) * 16);
+            }
+#pragma unroll
+        for (int t = 0; t < DT; ++t)
+            vr[t] = *reinterpret_cast<const kv_u32x4*>(vbase + (piece0 * D + 16 * t + col) * 16);
+
+        // ---- logits ----
+        float s[16];
+        const float kscale = (NP == 2 && quarter >= 2 ? ks[NP - 1] : ks[0]) * a.scale_log2;
+#pragma unroll
+        for (int s4 = 0; s4 < 4; ++s4) {
+            float4_t x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < KC; ++i) {
+                x = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv_unpack8<FORMAT>(kr[s4][i][0], kr[s4][i][1]), qf[2 * i], x,
+                                                           0, 0, 0);
+                x = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv_unpack8<FORMAT>(kr[s4][i][2], kr[s4][i][3]),
+                                                           qf[2 * i + 1], x, 0, 0, 0);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[4 * s4 + e] = x[e] * kscale;
+        }
+        bool whole = tb >= span.all_begin && tb + kTile <= span.all_end;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) whole = whole && held[i];
+        if (!whole) {
+            const bool ok = NP == 2 && quarter >= 2 ? held[NP - 1] : held[0];
+            const int j0 = tb + 16 * quarter;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                s[i] = ok && j0 + i >= lo && j0 + i < hi ? s[i] : -__builtin_huge_valf();
+            // bytes past the sequence's end may be anything, fp8 NaN among them
+            const int n = ok ? min(max(sq.len - j0, 0), 16) : 0;
+            kv_u32x4 keep;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int k = min(max(n - 4 * j, 0), 4);
+                keep[j] = k == 4 ? 0xFFFFFFFFu : (1u << (8 * k)) - 1u;
+            }
+#pragma unroll
+            for (int t = 0; t < DT; ++t) vr[t] &= keep;
+        }
+
+        // ---- softmax ----
+        float top = s[0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float mn = fmaxf(m, top);
+        const float unit_new = fmaxf(unit, NP == 2 ? fmaxf(vs[0], vs[NP - 1]) : vs[0]);
+        const float unit_inv = __builtin_amdgcn_rcpf(unit_new);
+        const float shrink = __builtin_amdgcn_exp2f(m - mn);
+        const float vscale = (NP == 2 && quarter >= 2 ? vs[NP - 1] : vs[0]) * unit_inv * kWeightUnit;
+        const float carry = shrink * (unit * unit_inv);
+        sum *= shrink;
+        half8_t pf[2];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float p = __builtin_amdgcn_exp2f(s[i] - mn);
+            sum += p;
+            pf[i >> 3][i & 7] = static_cast<half_t>(p * vscale);
+        }
+        m = mn;
+        unit = unit_new;
+#pragma unroll
+        for (int t = 0; t < DT; ++t) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[t][e] *= carry;
+            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv_unpack8<FORMAT>(vr[t][0], vr[t][1]), pf[0], acc[t], 0, 0,
+                                                            0);
+            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv_unpack8<FORMAT>(vr[t][2], vr[t][3]), pf[1], acc[t], 0, 0,
+                                                            0);
+        }
+    }
+
+    // ---- the waves' results, in true units ----
+    sum += __shfl_xor(sum, 16);
+    sum += __shfl_xor(sum, 32);
+    const float true_unit = unit * (1.0f / kWeightUnit);
+#pragma unroll
+    for (int t = 0; t < DT; ++t) *reinterpret_cast<float4_t*>(&so[wave][col][16 * t + 4 * quarter]) = acc[t] * true_unit;
+    if (quarter == 0) {
+        sm[wave][col] = m;
+        sl[wave][col] = sum;
+    }
+    __syncthreads();
+    float mm = kNone, ll = 0.f;
+    const int r16 = tid % kDecodeRows;
+    float w[kDecodeWaves];
+#pragma unroll
+    for (int v = 0; v < kDecodeWaves; ++v) mm = fmaxf(mm, sm[v][r16]);
+#pragma unroll
+    for (int v = 0; v < kDecodeWaves; ++v) {
+        w[v] = __builtin_amdgcn_exp2f(sm[v][r16] - mm);
+        ll += w[v] * sl[v][r16];
+    }
+    for (int d = tid / kDecodeRows * 4; d < D; d += NT / kDecodeRows * 4) {
+        float4_t o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int v = 0; v < kDecodeWaves; ++v) o += *reinterpret_cast<const float4_t*>(&so[v][r16][d]) * w[v];
+        *reinterpret_cast<float4_t*>(&so[0][r16][d]) = o;
+    }
+    __syncthreads();
+    if (tid < kDecodeRows) {
+        sm[0][tid] = mm;
+        sl[0][tid] = ll;
+    }
+    __syncthreads();
+    const int tile_id = b * static_cast<int>(gridDim.y) + static_cast<int>(blockIdx.y);
+    finish_rows<D, kDecodeRows, NT>(a, sq, sp, kv_head, row0, rows, tile_id, split, n_splits, first_split, last_split,
+                                    &so[0][0][0], SO, &sm[0][0], &sl[0][0], &s_flag);
+}
+
+// ---------------------------------------------------------------- many rows
+
+// Prefill: 128 query rows per block, 32 per wave. A 64-token tile of keys and
+// values is unpacked to fp16 once per block, into LDS as 16-byte pieces in
+// the operands' order (keys: 8 channels of a token, values: 8 tokens of a
+// channel; neighbouring lanes read neighbouring pieces, so without bank
+// conflicts), the next tile's bytes in flight meanwhile.
+// v_mfma_f32_32x32x16_f16: lane l supplies row / column l % 32 and k-slots
+// 8 (l / 32) .. + 7, and holds results 8 (i / 4) + 4 (l / 32) + i % 4 of
+// column l % 32. S^T row r is token 16 ((r / 4) % 2) + 4 (r / 8) + r % 4 of a
+// 32-token unit, so half h of the wave holds tokens 16 h + i.
+constexpr int kPrefillWaves = 4;
+constexpr int kPrefillRows = 32 * kPrefillWaves;
+
+template <int D, int FORMAT, int NP>
+__global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv_prefill_kernel(KvAttentionArgs a, Split sp,
+                                                                                          int n_splits) {
+    constexpr int DC = D / 16;
+    constexpr int DT = D / 32;
+    constexpr int NT = kPrefillWaves * kWave;
+    constexpr int TILE_PIECES = kTile * DC;         // stored 16-byte pieces of a tile, keys and values each
+    constexpr int PIECES = (TILE_PIECES + NT - 1) / NT;
+    constexpr int SO = D + 4;
+    constexpr int kStage = kTile * D * 2;           // halves of one stage (keys, then values)
+    constexpr size_t kBytes = std::max<size_t>(2 * kStage * sizeof(half_t), size_t{kPrefillRows} * SO * 4);
+    __shared__ __attribute__((aligned(16))) unsigned char lds[kBytes];
+    __shared__ float sm[kPrefillRows], sl[kPrefillRows];
+    __shared__ int s_flag;
+    half8_t* kst[2];
+    half8_t* vst[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        kst[i] = reinterpret_cast<half8_t*>(reinterpret_cast<half_t*>(lds) + i * kStage);
+        vst[i] = kst[i] + kTile * D / 8;
+    }
+
+    const KvPages& c = a.c;
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int col = lane & 31, half = lane >> 5;
+    const int split = blockIdx.x % n_splits;
+    const int b = blockIdx.z;
+    const int kv_head = blockIdx.y;
+    const int row_tiles = gridDim.x / n_splits;
+    // the last rows of a causal chunk see the most: first
+    const int row_tile = row_tiles - 1 - blockIdx.x / n_splits;
+    const int row0 = row_tile * kPrefillRows;
+    const KvSeq sq = kv_seq(c, b);
+    const int all_rows = sq.n * a.ratio;
+    if (row0 >= all_rows) return;
+    const int rows = min(kPrefillRows, all_rows - row0);
+    const Span span = row_span(a, sq, row0, rows);
+    const int first_split = span.begin < span.end ? span.begin / sp.tokens : 0;
+    const int last_split = span.begin < span.end ? (span.end - 1) / sp.tokens : 0;
+    if (split < first_split || split > last_split) return;
+
+    const int wrow = wave * 32 + col;
+    int lo = 0, hi = 0;
+    half8_t qf[DC];
+#pragma unroll
+    for (int i = 0; i < DC; ++i) qf[i] = half8_t{};
+    if (wrow < rows) {
+        const int token = (row0 + wrow) / a.ratio;
+        visible(a, sq, token, lo, hi);
+        const half_t* q = a.q + (static_cast<int64_t>(sq.row0) + token) * a.q_token +
+                          (kv_head * a.ratio + (row0 + wrow) % a.ratio) * a.q_head;
+#pragma unroll
+        for (int i = 0; i < DC; ++i) qf[i] = *reinterpret_cast<const half8_t*>(q + 16 * i + 8 * half);
+    }
+    // what this wave's rows see
+    const Span wspan = wave * 32 < rows ? row_span(a, sq, row0 + wave * 32, min(32, rows - wave * 32))
+                                        : Span{0, 0, 0, 0};
+
+    const int page_mask = (1 << c.log2_page) - 1;
+    const int64_t page_bytes = static_cast<int64_t>(D) << c.log2_page;
+    const int from = max(span.begin, split * sp.tokens) / kTile;
+    const int to = (min(static_cast<int64_t>(span.end), (static_cast<int64_t>(split) + 1) * sp.tokens) + kTile - 1) / kTile;
+
+    struct Pages {
+        bool held[NP];
+        float ks[NP], vs[NP];
+    };
+    kv_u32x4 kr[PIECES], vr[PIECES];
+    auto load = [&](int tile, Pages& pg) {
+        const int tb = tile * kTile;
+        int64_t block[NP];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int p = (tb >> c.log2_page) + i;
+            // a page past the sequence's end counts as not held, whatever its entry
+            const int id = (p << c.log2_page) < sq.len ? kv_page(c, b, p) : -1;
+            pg.held[i] = id >= 0;
+            block[i] = static_cast<int64_t>(max(id, 0)) * c.heads + kv_head;
+            pg.ks[i] = pg.held[i] ? c.k_scales[block[i]] : 0.f;
+            pg.vs[i] = pg.held[i] ? fmaxf(c.v_scales[block[i]], kTinyScale) : kTinyScale;
+        }
+        const int slot0 = NP == 2 ? 0 : tb & page_mask;
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+            const int e = tid + i * NT;
+            if (TILE_PIECES % NT != 0 && e >= TILE_PIECES) break;
+            const int t = e % kTile, ch = e / kTile;            // key piece: token t, channels 16 ch ..
+            const int kslot = NP == 2 ? t & 31 : slot0 + t;
+            kr[i] = *reinterpret_cast<const kv_u32x4*>(c.k_codes + (NP == 2 && t >= 32 ? block[NP - 1] : block[0]) * page_bytes +
+                                                       ((ch << c.log2_page) + kslot) * 16);
+            const int d = e % D, tc = e / D;                    // value piece: channel d, tokens 16 tc ..
+            const int vpiece = NP == 2 ? tc & 1 : (slot0 >> 4) + tc;
+            vr[i] = *reinterpret_cast<const kv_u32x4*>(c.v_codes + (NP == 2 && tc >= 2 ? block[NP - 1] : block[0]) * page_bytes +
+                                                       (vpiece * D + d) * 16);
+        }
+    };
+    auto stage = [&](int tile, const Pages& pg, half8_t* ks, half8_t* vs) {
+        const int tb = tile * kTile;
+        bool whole = tb + kTile <= sq.len;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) whole = whole && pg.held[i];
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+            const int e = tid + i * NT;
+            if (TILE_PIECES % NT != 0 && e >= TILE_PIECES) break;
+            const int t = e % kTile, ch = e / kTile;
+            ks[(2 * ch) * kTile + t] = kv_unpack8<FORMAT>(kr[i][0], kr[i][1]);
+            ks[(2 * ch + 1) * kTile + t] = kv_unpack8<FORMAT>(kr[i][2], kr[i][3]);
+            const int d = e % D, tc = e / D;
+            if (!whole) {
+                // bytes past the sequence's end may be anything, fp8 NaN among them
+                const bool ok = NP == 2 && tc >= 2 ? pg.held[NP - 1] : pg.held[0];
+                const int n = ok ? min(max(sq.len - (tb + 16 * tc), 0), 16) : 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int k = min(max(n - 4 * j, 0), 4);
+                    vr[i][j] &= k == 4 ? 0xFFFFFFFFu : (1u << (8 * k)) - 1u;
+                }
+            }
+            vs[(2 * tc) * D + d] = kv_unpack8<FORMAT>(vr[i][0], vr[i][1]);
+            vs[(2 * tc + 1) * D + d] = kv_unpack8<FORMAT>(vr[i][2], vr[i][3]);
+        }
+    };
+
+    float m = kNone, sum = 0.f, unit = 0.f;
+    float16_t acc[DT];
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[t][e] = 0.f;
+    const int krow = 16 * ((col >> 2) & 1) + 4 * (col >> 3) + (col & 3);
+
+    auto compute = [&](int tile, const Pages& pg, const half8_t* ks, const half8_t* vs) {
+        const int tb = tile * kTile;
+        if (tb >= wspan.end || tb + kTile <= wspan.begin) return;      // none of this wave's rows sees it
+        float16_t s[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[u][e] = 0.f;
+#pragma unroll
+            for (int i = 0; i < DC; ++i)
+                s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ks[(2 * i + half) * kTile + 32 * u + krow], qf[i], s[u], 0,
+                                                              0, 0);
+            const float kscale = pg.ks[NP == 2 ? u : 0] * a.scale_log2;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[u][e] *= kscale;
+        }
+        bool whole = tb >= wspan.all_begin && tb + kTile <= wspan.all_end;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) whole = whole && pg.held[i];
+        if (!whole) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int j = tb + 32 * u + 16 * half + e;
+                    s[u][e] = pg.held[NP == 2 ? u : 0] && j >= lo && j < hi ? s[u][e] : -__builtin_huge_valf();
+                }
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) top = fmaxf(top, s[u][e]);
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float mn = fmaxf(m, top);
+        const float unit_new = fmaxf(unit, NP == 2 ? fmaxf(pg.vs[0], pg.vs[NP - 1]) : pg.vs[0]);
+        const float unit_inv = __builtin_amdgcn_rcpf(unit_new);
+        const float shrink = __builtin_amdgcn_exp2f(m - mn);
+        const float carry = shrink * (unit * unit_inv);
+        sum *= shrink;
+        half8_t pf[2][2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const float vscale = pg.vs[NP == 2 ? u : 0] * unit_inv * kWeightUnit;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float p = __builtin_amdgcn_exp2f(s[u][e] - mn);
+                sum += p;
+                pf[u][e >> 3][e & 7] = static_cast<half_t>(p * vscale);
+            }
+        }
+        m = mn;
+        unit = unit_new;
+#pragma unroll
+        for (int t = 0; t < DT; ++t) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[t][e] *= carry;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vs[(4 * u + 2 * half + k) * D + 32 * t + col],
+                                                                    pf[u][k], acc[t], 0, 0, 0);
+        }
+    };
+
+    if (from < to) {
+        Pages pg[2];
+        load(from, pg[0]);
+        stage(from, pg[0], kst[0], vst[0]);
+        __syncthreads();
+        for (int tile = from; tile < to; tile += 2) {
+            if (tile + 1 < to) load(tile + 1, pg[1]);
+            compute(tile, pg[0], kst[0], vst[0]);
+            if (tile + 1 >= to) break;
+            stage(tile + 1, pg[1], kst[1], vst[1]);
+            __syncthreads();
+            if (tile + 2 < to) load(tile + 2, pg[0]);
+            compute(tile + 1, pg[1], kst[1], vst[1]);
+            if (tile + 2 < to) stage(tile + 2, pg[0], kst[0], vst[0]);
+            __syncthreads();
+        }
+    }
+    __syncthreads();        // the stages are free: the outputs take their place
+
+    sum += __shfl_xor(sum, 32);
+    const float true_unit = unit * (1.0f / kWeightUnit);
+    float* so = reinterpret_cast<float*>(lds);
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float4_t v = {acc[t][4 * q], acc[t][4 * q + 1], acc[t][4 * q + 2], acc[t][4 * q + 3]};
+            *reinterpret_cast<float4_t*>(so + wrow * SO + 32 * t + 8 * q + 4 * half) = v * true_unit;
+        }
+    if (half == 0) {
+        sm[wrow] = m;
+        sl[wrow] = sum;
+    }
+    __syncthreads();
+    const int tile_id = (b * c.heads + kv_head) * row_tiles + row_tile;
+    finish_rows<D, kPrefillRows, NT>(a, sq, sp, kv_head, row0, rows, tile_id, split, n_splits, first_split, last_split,
+                                     so, SO, sm, sl, &s_flag);
+}
+
+// ---------------------------------------------------------------- launch
+
+// Counters at the workspace's start, whatever the call: a split launch has at
+// most this many row tiles.
+constexpr int kCounters = 4096;
+constexpr size_t kCounterBytes = kCounters * sizeof(int);
+
+struct Plan {
+    bool decode;
+    int rows;               // query rows per block
+    int64_t row_tiles;      // per sequence and kv head
+    int splits;
+    int tokens;             // positions per split
+};
+
+// Few query rows per kv head: the decode kernel. The keys are split until the
+// blocks fill the GPU a few times over, each split at least one tile per wave.
+Plan plan_for(int n_seqs, int kv_heads, int ratio, int64_t max_tokens, int64_t max_len, bool have_workspace) {
+    Plan p;
+    const int64_t rows = max_tokens * ratio;
+    p.decode = rows <= 2 * kDecodeRows;
+    p.rows = p.decode ? kDecodeRows : kPrefillRows;
+    p.row_tiles = ceil_div(rows, p.rows);
+    const int64_t tiles = p.row_tiles * n_seqs * kv_heads;
+    const int64_t unit = p.decode ? kTile * kDecodeWaves : kTile * 8;
+    const int64_t units = std::max<int64_t>(1, ceil_div(max_len, unit));
+    int64_t splits = 1;
+    if (have_workspace && tiles <= kCounters) {
+        const int64_t want = static_cast<int64_t>(p.decode ? 4 : 2) * cu_count();
+        splits = std::max<int64_t>(1, std::min(units, want / tiles));
+    }
+    const int64_t per = ceil_div(units, splits);
+    p.tokens = static_cast<int>(std::min<int64_t>(per * unit, INT32_MAX / kTile * kTile));
+    p.splits = static_cast<int>(std::max<int64_t>(1, ceil_div(max_len, p.tokens)));
+    return p;
+}
+
+size_t plan_bytes(const Plan& p, int n_seqs, int kv_heads, int head_dim) {
+    const size_t tiles = static_cast<size_t>(p.row_tiles) * n_seqs * kv_heads;
+    const size_t floats = static_cast<size_t>(p.rows) * (head_dim + 2);
+    return kCounterBytes + (p.splits > 1 ? tiles * p.splits * floats * sizeof(float) : 0);
+}
+
+template <int D, int FORMAT, int NP>
+void launch_np(const KvAttentionArgs& a, const Plan& p, const Split& sp, hipStream_t stream) {
+    if (p.decode)
+        hipLaunchKernelGGL((kv_decode_kernel<D, FORMAT, NP>),
+                           dim3(static_cast<unsigned>(p.splits), static_cast<unsigned>(p.row_tiles * a.c.heads),
+                                static_cast<unsigned>(a.n_seqs)),
+                           dim3(kDecodeWaves * kWave), 0, stream, a, sp, p.splits);
+    else
+        hipLaunchKernelGGL((kv_prefill_kernel<D, FORMAT, NP>),
+                           dim3(static_cast<unsigned>(p.row_tiles * p.splits), static_cast<unsigned>(a.c.heads),
+                                static_cast<unsigned>(a.n_seqs)),
+                           dim3(kPrefillWaves * kWave), 0, stream, a, sp, p.splits);
+}
+template <int D>
+void launch_d(const KvAttentionArgs& a, const Plan& p, const Split& sp, hipStream_t stream) {
+    const bool two = a.c.log2_page == 5;
+    if (a.format == AWQ_KV_INT8) {
+        if (two) launch_np<D, AWQ_KV_INT8, 2>(a, p, sp, stream);
+        else launch_np<D, AWQ_KV_INT8, 1>(a, p, sp, stream);
+    } else {
+        if (two) launch_np<D, AWQ_KV_E4M3, 2>(a, p, sp, stream);
+        else launch_np<D, AWQ_KV_E4M3, 1>(a, p, sp, stream);
+    }
+}
+
+}  // namespace
+
+size_t kv_attention_workspace_bytes(int n_seqs, int kv_heads, int ratio, int head_dim, int64_t max_tokens,
+                                    int64_t max_len) {
+    return plan_bytes(plan_for(n_seqs, kv_heads, ratio, max_tokens, max_len, true), n_seqs, kv_heads, head_dim);
+}
+
+awq_status launch_kv_attention(const KvAttentionArgs& a, void* workspace, hipStream_t stream) {
+    const Plan p = plan_for(a.n_seqs, a.c.heads, a.ratio, a.max_tokens, a.c.max_len, workspace != nullptr);
+    if (p.row_tiles * p.splits >= (int64_t{1} << 31) || p.row_tiles * a.c.heads > (p.decode ? 65535 : INT64_MAX))
+        return AWQ_ERR_SHAPE;
+    Split sp;
+    sp.tokens = p.tokens;
+    sp.counters = static_cast<int*>(workspace);
+    sp.partials = workspace ? reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterBytes) : nullptr;
+    switch (a.head_dim) {
+        case 64: launch_d<64>(a, p, sp, stream); break;
+        case 96: launch_d<96>(a, p, sp, stream); break;
+        case 128: launch_d<128>(a, p, sp, stream); break;
+        case 192: launch_d<192>(a, p, sp, stream); break;
+        case 256: launch_d<256>(a, p, sp, stream); break;
+        default: return AWQ_ERR_CONFIG;
+    }
+    return last_launch_status();
+}
+
+}  // namespace awq
