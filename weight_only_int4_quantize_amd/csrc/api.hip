@@ -236,7 +236,7 @@ awq_status device_scratch(void** out, hipStream_t stream) {
 // column tile, is 2-3x slower than the GEMV there and 2-3x faster than the
 // GEMM tile everywhere); else the GEMM.
 int choose_path(int64_t M, int64_t N, int64_t K, int group_size, int path, bool have_workspace) {
-    const bool gemv_ok = gemv_supported(M, K);
+    const bool gemv_ok = gemv_supported(M, N, K);
     bool skinny_phased = false;
     const bool skinny_ok = skinny_supported(M, N, K, group_size, have_workspace, &skinny_phased);
     switch (path) {
@@ -713,7 +713,7 @@ awq_status awq_gemm_w8(const void* x_f16, const uint32_t* qweight, const void* s
     const half_t* sc = static_cast<const half_t*>(scales_f16);
     const half_t* zr = static_cast<const half_t*>(zeros_f16);
     half_t* y = static_cast<half_t*>(y_f16);
-    const bool gemv_ok = gemv_supported(M, K, 8);
+    const bool gemv_ok = gemv_supported(M, N, K, 8);
     if (path == 1 && !gemv_ok) return AWQ_ERR_CONFIG;
     // the MFMA form needs 32-bit byte offsets within a 256-row tile of x
     if (path == 2 && K * 256 * 2 >= (int64_t(1) << 31)) return AWQ_ERR_CONFIG;

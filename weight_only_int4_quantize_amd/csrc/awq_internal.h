@@ -58,7 +58,7 @@ awq_status launch_quantize(const half_t* w, const float* channel_scale, int64_t 
 // Decode GEMV y[M, N] = x[M, K] . dequant(Wq)^T for M <= kGemvMaxM.
 constexpr int kGemvMaxM = 8;
 // bits = 8: the W8A16 form (qweight [N, K/4], four byte codes per word).
-bool gemv_supported(int64_t M, int64_t K, int bits = 4);
+bool gemv_supported(int64_t M, int64_t N, int64_t K, int bits = 4);
 // Layers of few rows and long rows that the GEMV takes one-shot (every item
 // of a row in flight); the automatic choice prefers it there up to M = 4.
 bool gemv_few_rows(int64_t M, int64_t N, int64_t K, int bits = 4);

@@ -768,6 +768,12 @@ awq_status launch_t(const half_t* x, const GemvTarget<NL>& tg, int64_t N, int64_
     return last_launch_status();
 }
 
+// one row per wave of the streaming form (the reasons are in launch_m)
+bool gemv_one_row(int64_t M, int64_t N, int64_t kbs, int64_t waves) {
+    const bool fewer = ceil_div(N, waves) < 2 * ceil_div(ceil_div(N, 2), waves);
+    return M == 1 ? kbs <= 3 || fewer : M == 2 && fewer;
+}
+
 // Launch shape. Items are RPW rows x 2 chunks (64 packed words) per lane.
 //  * Rows of one item (4096 weights), or of two for W8: one row set per
 //    wavefront and all of it in flight from the start; 2 rows per wave share
@@ -824,8 +830,7 @@ awq_status launch_m(const half_t* x, const GemvTarget<NL>& tg, int64_t N, int64_
     // 8192 12.54 against 13.04, M = 1 2560 x 28672 (G = 64) 11.38 against
     // 12.43. At M >= 3 two rows always.
     const int64_t waves = blocks * 8;
-    const bool one_row = MT == 1 ? (kbs <= 3 || ceil_div(N, waves) < 2 * ceil_div(ceil_div(N, 2), waves))
-                                 : MT == 2 && ceil_div(N, waves) < 2 * ceil_div(ceil_div(N, 2), waves);
+    const bool one_row = gemv_one_row(MT, N, kbs, waves);
     // Staged (scale, zero) pairs (SZL): at M = 1 on rows of 5 items and
     // more, and at M = 2 with two rows per wave. Measured against per-chunk
     // pairs (us, as above): M = 2 4096 x 11008 9.37 -> 8.95, 8192 x 28672
@@ -849,10 +854,20 @@ awq_status launch_m(const half_t* x, const GemvTarget<NL>& tg, int64_t N, int64_
 
 }  // namespace
 
-bool gemv_supported(int64_t M, int64_t K, int bits) {
+bool gemv_supported(int64_t M, int64_t N, int64_t K, int bits) {
     if (M < 1 || M > kGemvMaxM) return false;
     if (K % (bits == 4 ? 32 : 16) != 0 || K > (int64_t(1) << 30)) return false;
-    return gemv_lds_bytes(M, K, bits) <= static_cast<size_t>(max_shared_bytes());
+    size_t lds = gemv_lds_bytes(M, K, bits);
+    // the streaming form (launch_m's rule) parks its rows' sums behind the
+    // staged x: 8 waves a block, one block per CU
+    const int64_t kbs = ceil_div(K >> (bits == 4 ? 5 : 4), 128);
+    const bool one_shot = kbs == 1 || (kbs == 2 && bits == 8) || gemv_few_rows(M, N, K, bits);
+    if (!one_shot) {
+        const int64_t waves = int64_t{8} * cu_count();
+        const int64_t rows = gemv_one_row(M, N, kbs, waves) ? ceil_div(N, waves) : 2 * ceil_div(ceil_div(N, 2), waves);
+        lds += static_cast<size_t>(8 * rows * M) * sizeof(float);
+    }
+    return lds <= static_cast<size_t>(max_shared_bytes());
 }
 
 namespace {
