@@ -522,6 +522,39 @@ awq_status awq_gemm_w8(const void* x_f16, const uint32_t* qweight,
                        size_t workspace_bytes, void* stream);
 
 /*
+ * awq_gemm_fused - the linear layer with what follows it in a decoder layer,
+ * in the same launch (rskf.cn §3.4 fuse_layers):
+ *   y = act(x . dequant(Wq)^T + bias) * mul + residual
+ * on the fp32 sums of awq_gemm (bits 4) or awq_gemm_w8 (bits 8), rounded to
+ * fp16 once. A gated MLP is the gate projection with AWQ_ACT_SILU and the
+ * up projection's output as mul; a block's last projection takes the
+ * residual stream.
+ *
+ *   bits            4 (qweight uint32 [N, K/8]) or 8 (uint32 [N, K/4])
+ *   bias_f16        device, fp16 [N] or NULL
+ *   activation      AWQ_ACT_NONE, _RELU, _SILU v / (1 + e^-v), _GELU
+ *                   v (1 + erf(v / sqrt 2)) / 2, or _GELU_TANH
+ *                   v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2
+ *   mul_f16, residual_f16   device, fp16 [M, N] or NULL, rows mul_stride and
+ *                   residual_stride halves apart (>= N; ignored with NULL)
+ *   y_f16           device, fp16 [M, N], packed (output). It may be
+ *                   residual_f16 or mul_f16 itself when their stride is N;
+ *                   otherwise it must not overlap any input.
+ *   path, workspace, the other arguments   as awq_gemm_ex (bits 4) or
+ *                   awq_gemm_w8 (bits 8)
+ * The kernel and the sums are those of the call without an epilogue.
+ */
+enum { AWQ_ACT_NONE = 0, AWQ_ACT_RELU = 1, AWQ_ACT_SILU = 2, AWQ_ACT_GELU = 3, AWQ_ACT_GELU_TANH = 4 };
+awq_status awq_gemm_fused(const void* x_f16, const uint32_t* qweight,
+                          const void* scales_f16, const void* zeros_f16,
+                          int64_t M, int64_t N, int64_t K, int group_size, int bits,
+                          const void* bias_f16, int activation,
+                          const void* mul_f16, int64_t mul_stride,
+                          const void* residual_f16, int64_t residual_stride,
+                          void* y_f16, int path, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/*
  * A paged 8-bit key / value cache, the second tensor a decode step streams
  * beside the weights: quantized as it is written, with the symmetric map of
  * aissn.com 对称/非对称量化 (zero-point 0) and one fp32 scale per page (a

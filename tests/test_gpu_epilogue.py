@@ -1,0 +1,261 @@
+"""awq_gemm_fused, y = act(v + bias) * mul + residual on the linear layer's
+sums v, on every kernel the layer runs.
+
+The kernel and the sums are those of the plain call, which gives y0 = fp16(v):
+|v - y0| <= 2^-11 |y0| + 2^-25 (half a step; half a subnormal step). Every
+activation's slope is below 1.13, its own arithmetic is within 2^-18 of its
+value plus 2^-22 (the hardware's exponential and reciprocal; GELU's erf), so
+against the formula in float64 on y0
+  |err| <= |mul| (1.13 (2^-11 |y0| + 2^-25) + 2^-18 |act| + 2^-22)
+           + 2^-22 (|act mul| + |residual|) + 2^-11 |y| + 2^-25,
+the last two the output's own rounding, the ones before it the fp32 product
+and sum. The whole is also held to the linear layer's bar against the oracle.
+"""
+
+import math
+
+import numpy as np
+import pytest
+
+import oracle
+import synth
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import weight_only_int4_quantize_amd as awq  # noqa: E402
+
+from test_gpu_parity import dev, host, say  # noqa: E402
+
+ACTS = list(awq.ACTIVATIONS)
+
+
+def act64(v, name):
+    v = np.asarray(v, np.float64)
+    if name == "relu":
+        return np.maximum(v, 0)
+    if name == "silu":
+        return v / (1 + np.exp(-v))
+    if name == "gelu":
+        return 0.5 * v * np.vectorize(math.erfc)(-v / math.sqrt(2))
+    if name == "gelu_tanh":
+        return 0.5 * v * (1 + np.tanh(math.sqrt(2 / math.pi) * (v + 0.044715 * v ** 3)))
+    return v
+
+
+def layer(M, N, K, G, bits, seed, w_std=0.02):
+    lay = synth.make_layer(N, K, M, seed=seed, w_std=w_std)
+    q = oracle.quantize(lay["w"], G) if bits == 4 else oracle.quantize_w8(lay["w"], G)
+    return lay["x"], q, (dev(lay["x"]), dev(q[0].view(np.int32)), dev(q[1]), dev(q[2]))
+
+
+def plain(t, G, bits, path, ws):
+    if bits == 8:
+        return awq.awq_gemm_w8(*t, G, path=path, workspace=ws)
+    return awq.awq_gemm(*t, G, path=path, workspace=ws)
+
+
+def check(y, y0, act, bias, mul, res, what):
+    y, y0 = y.astype(np.float64), y0.astype(np.float64)
+    with np.errstate(over="ignore"):
+        a = act64(y0 + (0 if bias is None else bias.astype(np.float64)), act)
+    m = 1.0 if mul is None else mul.astype(np.float64)
+    r = 0.0 if res is None else res.astype(np.float64)
+    want = a * m + r
+    tol = np.abs(m) * (1.13 * (2.0 ** -11 * np.abs(y0) + 2.0 ** -25) + 2.0 ** -18 * np.abs(a) + 2.0 ** -22) + \
+        2.0 ** -22 * (np.abs(a * m) + np.abs(r)) + 2.0 ** -11 * np.abs(want) + 2.0 ** -25
+    err = np.abs(y - want)
+    assert np.isfinite(y).all() and (err <= tol).all(), f"{what}: worst {np.max(err / tol):.3f} of the bound"
+
+
+SHAPES = [
+    # M, N, K, G, bits, path, workspace, the kernel that runs
+    (1, 4096, 4096, 128, 4, 0, False, 1),       # GEMV, one-shot, two rows a wave
+    (1, 1000, 4096, 64, 4, 0, False, 1),        # one row a wave
+    (1, 513, 8192, 128, 4, 0, False, 1),        # few rows, 8 waves
+    (4, 130, 16384, 128, 4, 1, False, 1),       # four items in flight, four rows of x
+    (1, 4099, 11008, 128, 4, 0, False, 1),      # streaming
+    (1, 2600, 28672, 128, 4, 0, False, 1),      # streaming, staged pairs
+    (2, 4096, 11008, 128, 4, 0, False, 1),      # streaming at two rows of x
+    (2, 4100, 4096, 128, 4, 0, False, 1),       # four rows a wave
+    (5, 4100, 4096, 512, 4, 1, False, 1),
+    (8, 300, 8192, 256, 4, 1, False, 1),        # streaming at eight
+    (3, 4096, 4096, 128, 4, 0, True, 4),        # column tiles
+    (16, 4096, 4096, 128, 4, 0, True, 4),
+    (16, 11008, 4096, 128, 4, 0, True, 4),      # several tiles a block
+    (7, 777, 2048, 256, 4, 0, True, 4),
+    (32, 1001, 4096, 32, 4, 0, True, 4),
+    (17, 8192, 8192, 64, 4, 4, False, 4),
+    (64, 4096, 4096, 128, 4, 0, True, 3),       # skinny, K splits
+    (33, 1003, 2048, 64, 4, 0, False, 3),       # no split
+    (12, 500, 11008, 128, 4, 3, False, 3),      # K in phases
+    (40, 700, 4096, 256, 4, 0, True, 3),
+    (200, 512, 4096, 128, 4, 0, True, 2),       # GEMM, stream-K
+    (300, 1000, 1024, 64, 4, 0, False, 2),
+    (129, 257, 512, 32, 4, 2, True, 2),         # the older form
+    (70, 257, 512, 32, 4, 2, False, 2),
+    (1, 1000, 4096, 128, 8, 0, False, 1),       # W8
+    (3, 4096, 11008, 64, 8, 0, False, 1),
+    (8, 513, 8192, 256, 8, 0, False, 1),
+    (100, 700, 2048, 128, 8, 0, True, 2),
+    (260, 390, 1024, 512, 8, 0, False, 2),
+]
+
+
+@pytest.mark.parametrize("M,N,K,G,bits,path,with_ws,kernel", SHAPES)
+def test_every_kernel(M, N, K, G, bits, path, with_ws, kernel):
+    say("fused", M, N, K, G, bits, path, with_ws)
+    if bits == 4:
+        assert awq.gemm_kernel(M, N, K, G, path, with_ws) == awq.KERNEL_NAMES[kernel]
+    x, q, t = layer(M, N, K, G, bits, [31, M, N, K])
+    ws = awq.gemm_workspace(M, N, K) if with_ws else None
+    rng = np.random.default_rng([32, M, N])
+    bias = (rng.standard_normal(N) * 0.5).astype(np.float16)
+    mul = rng.standard_normal((M, N)).astype(np.float16)
+    res = (rng.standard_normal((M, N)) * 2).astype(np.float16)
+    y0 = host(plain(t, G, bits, path, ws))
+    ref = oracle.linear_ref(x, *q, G) if bits == 4 else oracle.linear_ref_w8(x, *q, G)
+    small = M * N < 40000
+    for act in ACTS:
+        # every combination on the small shapes, a few on the others
+        for c in range(8) if small else ((7, 1, 6) if act == "silu" else (ACTS.index(act),)):
+            b, m, r = (v if c & (1 << i) else None for i, v in enumerate((bias, mul, res)))
+            y = awq.awq_gemm_fused(*t, G, bias=None if b is None else dev(b), activation=act,
+                                   mul=None if m is None else dev(m), residual=None if r is None else dev(r), path=path,
+                                   workspace=ws)
+            torch.cuda.synchronize()
+            check(host(y), y0, act, b, m, r, f"{act} {c}")
+            if c == 7:
+                want = act64(ref + b.astype(np.float64), act) * m + r
+                rel = np.linalg.norm(host(y).astype(np.float64) - want) / np.linalg.norm(want)
+                assert rel <= 1e-3, rel
+    if ws is not None:
+        assert not host(ws[:4096]).any()        # ready for the next call
+
+
+@pytest.mark.parametrize("M,N,K,G,path", [(1, 4096, 4096, 128, 0), (1, 4096, 11008, 128, 0), (16, 1000, 4096, 128, 0),
+                                          (40, 700, 4096, 128, 0), (200, 512, 4096, 128, 0), (150, 390, 512, 32, 0)])
+def test_in_place_and_strides(M, N, K, G, path):
+    """The residual stream updated in place, mul overwritten, operands as
+    slices of wider tensors; the same bits as out of place."""
+    x, q, t = layer(M, N, K, G, 4, [33, M, N])
+    ws = awq.gemm_workspace(M, N, K)
+    rng = np.random.default_rng([34, M])
+    mul, res = (dev(rng.standard_normal((M, N)).astype(np.float16)) for _ in range(2))
+    bias = dev(rng.standard_normal(N).astype(np.float16))
+    want = host(awq.awq_gemm_fused(*t, G, bias=bias, activation="silu", mul=mul, residual=res, path=path, workspace=ws))
+    for name in ("residual", "mul"):
+        a = {"mul": mul.clone(), "residual": res.clone()}
+        got = awq.awq_gemm_fused(*t, G, bias=bias, activation="silu", **a, path=path, workspace=ws, out=a[name])
+        np.testing.assert_array_equal(host(got), want)
+    wide = torch.full((M, 2 * N + 3), float("nan"), dtype=torch.float16, device="cuda")
+    wide[:, 1: N + 1], wide[:, N + 2: 2 * N + 2] = mul, res
+    got = awq.awq_gemm_fused(*t, G, bias=bias, activation="silu", mul=wide[:, 1: N + 1],
+                             residual=wide[:, N + 2: 2 * N + 2], path=path, workspace=ws)
+    np.testing.assert_array_equal(host(got), want)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        got = awq.awq_gemm_fused(*t, G, bias=bias, activation="silu", mul=mul, residual=res, path=path, workspace=ws)
+    torch.cuda.synchronize()
+    np.testing.assert_array_equal(host(got), want)
+
+
+@pytest.mark.parametrize("M,N,K,G,bits", [(1, 512, 1024, 128, 4), (20, 512, 1024, 128, 4), (130, 512, 1024, 128, 4),
+                                          (2, 512, 1024, 64, 8)])
+def test_nothing_to_fuse_is_the_plain_call(M, N, K, G, bits):
+    x, q, t = layer(M, N, K, G, bits, [35, M])
+    np.testing.assert_array_equal(host(awq.awq_gemm_fused(*t, G)), host(plain(t, G, bits, 0, None)))
+
+
+@pytest.mark.parametrize("M", [1, 9, 100])
+def test_activations_far_out(M):
+    """Sums of hundreds either way: the sigmoids saturate, nothing is NaN."""
+    x, q, t = layer(M, 300, 1024, 128, 4, [36, M], w_std=0.5)
+    big = dev((x.astype(np.float64) * 4).astype(np.float16))
+    t = (big,) + t[1:]
+    y0 = host(awq.awq_gemm(*t, 128))
+    assert np.abs(y0).max() > 100
+    for act in ACTS:
+        check(host(awq.awq_gemm_fused(*t, 128, activation=act, bias=dev(np.zeros(300, np.float16)))), y0, act, None,
+              None, None, act)
+
+
+def test_empty_and_graph():
+    x, q, t = layer(1, 512, 1024, 128, 4, [37])
+    assert awq.awq_gemm_fused(t[0][:0], *t[1:], activation="relu").shape == (0, 512)
+    bias = dev(np.ones(512, np.float16))
+    out = torch.zeros(1, 512, dtype=torch.float16, device="cuda")
+    ws = awq.gemm_workspace(1, 512, 1024)
+    xs = t[0].clone()
+    call = lambda o: awq.awq_gemm_fused(xs, *t[1:], bias=bias, activation="silu", residual=o, out=o, workspace=ws)  # noqa: E731
+    call(out)
+    torch.cuda.synchronize()
+    out.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(out)
+    out.zero_()
+    mine = torch.zeros_like(out)
+    for i in range(4):
+        xs.copy_(t[0] * (i + 1))
+        graph.replay()
+        torch.cuda.synchronize()
+        call(mine)
+        np.testing.assert_array_equal(host(out), host(mine))
+
+
+def test_decoder_layer_run():
+    """The operators together, as a decode step uses them: q/k/v with bias, the
+    cache write, attention, the output projection into the residual stream and
+    a gated MLP, against the same step from the parts' float64 formulas, each
+    on the operators' own inputs (so one part's rounding is not counted in the
+    next)."""
+    from oracle import kv_oracle
+    rng = np.random.default_rng(40)
+    B, heads, kv, D, hid = 3, 8, 2, 64, 512
+    mats = {}
+    for name, n, k in (("q", heads * D, hid), ("k", kv * D, hid), ("v", kv * D, hid), ("o", hid, heads * D),
+                       ("gate", 1024, hid), ("up", 1024, hid), ("down", hid, 1024)):
+        w = (rng.standard_normal((n, k)) * 0.05).astype(np.float16)
+        mats[name] = (w, *awq.awq_quantize(dev(w), 128))
+    ref = {n: oracle.dequantize(host(m[1]).view(np.uint32), host(m[2]), host(m[3]), 128, m[0].shape[1])
+           for n, m in mats.items()}
+    bias = {n: dev((rng.standard_normal(ref[n].shape[0]) * 0.1).astype(np.float16)) for n in "qkv"}
+    cache = awq.KVCache.empty(9, kv, D, 32, "int8")
+    kc, vc = np.zeros((9, kv, 32, D)), np.zeros((9, kv, 32, D))
+    ks, vs = np.zeros((9, kv), np.float32), np.zeros((9, kv), np.float32)
+    table = rng.permutation(9).astype(np.int32).reshape(3, 3)
+    lens = np.zeros(B, np.int32)
+    ws = awq.gemm_workspace(80, 1024, 1024)
+    fused = lambda x, n, **kw: awq.awq_gemm_fused(x, *mats[n][1:], 128, workspace=ws, **kw)  # noqa: E731
+
+    def near(got, want, x, name, mag=1.0):
+        got, want = host(got).astype(np.float64), np.asarray(want)
+        rel = np.linalg.norm(got - want) / np.linalg.norm(want)
+        assert rel <= 1e-3, (name, rel)
+
+    for new in ([30, 40, 10], [1, 1, 1], [1, 1, 1]):
+        lens += np.array(new, np.int32)
+        T = sum(new)
+        cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        seqs = awq.KVSeqs(dev(table), dev(cu), dev(lens.copy()), max(new), int(lens.max()))
+        h = dev(rng.standard_normal((T, hid)).astype(np.float16))
+        h0 = host(h).astype(np.float64)
+        q, k, v = (fused(h, n, bias=bias[n]) for n in "qkv")
+        for n, t in (("q", q), ("k", k), ("v", v)):
+            near(t, h0 @ ref[n].T + host(bias[n]).astype(np.float64), h, n)
+        awq.awq_kv_write(cache, seqs, k.view(T, kv, D), v.view(T, kv, D))
+        kv_oracle.write(kc, ks, host(k).reshape(T, kv, D), table, cu, lens, "int8")
+        kv_oracle.write(vc, vs, host(v).reshape(T, kv, D), table, cu, lens, "int8")
+        aw = awq.kv_attention_workspace(cache, seqs, heads)
+        a = awq.awq_kv_attention(q.view(T, heads, D), cache, seqs, workspace=aw)
+        near(a, kv_oracle.attention(host(q).reshape(T, heads, D), kc, ks, vc, vs, table, cu, lens, D ** -0.5)[0], q, "a")
+        fused(a.view(T, heads * D), "o", residual=h, out=h)
+        near(h, h0 + host(a).reshape(T, -1).astype(np.float64) @ ref["o"].T, a, "o")
+        h1 = host(h).astype(np.float64)
+        up = fused(h, "up")
+        mid = fused(h, "gate", activation="silu", mul=up)
+        near(mid, act64(h1 @ ref["gate"].T, "silu") * host(up).astype(np.float64), h, "gate")
+        fused(mid, "down", residual=h, out=h)
+        near(h, h1 + host(mid).astype(np.float64) @ ref["down"].T, mid, "down")

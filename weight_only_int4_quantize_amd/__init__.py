@@ -11,6 +11,8 @@ Entry points (same names as the C ABI in include/awq.h):
         (awq_gemm_ex when a workspace from gemm_workspace(M, N, K) is given)
     awq_activation_absmean(x) -> m
     awq_scale_search(w, x, group_size=128, alphas=None) -> losses, best_index, best_scales
+    awq_gemm_fused(x, qweight, scales, zeros, group_size=128, bias=None, activation="none", mul=None,
+        residual=None) -> y
     awq_kv_write(cache, seqs, k, v), awq_kv_read(cache, seqs) -> k, v
     awq_kv_attention(q, cache, seqs) -> out
         (a paged 8-bit cache, KVCache, and a batch of sequences over it, KVSeqs)
@@ -34,6 +36,7 @@ STATUS_NAMES = {
 PATH_AUTO, PATH_GEMV, PATH_GEMM, PATH_SKINNY, PATH_COLTILE = 0, 1, 2, 3, 4
 QUANT_ASYMMETRIC, QUANT_SYMMETRIC = 0, 1
 
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 KV_FORMATS = {"int8": 0, "e4m3": 1}
 
 _lib = None
@@ -125,6 +128,9 @@ def load() -> ctypes.CDLL:
     L.awq_quantize_w8.argtypes = [c_vp, c_vp, c_i64, c_i64, c_int, c_int, c_vp, c_vp, c_vp, c_vp]
     L.awq_gemm_w8.restype = c_int
     L.awq_gemm_w8.argtypes = [c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_int, c_vp, c_int, c_vp, c_sz, c_vp]
+    L.awq_gemm_fused.restype = c_int
+    L.awq_gemm_fused.argtypes = [c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_int, c_int, c_vp, c_int, c_vp, c_i64,
+                                 c_vp, c_i64, c_vp, c_int, c_vp, c_sz, c_vp]
     L.awq_kv_write.restype = c_int
     L.awq_kv_write.argtypes = [c_vp, c_vp, c_vp, c_i64, c_i64, c_vp, c_i64, c_i64, c_i64, c_vp]
     L.awq_kv_read.restype = c_int
@@ -570,6 +576,77 @@ def awq_gemm_w8(x, qweight, scales, zeros, group_size: int = 128, path: int = PA
                             _ptr(workspace), nbytes, _stream(x.device))
     _check("awq_gemm_w8", st)
     return y
+
+
+# ---------------------------------------------------------------- the linear layer with its epilogue
+
+def _need_rows(name: str, t, M: int, N: int, device) -> int:
+    """fp16 [M, N] with contiguous rows on `device`; returns its row stride."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.float16:
+        raise TypeError(f"{name} must be torch.float16, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if tuple(t.shape) != (M, N):
+        raise ValueError(f"{name} must be [{M}, {N}], got {list(t.shape)}")
+    if N > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    return t.stride(0) if M > 1 else N
+
+
+def awq_gemm_fused(x, qweight, scales, zeros, group_size: int = 128, bias=None, activation: str = "none", mul=None,
+                   residual=None, path: int = PATH_AUTO, out=None, workspace=None):
+    """awq_gemm_fused: y = act(x . dequant(Wq)^T + bias) * mul + residual in
+    one launch, INT4 or W8 weights by qweight's width (K / 8 or K / 4 words).
+
+    bias fp16 [N]; mul and residual fp16 [M, N], rows any stride apart;
+    activation one of ACTIVATIONS. out may be residual or mul itself (when
+    packed). workspace: gemm_workspace(M, N, K)."""
+    torch = _torch()
+    _need_gpu("x", x, torch.float16)
+    _need_gpu("qweight", qweight, torch.int32)
+    _need_gpu("scales", scales, torch.float16)
+    _need_gpu("zeros", zeros, torch.float16)
+    if x.dim() != 2 or qweight.dim() != 2:
+        raise ValueError("x and qweight must be 2-D")
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
+    M, K = x.shape
+    N, words = qweight.shape
+    bits = 4 if words * 8 == K else 8
+    if words * 32 != K * bits:
+        raise ValueError(f"qweight has {words} words per row, K={K} needs {K // 8} (INT4) or {K // 4} (W8)")
+    if scales.shape != (N, K // group_size) or zeros.shape != scales.shape:
+        raise ValueError("scales/zeros must be [N, K/group_size]")
+    dev = x.device
+    if not (qweight.device == scales.device == zeros.device == dev):
+        raise ValueError(f"the layer's tensors must be on {dev}")
+    if bias is not None:
+        _need_gpu("bias", bias, torch.float16)
+        if tuple(bias.shape) != (N,) or bias.device != dev:
+            raise ValueError(f"bias must be [{N}] on {dev}")
+    mul_stride = _need_rows("mul", mul, M, N, dev) if mul is not None else 0
+    residual_stride = _need_rows("residual", residual, M, N, dev) if residual is not None else 0
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.float16, device=dev)
+    else:
+        _need_gpu("out", out, torch.float16)
+        if tuple(out.shape) != (M, N) or out.device != dev:
+            raise ValueError(f"out must be [{M}, {N}] on {dev}")
+    nbytes = 0
+    if workspace is not None:
+        _need_gpu("workspace", workspace, torch.uint8)
+        if workspace.device != dev:
+            raise ValueError(f"workspace must be on {dev}")
+        nbytes = workspace.numel()
+    st = _on_device(dev, load().awq_gemm_fused, x.data_ptr(), qweight.data_ptr(), scales.data_ptr(), zeros.data_ptr(),
+                    M, N, K, group_size, bits, _ptr(bias), ACTIVATIONS[activation], _ptr(mul), mul_stride,
+                    _ptr(residual), residual_stride, out.data_ptr(), path, _ptr(workspace), nbytes)
+    if st != AWQ_OK:
+        _check("awq_gemm_fused", st)
+    return out
 
 
 # ---------------------------------------------------------------- the paged 8-bit key / value cache

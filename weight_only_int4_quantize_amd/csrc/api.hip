@@ -263,7 +263,8 @@ int choose_path(int64_t M, int64_t N, int64_t K, int group_size, int path, bool 
 // unsplit.
 awq_status gemm_dispatch(const void* x_f16, const uint32_t* qweight, const void* scales_f16, const void* zeros_f16,
                          int64_t M, int64_t N, int64_t K, int group_size, void* y_f16, int path, void* workspace,
-                         size_t workspace_bytes, bool split_gemm, bool library_scratch, hipStream_t stream) {
+                         size_t workspace_bytes, bool split_gemm, bool library_scratch, hipStream_t stream,
+                         const Epilogue* epilogue = nullptr) {
     awq_status st = check_dims(N, K, group_size);
     if (st != AWQ_OK) return st;
     if (path < 0 || path > 4) return AWQ_ERR_CONFIG;
@@ -282,8 +283,8 @@ awq_status gemm_dispatch(const void* x_f16, const uint32_t* qweight, const void*
     const int chosen = choose_path(M, N, K, group_size, path, workspace != nullptr || library_scratch);
     if (chosen < 0) return AWQ_ERR_CONFIG;
     const bool use_skinny = chosen == 3;
-    if (chosen == 4) return launch_coltile(x, qweight, sc, zr, M, N, K, group_size, y, stream);
-    if (chosen == 1) return launch_gemv(x, qweight, sc, zr, M, N, K, group_size, y, stream);
+    if (chosen == 4) return launch_coltile(x, qweight, sc, zr, M, N, K, group_size, y, stream, epilogue);
+    if (chosen == 1) return launch_gemv(x, qweight, sc, zr, M, N, K, group_size, y, stream, 4, epilogue);
     if (!use_skinny && !split_gemm) workspace = nullptr;
     if (use_skinny && library_scratch) {
         if (skinny_workspace_bytes(M, N, K) > kNoAllocScratchBytes) return AWQ_ERR_WORKSPACE;
@@ -295,8 +296,8 @@ awq_status gemm_dispatch(const void* x_f16, const uint32_t* qweight, const void*
         const size_t need = use_skinny ? skinny_workspace_bytes(M, N, K) : gemm_workspace_bytes(M, N);
         if (workspace_bytes < need) return AWQ_ERR_WORKSPACE;
     }
-    if (use_skinny) return launch_skinny(x, qweight, sc, zr, M, N, K, group_size, y, workspace, stream);
-    GemmArgs a;
+    if (use_skinny) return launch_skinny(x, qweight, sc, zr, M, N, K, group_size, y, workspace, stream, epilogue);
+    GemmFusedArgs a;
     a.a = x;
     a.qweight = qweight;
     a.scales = sc;
@@ -306,7 +307,58 @@ awq_status gemm_dispatch(const void* x_f16, const uint32_t* qweight, const void*
     a.N = N;
     a.K = K;
     a.y16 = y;
+    if (epilogue) {
+        a.epilogue = *epilogue;
+        return launch_gemm_fused(a, GemmB::kInt4, stream, workspace);
+    }
     return launch_gemm(a, GemmB::kInt4, GemmOut::kF16, stream, workspace);
+}
+
+// The W8 linear layer behind awq_gemm_w8 and awq_gemm_fused.
+awq_status w8_dispatch(const void* x_f16, const uint32_t* qweight, const void* scales_f16, const void* zeros_f16,
+                       int64_t M, int64_t N, int64_t K, int group_size, void* y_f16, int path, void* workspace,
+                       size_t workspace_bytes, hipStream_t stream, const Epilogue* epilogue) {
+    awq_status st = check_dims(N, K, group_size);
+    if (st != AWQ_OK) return st;
+    if (group_size < 64) return AWQ_ERR_CONFIG;
+    if (path < 0 || path > 2) return AWQ_ERR_CONFIG;
+    if (M < 0 || M > kMaxDim) return AWQ_ERR_SHAPE;
+    if (M > (int64_t(1) << 31) - 256 || N > (int64_t(1) << 31) - 256) return AWQ_ERR_SHAPE;
+    if (M == 0 || N == 0) return AWQ_OK;
+    if (!x_f16 || !qweight || !scales_f16 || !zeros_f16 || !y_f16) return AWQ_ERR_NULL;
+    if (!aligned16(x_f16) || !aligned16(qweight) || (reinterpret_cast<uintptr_t>(scales_f16) & 1) ||
+        (reinterpret_cast<uintptr_t>(zeros_f16) & 1) || (reinterpret_cast<uintptr_t>(y_f16) & 1))
+        return AWQ_ERR_ALIGN;
+    const half_t* x = static_cast<const half_t*>(x_f16);
+    const half_t* sc = static_cast<const half_t*>(scales_f16);
+    const half_t* zr = static_cast<const half_t*>(zeros_f16);
+    half_t* y = static_cast<half_t*>(y_f16);
+    const bool gemv_ok = gemv_supported(M, N, K, 8);
+    if (path == 1 && !gemv_ok) return AWQ_ERR_CONFIG;
+    // the MFMA form needs 32-bit byte offsets within a 256-row tile of x
+    if (path == 2 && K * 256 * 2 >= (int64_t(1) << 31)) return AWQ_ERR_CONFIG;
+    if (path == 1 || (path == 0 && gemv_ok))
+        return launch_gemv(x, qweight, sc, zr, M, N, K, group_size, y, stream, 8, epilogue);
+    if (K * 256 * 2 >= (int64_t(1) << 31)) return AWQ_ERR_SHAPE;
+    if (workspace != nullptr) {
+        if (reinterpret_cast<uintptr_t>(workspace) & 255) return AWQ_ERR_ALIGN;
+        if (workspace_bytes < gemm_workspace_bytes(M, N)) return AWQ_ERR_WORKSPACE;
+    }
+    GemmFusedArgs a;
+    a.a = x;
+    a.qweight = qweight;
+    a.scales = sc;
+    a.zeros = zr;
+    a.group_size = group_size;
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.y16 = y;
+    if (epilogue) {
+        a.epilogue = *epilogue;
+        return launch_gemm_fused(a, GemmB::kInt8, stream, workspace);
+    }
+    return launch_gemm(a, GemmB::kInt8, GemmOut::kF16, stream, workspace);
 }
 
 }  // namespace
@@ -698,43 +750,38 @@ awq_status awq_quantize_w8(const void* w_f16, const float* channel_scale, int64_
 awq_status awq_gemm_w8(const void* x_f16, const uint32_t* qweight, const void* scales_f16, const void* zeros_f16,
                        int64_t M, int64_t N, int64_t K, int group_size, void* y_f16, int path, void* workspace,
                        size_t workspace_bytes, void* stream) {
-    awq_status st = check_dims(N, K, group_size);
-    if (st != AWQ_OK) return st;
-    if (group_size < 64) return AWQ_ERR_CONFIG;
-    if (path < 0 || path > 2) return AWQ_ERR_CONFIG;
-    if (M < 0 || M > kMaxDim) return AWQ_ERR_SHAPE;
-    if (M > (int64_t(1) << 31) - 256 || N > (int64_t(1) << 31) - 256) return AWQ_ERR_SHAPE;
-    if (M == 0 || N == 0) return AWQ_OK;
-    if (!x_f16 || !qweight || !scales_f16 || !zeros_f16 || !y_f16) return AWQ_ERR_NULL;
-    if (!aligned16(x_f16) || !aligned16(qweight) || (reinterpret_cast<uintptr_t>(scales_f16) & 1) ||
-        (reinterpret_cast<uintptr_t>(zeros_f16) & 1) || (reinterpret_cast<uintptr_t>(y_f16) & 1))
+    return w8_dispatch(x_f16, qweight, scales_f16, zeros_f16, M, N, K, group_size, y_f16, path, workspace,
+                       workspace_bytes, as_stream(stream), nullptr);
+}
+
+awq_status awq_gemm_fused(const void* x_f16, const uint32_t* qweight, const void* scales_f16, const void* zeros_f16,
+                          int64_t M, int64_t N, int64_t K, int group_size, int bits, const void* bias_f16,
+                          int activation, const void* mul_f16, int64_t mul_stride, const void* residual_f16,
+                          int64_t residual_stride, void* y_f16, int path, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+    if (bits != 4 && bits != 8) return AWQ_ERR_CONFIG;
+    if (activation < AWQ_ACT_NONE || activation > AWQ_ACT_GELU_TANH) return AWQ_ERR_CONFIG;
+    if ((mul_f16 && (mul_stride < N || mul_stride > kMaxDim)) ||
+        (residual_f16 && (residual_stride < N || residual_stride > kMaxDim)))
+        return AWQ_ERR_SHAPE;
+    if ((reinterpret_cast<uintptr_t>(bias_f16) & 1) || (reinterpret_cast<uintptr_t>(mul_f16) & 1) ||
+        (reinterpret_cast<uintptr_t>(residual_f16) & 1))
         return AWQ_ERR_ALIGN;
-    const half_t* x = static_cast<const half_t*>(x_f16);
-    const half_t* sc = static_cast<const half_t*>(scales_f16);
-    const half_t* zr = static_cast<const half_t*>(zeros_f16);
-    half_t* y = static_cast<half_t*>(y_f16);
-    const bool gemv_ok = gemv_supported(M, N, K, 8);
-    if (path == 1 && !gemv_ok) return AWQ_ERR_CONFIG;
-    // the MFMA form needs 32-bit byte offsets within a 256-row tile of x
-    if (path == 2 && K * 256 * 2 >= (int64_t(1) << 31)) return AWQ_ERR_CONFIG;
-    if (path == 1 || (path == 0 && gemv_ok))
-        return launch_gemv(x, qweight, sc, zr, M, N, K, group_size, y, as_stream(stream), 8);
-    if (K * 256 * 2 >= (int64_t(1) << 31)) return AWQ_ERR_SHAPE;
-    if (workspace != nullptr) {
-        if (reinterpret_cast<uintptr_t>(workspace) & 255) return AWQ_ERR_ALIGN;
-        if (workspace_bytes < gemm_workspace_bytes(M, N)) return AWQ_ERR_WORKSPACE;
-    }
-    GemmArgs a;
-    a.a = x;
-    a.qweight = qweight;
-    a.scales = sc;
-    a.zeros = zr;
-    a.group_size = group_size;
-    a.M = M;
-    a.N = N;
-    a.K = K;
-    a.y16 = y;
-    return launch_gemm(a, GemmB::kInt8, GemmOut::kF16, as_stream(stream), workspace);
+    Epilogue e;
+    e.bias = static_cast<const half_t*>(bias_f16);
+    e.mul = static_cast<const half_t*>(mul_f16);
+    e.residual = static_cast<const half_t*>(residual_f16);
+    e.mul_stride = mul_stride;
+    e.residual_stride = residual_stride;
+    e.act = activation;
+    // nothing to fuse: the plain kernels
+    const bool plain = !bias_f16 && !mul_f16 && !residual_f16 && activation == AWQ_ACT_NONE;
+    const Epilogue* epilogue = plain ? nullptr : &e;
+    if (bits == 8)
+        return w8_dispatch(x_f16, qweight, scales_f16, zeros_f16, M, N, K, group_size, y_f16, path, workspace,
+                           workspace_bytes, as_stream(stream), epilogue);
+    return gemm_dispatch(x_f16, qweight, scales_f16, zeros_f16, M, N, K, group_size, y_f16, path, workspace,
+                         workspace_bytes, true, false, as_stream(stream), epilogue);
 }
 
 }  // extern "C"

@@ -42,7 +42,19 @@ inline int cu_count() {
 }
 inline awq_status last_launch_status() { return hip_status(hipGetLastError()); }
 
+// The linear layer's epilogue y = act(v + bias) * mul + residual
+// (awq_gemm_fused): fp16 operands, nullptr where there is none. mul and
+// residual have row strides in halves.
+struct Epilogue {
+    const half_t* bias = nullptr;
+    const half_t* mul = nullptr;
+    const half_t* residual = nullptr;
+    int64_t mul_stride = 0, residual_stride = 0;
+    int act = AWQ_ACT_NONE;
+};
+
 // ---- launchers (each returns after enqueueing on `stream`) ----
+// The linear kernels' launchers take an epilogue, or nullptr for none.
 
 // Group-wise INT4 quantization of W[N, K] (optionally times channel_scale[K]),
 // asymmetric (the group's [min, max]) or symmetric (max |w| -> +-7, zero 8),
@@ -64,7 +76,7 @@ bool gemv_supported(int64_t M, int64_t N, int64_t K, int bits = 4);
 bool gemv_few_rows(int64_t M, int64_t N, int64_t K, int bits = 4);
 awq_status launch_gemv(const half_t* x, const uint32_t* qweight, const half_t* scales,
                        const half_t* zeros, int64_t M, int64_t N, int64_t K, int group_size,
-                       half_t* y, hipStream_t stream, int bits = 4);
+                       half_t* y, hipStream_t stream, int bits = 4, const Epilogue* epilogue = nullptr);
 // Several INT4 layers that share x (and K, G) in one GEMV launch: their rows
 // stacked in order, layer i < n owning rows [row0[i], row0[i + 1]), each row
 // read from and written to its own layer's tensors; row0[n] is the total and
@@ -84,7 +96,7 @@ awq_status launch_gemv_grouped(const half_t* x, const GemvLayers& layers, int64_
 
 // MFMA GEMM. The B operand is INT4 or W8 (qweight/scales/zeros) or fp16 W[N, K].
 enum class GemmB { kInt4, kF16, kInt8 };
-enum class GemmOut { kF16, kF32, kLoss };
+enum class GemmOut { kF16, kF32, kLoss, kFused };    // kFused: fp16 behind the epilogue
 // The searches' fp32 reference output (kF32 results, kLoss references) is
 // kept in the accumulator order of v_mfma_f32_32x32x16: 256 x 128 tiles
 // (row-major over ceil(N / 128) tile columns), each of 32 sub-tiles of
@@ -129,6 +141,10 @@ struct GemmArgs {
     // of launch_tile_fp16_b.
     bool b_tiled = false;
 };
+// kFused: the same with the epilogue
+struct GemmFusedArgs : GemmArgs {
+    Epilogue epilogue;
+};
 // fp16 W[N, K] (K a multiple of 64) into the fp16-B reference's tiled order:
 // 16-byte piece (lane, v) of 32-row group g and 64-k step t, at piece index
 // ((g * K / 64 + t) * 4 + v) * 64 + lane, holds W[32 g + lane % 32]
@@ -161,6 +177,8 @@ int64_t gemm_tile_count(int64_t M, int64_t N);
 size_t gemm_workspace_bytes(int64_t M, int64_t N);
 awq_status launch_gemm(const GemmArgs& args, GemmB b, GemmOut out, hipStream_t stream,
                        void* workspace = nullptr);
+// quantized B, fp16 output behind the epilogue
+awq_status launch_gemm_fused(const GemmFusedArgs& args, GemmB b, hipStream_t stream, void* workspace);
 
 // Skinny MFMA GEMM for 4 < M <= 64 (decode batches): 16x16x32 MFMAs whose B
 // operand is one packed word per lane, K optionally split across blocks
@@ -174,7 +192,7 @@ bool skinny_supported(int64_t M, int64_t N, int64_t K, int group_size, bool have
 size_t skinny_workspace_bytes(int64_t M, int64_t N, int64_t K);
 awq_status launch_skinny(const half_t* x, const uint32_t* qweight, const half_t* scales,
                          const half_t* zeros, int64_t M, int64_t N, int64_t K, int group_size,
-                         half_t* y, void* workspace, hipStream_t stream);
+                         half_t* y, void* workspace, hipStream_t stream, const Epilogue* epilogue = nullptr);
 
 // Column-tile MFMA kernel for small batches (M <= kColTileMaxM): one block
 // per 16 output columns over all of K, x read straight into the MFMA A
@@ -186,7 +204,7 @@ bool coltile_supported(int64_t M, int64_t N, int64_t K, int group_size);
 bool coltile_preferred(int64_t M, int64_t N, int64_t K, int group_size, bool have_workspace);
 awq_status launch_coltile(const half_t* x, const uint32_t* qweight, const half_t* scales,
                           const half_t* zeros, int64_t M, int64_t N, int64_t K, int group_size,
-                          half_t* y, hipStream_t stream);
+                          half_t* y, hipStream_t stream, const Epilogue* epilogue = nullptr);
 // The layers of `layers` (as for launch_gemv_grouped), sharing x, in one
 // column-tile launch: each layer on whole blocks of its own columns, the
 // tile and wave counts those of their total rows.

@@ -35,7 +35,7 @@
 // fp16 (q - z) in the order (0,4,1,5,2,6,3,7), and x is permuted to match.
 #include <algorithm>
 
-#include "awq_internal.h"
+#include "epilogue.h"
 
 namespace awq {
 namespace {
@@ -106,10 +106,14 @@ struct CtSlot {
 // rounded up MFMA row blocks; XP 16-byte x pieces per lane and group; CT
 // 16-column MFMA tiles per block, which share every x operand read.
 // The block's work: block `blk` of the layer (qweight, scales, zeros, y, N).
-template <int XR, int WPL, int NW, int DEPTH, int CT>
+// EPI: the epilogue, its operands loaded by the threads that store, behind
+// the ring's first loads when a thread stores at most two outputs, else ahead
+// of the waves' sums.
+template <int XR, int WPL, int NW, int DEPTH, int CT, class EPI = NoEpilogue>
 __device__ __forceinline__ void coltile_body(const half_t* __restrict__ x, const uint32_t* __restrict__ qweight,
                                              const half_t* __restrict__ scales, const half_t* __restrict__ zeros,
-                                             half_t* __restrict__ y, int M, int N, int K, int blk) {
+                                             half_t* y, int M, int N, int K, int blk, const EPI& epi = EPI{}) {
+    constexpr bool kEpi = std::is_same_v<EPI, Epilogue>;
     constexpr int G = WPL * 32;
     constexpr int MB = (XR + 15) / 16;
     constexpr int COLS = kCtCols * CT;
@@ -203,6 +207,23 @@ __device__ __forceinline__ void coltile_body(const half_t* __restrict__ x, const
         load(ring[d], g0 + d);
         __builtin_amdgcn_sched_barrier(0);
     }
+    constexpr int kOuts = (CT * MB * 256 + NW * 64 - 1) / (NW * 64);     // outputs a thread stores
+    [[maybe_unused]] EpilogueBits eb[kEpi ? kOuts : 1] = {};
+    [[maybe_unused]] auto load_epilogue = [&] {
+        if constexpr (kEpi) {
+#pragma unroll
+            for (int k = 0; k < kOuts; ++k) {
+                const int i = tid + k * NW * 64;
+                const int t = i / (MB * 256), r = i - t * (MB * 256);
+                const int row = 16 * (r >> 8) + 4 * ((r >> 2) >> 4 & 3) + (r & 3);
+                const int n = n0 + kCtCols * t + ((r >> 2) & 15);
+                if (i < CT * MB * 256 && row < M && n < N) eb[k] = epilogue_load(epi, row, n);
+            }
+        }
+    };
+    // (instances held to 128 VGPRs with full slots have none to spare)
+    constexpr bool kEarly = kOuts <= 2 && !(CT == 1 && XR * WPL == 64);
+    if constexpr (kEpi && kEarly) load_epilogue();
 #pragma unroll
     for (int i = 0; i < kCtSZ; ++i) {
         const int e = tid + i * NW * 64;
@@ -292,6 +313,7 @@ __device__ __forceinline__ void coltile_body(const half_t* __restrict__ x, const
     // ---- the waves' sums, added in wave order: lane l holds rows
     //      16 mb + 4 (l / 16) + e of column 16 t + l % 16 (over the x
     //      buffers, which every wave is done with after the barrier) ----
+    if constexpr (kEpi && !kEarly) load_epilogue();
     __syncthreads();
     float4_t* red = reinterpret_cast<float4_t*>(lds + ct_x_offset(ng, CT));
 #pragma unroll
@@ -299,6 +321,21 @@ __device__ __forceinline__ void coltile_body(const half_t* __restrict__ x, const
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) red[((wave * CT + t) * MB + mb) * 64 + lane] = acc[t][mb];
     __syncthreads();
+    if constexpr (kEpi) {
+#pragma unroll
+        for (int k = 0; k < kOuts; ++k) {
+            const int i = tid + k * NW * 64;
+            if (i >= CT * MB * 256) break;
+            const int t = i / (MB * 256), r = i - t * (MB * 256);
+            const int mb = r >> 8, l = (r >> 2) & 63, e = r & 3;
+            float sum = 0.f;
+            for (int w = 0; w < NW; ++w) sum += red[((w * CT + t) * MB + mb) * 64 + l][e];
+            const int row = 16 * mb + 4 * (l >> 4) + e;
+            const int n = n0 + kCtCols * t + (l & 15);
+            if (row < M && n < N) y[static_cast<int64_t>(row) * N + n] = epilogue_apply(epi, sum, eb[k]);
+        }
+        return;
+    }
     for (int i = tid; i < CT * MB * 256; i += NW * 64) {
         const int t = i / (MB * 256), r = i - t * (MB * 256);
         const int mb = r >> 8, l = (r >> 2) & 63, e = r & 3;
@@ -315,6 +352,14 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(ct_wave
     const half_t* __restrict__ x, const uint32_t* __restrict__ qweight, const half_t* __restrict__ scales,
     const half_t* __restrict__ zeros, half_t* __restrict__ y, int M, int N, int K) {
     coltile_body<XR, WPL, NW, DEPTH, CT>(x, qweight, scales, zeros, y, M, N, K, blockIdx.x);
+}
+
+// The same with the epilogue.
+template <int XR, int WPL, int NW, int DEPTH, int CT>
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(ct_waves_per_eu(XR, WPL, CT, NW)))) void coltile_fused_kernel(
+    const half_t* __restrict__ x, const uint32_t* __restrict__ qweight, const half_t* __restrict__ scales,
+    const half_t* __restrict__ zeros, half_t* y, int M, int N, int K, Epilogue epi) {
+    coltile_body<XR, WPL, NW, DEPTH, CT, Epilogue>(x, qweight, scales, zeros, y, M, N, K, blockIdx.x, epi);
 }
 
 // Several layers that share x in one launch: layer i owns the blocks
@@ -493,6 +538,7 @@ struct CtTarget {
     const half_t* zeros;
     half_t* y;
     const GemvLayers* layers;
+    const Epilogue* epilogue;       // one layer only
 };
 
 template <typename Kernel>
@@ -508,6 +554,17 @@ awq_status launch_ct(const half_t* x, const CtTarget& tg, int M, int N, int K, h
     constexpr int DEPTH = ct_depth(XR, WPL, CT);
     constexpr int COLS = kCtCols * CT;
     const size_t lds = ct_lds_bytes(K, WPL * 32, XR, NW, CT);
+    if (tg.epilogue != nullptr) {
+        static bool attr_set = false;
+        if (!attr_set) {
+            const awq_status st = ct_allow_lds(&coltile_fused_kernel<XR, WPL, NW, DEPTH, CT>);
+            if (st != AWQ_OK) return st;
+            attr_set = true;
+        }
+        hipLaunchKernelGGL((coltile_fused_kernel<XR, WPL, NW, DEPTH, CT>), dim3(static_cast<unsigned>(ceil_div(N, COLS))),
+                           dim3(NW * 64), lds, stream, x, tg.qweight, tg.scales, tg.zeros, tg.y, M, N, K, *tg.epilogue);
+        return last_launch_status();
+    }
     if (tg.layers == nullptr) {
         static bool attr_set = false;
         if (!attr_set) {
@@ -685,10 +742,11 @@ bool coltile_grouped_supported(int64_t M, const GemvLayers& layers, int64_t K, i
 }
 
 awq_status launch_coltile(const half_t* x, const uint32_t* qweight, const half_t* scales, const half_t* zeros,
-                          int64_t M, int64_t N, int64_t K, int group_size, half_t* y, hipStream_t stream) {
+                          int64_t M, int64_t N, int64_t K, int group_size, half_t* y, hipStream_t stream,
+                          const Epilogue* epilogue) {
     if (M == 0 || N == 0) return AWQ_OK;
     if (!coltile_supported(M, N, K, group_size)) return AWQ_ERR_CONFIG;
-    const CtTarget tg{qweight, scales, zeros, y, nullptr};
+    const CtTarget tg{qweight, scales, zeros, y, nullptr, epilogue};
     return launch_ct_g(x, tg, static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), group_size, stream);
 }
 
@@ -697,7 +755,7 @@ awq_status launch_coltile_grouped(const half_t* x, const GemvLayers& layers, int
     const int64_t total = layers.row0[layers.n];
     if (M == 0 || total == 0) return AWQ_OK;
     if (!coltile_grouped_supported(M, layers, K, group_size)) return AWQ_ERR_CONFIG;
-    const CtTarget tg{nullptr, nullptr, nullptr, nullptr, &layers};
+    const CtTarget tg{nullptr, nullptr, nullptr, nullptr, &layers, nullptr};
     return launch_ct_g(x, tg, static_cast<int>(M), static_cast<int>(total), static_cast<int>(K), group_size, stream);
 }
 

@@ -45,7 +45,9 @@
 // [l mod 32].
 #include <algorithm>
 
-#include "awq_internal.h"
+#include <type_traits>
+
+#include "epilogue.h"
 
 namespace awq {
 namespace {
@@ -234,9 +236,11 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t partial_rsrc(float* p, int byt
 // the tiled order of GemmArgs::b_tiled, so each wave's load of a K step is
 // one contiguous 1 KB piece per 16 bytes a lane takes (8 cache lines against
 // 32 for row-major B).
+template <GemmOut OMODE>
+using ArgsOf = std::conditional_t<OMODE == GemmOut::kFused, GemmFusedArgs, GemmArgs>;
 template <int BM, int BN, GemmB BMODE, GemmOut OMODE, bool STREAMK, bool DIRECT, int WGM = 2, int NT = kThreads,
           bool SKDMA = false, bool TILEDB = false>
-__global__ __launch_bounds__(NT, 512 / NT) void gemm_kernel(GemmArgs args, int tiles_n, StreamK sk) {
+__global__ __launch_bounds__(NT, 512 / NT) void gemm_kernel(ArgsOf<OMODE> args, int tiles_n, StreamK sk) {
     constexpr int WGN = NT / kWave / WGM;
     constexpr int WTM = BM / WGM;               // wave tile rows
     constexpr int WTN = BN / WGN;               // wave tile cols
@@ -641,6 +645,9 @@ __global__ __launch_bounds__(NT, 512 / NT) void gemm_kernel(GemmArgs args, int t
         if (m < M && n < N) {
             if constexpr (OMODE == GemmOut::kF16) {
                 args.y16[static_cast<int64_t>(m) * N + n] = static_cast<half_t>(v);
+            } else if constexpr (OMODE == GemmOut::kFused) {
+                args.y16[static_cast<int64_t>(m) * N + n] =
+                    epilogue_apply(args.epilogue, v, epilogue_load(args.epilogue, m, n));
             } else if constexpr (OMODE == GemmOut::kF32) {
                 args.y32[ref_offset(m, n, ref_tiles_n)] = v;
             } else {
@@ -674,6 +681,32 @@ __global__ __launch_bounds__(NT, 512 / NT) void gemm_kernel(GemmArgs args, int t
                 for (int j = 0; j < TN; ++j)
 #pragma unroll
                     for (int e = 0; e < 16; ++e) emit(tm, tn, i, j, e, acc[i][j][e], sq);
+        } else if constexpr (OMODE == GemmOut::kFused) {
+            // a sub-tile's operands are loaded while the one before it is
+            // finished and stored
+            EpilogueBits eb[2][16];
+            auto load = [&](int ij, EpilogueBits (&b)[16]) {
+                const int n = tn + wn + ij % TN * 32 + lcol;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int m = tm + wm + ij / TN * 32 + (e >> 2) * 8 + lrow4 + (e & 3);
+                    b[e] = EpilogueBits{0, 0, 0};
+                    if (m < M && n < N) b[e] = epilogue_load(args.epilogue, m, n);
+                }
+            };
+            load(0, eb[0]);
+#pragma unroll
+            for (int ij = 0; ij < TM * TN; ++ij) {
+                if (ij + 1 < TM * TN) load(ij + 1, eb[(ij + 1) & 1]);
+                const int n = tn + wn + ij % TN * 32 + lcol;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int m = tm + wm + ij / TN * 32 + (e >> 2) * 8 + lrow4 + (e & 3);
+                    if (m < M && n < N)
+                        args.y16[static_cast<int64_t>(m) * N + n] =
+                            epilogue_apply(args.epilogue, acc[ij / TN][ij % TN][e], eb[ij & 1][e]);
+                }
+            }
         } else {
             // tiled layout: a lane's 16 values of a sub-tile are contiguous.
             // Sub-tiles that start inside [0, M) x [0, N) lie inside the
@@ -794,7 +827,7 @@ __global__ __launch_bounds__(NT, 512 / NT) void gemm_kernel(GemmArgs args, int t
             // each chunk's four outputs written as soon as they are complete.
             {
                 constexpr int kChunks = TM * TN * 4;
-                constexpr int kBatch = 8;
+                constexpr int kBatch = OMODE == GemmOut::kFused ? 4 : 8;   // fewer: the operands take registers too
                 float sq = 0.f;
 #pragma unroll
                 for (int c0 = 0; c0 < kChunks; c0 += kBatch) {
@@ -891,7 +924,8 @@ size_t partials_bytes() {
 }
 
 template <const Geometry& GEO, GemmB BMODE, GemmOut OMODE, bool DIRECT, int WGM = 2>
-void launch_cfg(const GemmArgs& args, void* workspace, hipStream_t stream) {
+void launch_cfg(const ArgsOf<OMODE>& args, void* workspace, hipStream_t stream) {
+    constexpr bool kHalfOut = OMODE == GemmOut::kF16 || OMODE == GemmOut::kFused;
     if constexpr (((OMODE == GemmOut::kLoss && BMODE == GemmB::kInt4) ||
                    (OMODE == GemmOut::kF32 && BMODE == GemmB::kF16)) && DIRECT && GEO.bn == 128) {
         if (args.b_tiled) {
@@ -908,8 +942,8 @@ void launch_cfg(const GemmArgs& args, void* workspace, hipStream_t stream) {
     StreamK sk;
     // Only fp16-output products take a workspace (the searches' fp32 and
     // loss forms never split), so the split instances exist for them alone.
-    if constexpr (OMODE != GemmOut::kF16) workspace = nullptr;
-    if (OMODE == GemmOut::kF16 && workspace != nullptr && use_stream_k(GEO, tiles, steps)) {
+    if constexpr (!kHalfOut) workspace = nullptr;
+    if (kHalfOut && workspace != nullptr && use_stream_k(GEO, tiles, steps)) {
         sk.ipt = static_cast<int>(steps);
         sk.total = static_cast<int>(tiles * sk.ipt);
         sk.grid = stream_k_grid(GEO, tiles, steps);
@@ -917,13 +951,13 @@ void launch_cfg(const GemmArgs& args, void* workspace, hipStream_t stream) {
         sk.r = sk.total % sk.grid;
         sk.counters = static_cast<int*>(workspace);
         sk.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + split_counter_bytes());
-        if constexpr (OMODE == GemmOut::kF16)
+        if constexpr (kHalfOut)
             hipLaunchKernelGGL((gemm_kernel<GEO.bm, GEO.bn, BMODE, OMODE, true, DIRECT, WGM, GEO.threads>),
                                dim3(static_cast<unsigned>(sk.grid)), dim3(GEO.threads), 0, stream, args,
                                static_cast<int>(tiles_n), sk);
         return;
     }
-    if constexpr (DIRECT && OMODE == GemmOut::kF16) {
+    if constexpr (DIRECT && kHalfOut) {
         if (workspace != nullptr && use_hybrid(GEO, tiles, steps)) {
             sk.dp_tiles = static_cast<int>(tiles / resident_slots(GEO) * resident_slots(GEO));
             const int64_t tail = tiles - sk.dp_tiles;
@@ -977,7 +1011,7 @@ bool use_wide(const GemmArgs& args, bool have_workspace) {
 // reference tile, which two blocks per CU overlap with each other's MFMAs
 // (the full-size scale search measured 153 ms there against 156 ms wide).
 template <GemmB BMODE, GemmOut OMODE>
-void launch_direct(const GemmArgs& args, void* workspace, hipStream_t stream) {
+void launch_direct(const ArgsOf<OMODE>& args, void* workspace, hipStream_t stream) {
     if constexpr (OMODE != GemmOut::kLoss) {
         if (use_wide(args, workspace != nullptr)) {
             launch_cfg<kWideTile, BMODE, OMODE, true, kDirectWgm>(args, workspace, stream);
@@ -988,7 +1022,7 @@ void launch_direct(const GemmArgs& args, void* workspace, hipStream_t stream) {
 }
 
 template <GemmOut OMODE>
-void launch_int4(const GemmArgs& args, void* workspace, hipStream_t stream) {
+void launch_int4(const ArgsOf<OMODE>& args, void* workspace, hipStream_t stream) {
     if (args.b_tiled && (OMODE != GemmOut::kLoss || !direct_ok(args))) return;   // caller checks: see launch_gemm
     if (direct_ok(args))
         launch_direct<GemmB::kInt4, OMODE>(args, workspace, stream);
@@ -1060,6 +1094,7 @@ awq_status launch_gemm(const GemmArgs& args, GemmB b, GemmOut out, hipStream_t s
             case GemmOut::kF16: launch_int4<GemmOut::kF16>(args, workspace, stream); break;
             case GemmOut::kF32: launch_int4<GemmOut::kF32>(args, workspace, stream); break;
             case GemmOut::kLoss: launch_int4<GemmOut::kLoss>(args, workspace, stream); break;
+            case GemmOut::kFused: return AWQ_ERR_CONFIG;    // launch_gemm_fused
         }
     } else {
         switch (out) {
@@ -1073,8 +1108,21 @@ awq_status launch_gemm(const GemmArgs& args, GemmB b, GemmOut out, hipStream_t s
                 else
                     launch_cfg<kNarrowTile, GemmB::kF16, GemmOut::kF32, false>(args, workspace, stream);
                 break;
-            case GemmOut::kLoss: return AWQ_ERR_CONFIG;
+            case GemmOut::kLoss:
+            case GemmOut::kFused: return AWQ_ERR_CONFIG;
         }
+    }
+    return last_launch_status();
+}
+
+awq_status launch_gemm_fused(const GemmFusedArgs& args, GemmB b, hipStream_t stream, void* workspace) {
+    if (args.M == 0 || args.N == 0) return AWQ_OK;
+    if (args.b_tiled || b == GemmB::kF16) return AWQ_ERR_CONFIG;
+    if (b == GemmB::kInt8) {
+        if (!direct_ok(args)) return AWQ_ERR_CONFIG;
+        launch_direct<GemmB::kInt8, GemmOut::kFused>(args, workspace, stream);
+    } else {
+        launch_int4<GemmOut::kFused>(args, workspace, stream);
     }
     return last_launch_status();
 }

@@ -32,7 +32,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "awq_internal.h"
+#include "epilogue.h"
 
 namespace awq {
 
@@ -300,11 +300,19 @@ constexpr int kSzPre = 4;   // 16-byte (scale, zero) pieces per thread loaded ah
 __host__ __device__ inline int gemv_sz_word_offset(int mt, int nchunk, int xv, int slots) {
     return (mt * nchunk * xv * 4 + mt * nchunk * 2 + slots * mt + 3) & ~3;
 }
-template <int BITS, int MT, int RPW, int CPL, int DEPTH, bool ONESHOT, int NW, int NL, bool SZL = false>
+//
+// EPI (single layer): the epilogue. One-shot: lane i MT + m of a wave holds
+// output (row i, m), loads its operands behind the weights and stores it.
+// Streaming: the thread that writes a parked sum loads them (at M <= 2, for
+// its first one, ahead of the stream).
+template <int BITS, int MT, int RPW, int CPL, int DEPTH, bool ONESHOT, int NW, int NL, bool SZL = false,
+          class EPI = NoEpilogue>
 __device__ __forceinline__ void gemv_body(const half_t* __restrict__ x, const uint32_t* __restrict__ qweight,
                                           const half_t* __restrict__ scales, const half_t* __restrict__ zeros,
-                                          half_t* __restrict__ y, int N, int K, int log2g, int max_sets,
-                                          int nblocks, const LayersArg<NL>& L) {
+                                          half_t* y, int N, int K, int log2g, int max_sets,
+                                          int nblocks, const LayersArg<NL>& L, const EPI& epi = EPI{}) {
+    constexpr bool kEpi = std::is_same_v<EPI, Epilogue>;
+    static_assert(!kEpi || (NL == 0 && RPW * MT <= 64), "the epilogue: one layer, one lane per output");
     extern __shared__ uint4 smem[];
     constexpr int XV = Chunk<BITS>::kXV;
     const int nchunk = K >> Chunk<BITS>::kShift;    // 32 (INT4) or 16 (W8) weights per chunk
@@ -433,6 +441,30 @@ __device__ __forceinline__ void gemv_body(const half_t* __restrict__ x, const ui
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) issue(ring[d]);
 
+    // the epilogue's operands: one-shot, the wave's row set (one per wave), a
+    // lane each; streaming, the outputs of the thread's first parked slot
+    [[maybe_unused]] EpilogueBits eb[kEpi && !ONESHOT ? MT : 1] = {};
+    auto slot_row = [&](int sl) {
+        const int w = sl / (max_sets * RPW);
+        const int rem = sl - w * max_sets * RPW;
+        const int cs = rem / RPW;
+        const int wg = blockIdx.x * NW + w;
+        const int sets_w = wg < nsets ? (nsets - 1 - wg) / W + 1 : 0;
+        const int row = (wg + cs * W) * RPW + rem - cs * RPW;
+        return sl < NW * max_sets * RPW && cs < sets_w && row < N ? row : -1;
+    };
+    constexpr bool kEarly = ONESHOT ? MT * DEPTH <= 12 : MT <= 2;     // registers to spare
+    if constexpr (kEpi && ONESHOT && kEarly) {
+        const int row = wid * RPW + lane / MT;
+        if (lane < RPW * MT && row < N) eb[0] = epilogue_load(epi, lane % MT, row);
+    } else if constexpr (kEpi && kEarly) {
+        const int row = slot_row(threadIdx.x);
+        if (row >= 0) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m) eb[m] = epilogue_load(epi, m, row);
+        }
+    }
+
     // 2. stage x in LDS while the weights are in flight
 #pragma unroll
     for (int p = 0; p < XPRE; ++p)
@@ -485,18 +517,31 @@ __device__ __forceinline__ void gemv_body(const half_t* __restrict__ x, const ui
                     // row set finished: reduce; lane 63 stores the sums (one-shot)
                     // or parks them in LDS (streaming: no stores among the loads)
                     const int r0 = (wid + c_set * W) * RPW;
+                    [[maybe_unused]] float mine = 0.f;
 #pragma unroll
                     for (int i = 0; i < RPW; ++i) {
 #pragma unroll
                         for (int m = 0; m < MT; ++m) {
                             const float v = wave_sum_lane63(acc[i][m]);
-                            if (ONESHOT) {
+                            if constexpr (ONESHOT && kEpi) {
+                                // the sum to the lane of its output
+                                const float total = __builtin_bit_cast(
+                                    float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+                                mine = lane == i * MT + m ? total : mine;
+                            } else if (ONESHOT) {
                                 if (lane == 63 && r0 + i < N) store_y(m, r0 + i, v);
                             } else if (lane == 63) {
                                 yl[((wave * max_sets + c_set) * RPW + i) * MT + m] = v;
                             }
                             acc[i][m] = 0.f;
                         }
+                    }
+                    if constexpr (ONESHOT && kEpi) {
+                        const int row = r0 + lane / MT;
+                        if constexpr (!kEarly)
+                            if (lane < RPW * MT && row < N) eb[0] = epilogue_load(epi, lane % MT, row);
+                        if (lane < RPW * MT && row < N)
+                            y[static_cast<int64_t>(lane % MT) * N + row] = epilogue_apply(epi, mine, eb[0]);
                     }
                     c_kb = 0;
                     ++c_set;
@@ -510,6 +555,20 @@ __device__ __forceinline__ void gemv_body(const half_t* __restrict__ x, const ui
     // 4. write the block's rows
     __syncthreads();
     const int slots = NW * max_sets * RPW;
+    if constexpr (kEpi) {
+        for (int sl = threadIdx.x; sl < slots; sl += NW * 64) {
+            const int row = slot_row(sl);
+            if (row < 0) continue;
+            if (!kEarly || sl != static_cast<int>(threadIdx.x)) {
+#pragma unroll
+                for (int m = 0; m < MT; ++m) eb[m] = epilogue_load(epi, m, row);
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                y[static_cast<int64_t>(m) * N + row] = epilogue_apply(epi, yl[sl * MT + m], eb[m]);
+        }
+        return;
+    }
     for (int sl = threadIdx.x; sl < slots; sl += NW * 64) {
         const int w = sl / (max_sets * RPW);
         const int rem = sl - w * max_sets * RPW;
@@ -541,6 +600,18 @@ __global__ __launch_bounds__(NW * 64) void gemv_kernel(const half_t* __restrict_
                                                    int nblocks) {
     gemv_body<BITS, MT, RPW, CPL, DEPTH, ONESHOT, NW, 0, SZL>(x, qweight, scales, zeros, y, N, K, shape & 0xFF,
                                                                shape >> 8, nblocks, NoLayers{});
+}
+// The same with the epilogue, whose operands follow the preloaded arguments
+// (their loads are issued behind the weights').
+template <int BITS, int MT, int RPW, int CPL, int DEPTH, bool ONESHOT, int NW, bool SZL = false>
+__global__ __launch_bounds__(NW * 64) void gemv_fused_kernel(const half_t* __restrict__ x,
+                                                         const uint32_t* __restrict__ qweight,
+                                                         const half_t* __restrict__ scales,
+                                                         const half_t* __restrict__ zeros, half_t* y, int N, int K,
+                                                         int shape, int nblocks, Epilogue epi) {
+    gemv_body<BITS, MT, RPW, CPL, DEPTH, ONESHOT, NW, 0, SZL, Epilogue>(x, qweight, scales, zeros, y, N, K,
+                                                                         shape & 0xFF, shape >> 8, nblocks, NoLayers{},
+                                                                         epi);
 }
 // The grouped form takes the weight pointers of up to four layers and the
 // first stacked rows of layers 1-3 as separate arguments: preloading covers
@@ -658,6 +729,7 @@ struct GemvTarget {
     const half_t* zeros;
     half_t* y;
     LayersArg<NL> L;
+    const Epilogue* epilogue = nullptr;     // one layer only
 };
 
 // LDS of a streaming launch with its (scale, zero) pairs staged (SZL), or 0
@@ -686,8 +758,10 @@ awq_status launch_t(const half_t* x, const GemvTarget<NL>& tg, int64_t N, int64_
     if constexpr (NL > 0)
         kern = reinterpret_cast<const void*>(&gemv_grouped_kernel<BITS, MT, RPW, CPL, DEPTH, ONESHOT, NW, NL>);
     else
-        kern = reinterpret_cast<const void*>(&gemv_kernel<BITS, MT, RPW, CPL, DEPTH, ONESHOT, NW, SZL>);
-    static bool attr_set = false;
+        kern = tg.epilogue ? reinterpret_cast<const void*>(&gemv_fused_kernel<BITS, MT, RPW, CPL, DEPTH, ONESHOT, NW, SZL>)
+                           : reinterpret_cast<const void*>(&gemv_kernel<BITS, MT, RPW, CPL, DEPTH, ONESHOT, NW, SZL>);
+    static bool attr_sets[2] = {false, false};
+    bool& attr_set = attr_sets[tg.epilogue != nullptr];
     if (!attr_set) {
         if (hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, max_shared_bytes()) != hipSuccess)
             return AWQ_ERR_HIP;
@@ -761,6 +835,11 @@ awq_status launch_t(const half_t* x, const GemvTarget<NL>& tg, int64_t N, int64_
                            static_cast<int>(K), log2g | static_cast<int>(max_sets << 8), static_cast<int>(blocks),
                            T.q0, T.q1, T.q2, T.b1, T.b2, T.q3, T.b3, tail);
     }
+    else if (tg.epilogue)
+        hipLaunchKernelGGL((gemv_fused_kernel<BITS, MT, RPW, CPL, DEPTH, ONESHOT, NW, SZL>),
+                           dim3(static_cast<unsigned>(blocks)), dim3(NW * 64), lds, stream, x, tg.qweight, tg.scales,
+                           tg.zeros, tg.y, static_cast<int>(N), static_cast<int>(K),
+                           log2g | static_cast<int>(max_sets << 8), static_cast<int>(blocks), *tg.epilogue);
     else
         hipLaunchKernelGGL((gemv_kernel<BITS, MT, RPW, CPL, DEPTH, ONESHOT, NW, SZL>), dim3(static_cast<unsigned>(blocks)),
                            dim3(NW * 64), lds, stream, x, tg.qweight, tg.scales, tg.zeros, tg.y, static_cast<int>(N),
@@ -873,8 +952,9 @@ bool gemv_supported(int64_t M, int64_t N, int64_t K, int bits) {
 namespace {
 template <int BITS>
 awq_status launch_gemv_bits(const half_t* x, const uint32_t* qweight, const half_t* scales, const half_t* zeros,
-                            int64_t M, int64_t N, int64_t K, int log2g, half_t* y, hipStream_t stream) {
-    const GemvTarget<0> tg{qweight, scales, zeros, y, NoLayers{}};
+                            int64_t M, int64_t N, int64_t K, int log2g, half_t* y, hipStream_t stream,
+                            const Epilogue* epilogue) {
+    const GemvTarget<0> tg{qweight, scales, zeros, y, NoLayers{}, epilogue};
     switch (M) {
         case 1: return launch_m<BITS, 1>(x, tg, N, K, log2g, stream);
         case 2: return launch_m<BITS, 2>(x, tg, N, K, log2g, stream);
@@ -891,10 +971,10 @@ awq_status launch_gemv_bits(const half_t* x, const uint32_t* qweight, const half
 
 awq_status launch_gemv(const half_t* x, const uint32_t* qweight, const half_t* scales,
                        const half_t* zeros, int64_t M, int64_t N, int64_t K, int group_size,
-                       half_t* y, hipStream_t stream, int bits) {
+                       half_t* y, hipStream_t stream, int bits, const Epilogue* epilogue) {
     const int log2g = 31 - __builtin_clz(static_cast<unsigned>(group_size));   // G is a power of two >= 32
-    if (bits == 8) return launch_gemv_bits<8>(x, qweight, scales, zeros, M, N, K, log2g, y, stream);
-    return launch_gemv_bits<4>(x, qweight, scales, zeros, M, N, K, log2g, y, stream);
+    if (bits == 8) return launch_gemv_bits<8>(x, qweight, scales, zeros, M, N, K, log2g, y, stream, epilogue);
+    return launch_gemv_bits<4>(x, qweight, scales, zeros, M, N, K, log2g, y, stream, epilogue);
 }
 
 namespace {

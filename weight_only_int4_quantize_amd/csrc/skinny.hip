@@ -34,7 +34,9 @@
 //   so each starts on slot 0.
 #include <algorithm>
 
-#include "awq_internal.h"
+#include <type_traits>
+
+#include "epilogue.h"
 
 namespace awq {
 namespace {
@@ -119,14 +121,15 @@ constexpr int kSkSZForm[3] = {4, 8, 32};
 // phase_groups < 65536): with it every argument the waves need before the
 // fixup is within the 14 preloaded argument dwords (the partial and counter
 // pointers, used last, follow)
-template <int MB, int WPL, int FORM>
-__global__ __launch_bounds__(kSkThreads, 1) void skinny_kernel(const half_t* __restrict__ x,
-                                                              const uint32_t* __restrict__ qweight,
-                                                              const half_t* __restrict__ scales,
-                                                              const half_t* __restrict__ zeros,
-                                                              half_t* __restrict__ y, int N, int K, uint32_t msp,
-                                                              float* __restrict__ partials,
-                                                              int* __restrict__ counters) {
+//
+// EPI: the epilogue, its operands loaded ahead of the partial tiles' sums by
+// the threads that store.
+template <int MB, int WPL, int FORM, class EPI = NoEpilogue>
+__device__ __forceinline__ void skinny_body(const half_t* __restrict__ x, const uint32_t* __restrict__ qweight,
+                                            const half_t* __restrict__ scales, const half_t* __restrict__ zeros,
+                                            half_t* y, int N, int K, uint32_t msp, float* __restrict__ partials,
+                                            int* __restrict__ counters, const EPI& epi = EPI{}) {
+    constexpr bool kEpi = std::is_same_v<EPI, Epilogue>;
     const int M = static_cast<int>(msp & 127u);
     const int splits = static_cast<int>((msp >> 7) & 511u);
     const int phase_groups = static_cast<int>(msp >> 16);
@@ -343,20 +346,41 @@ __global__ __launch_bounds__(kSkThreads, 1) void skinny_kernel(const half_t* __r
     }
 
     // ---- epilogue: lane holds rows 16 mb + 4 lg + e of column n ----
+    // EPI: a row block's operands are loaded while the one before it is stored
+    [[maybe_unused]] EpilogueBits eb[2][2][4] = {};
+    [[maybe_unused]] auto load_epilogue = [&](int mb) {
+        if constexpr (kEpi) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int m = 16 * mb + 4 * lg + e, n = n_base + 16 * t + col;
+                    if (m < M && n < N) eb[mb & 1][t][e] = epilogue_load(epi, m, n);
+                }
+        }
+    };
     auto emit = [&](const float4_t (&v)[MB][2]) {
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb)
+        for (int mb = 0; mb < MB; ++mb) {
+            if (mb + 1 < MB) load_epilogue(mb + 1);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const int n = n_base + 16 * t + col;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int m = 16 * mb + 4 * lg + e;
-                    if (m < M && n < N) y[static_cast<int64_t>(m) * N + n] = static_cast<half_t>(v[mb][t][e]);
+                    if constexpr (kEpi) {
+                        if (m < M && n < N)
+                            y[static_cast<int64_t>(m) * N + n] = epilogue_apply(epi, v[mb][t][e], eb[mb & 1][t][e]);
+                    } else if (m < M && n < N) {
+                        y[static_cast<int64_t>(m) * N + n] = static_cast<half_t>(v[mb][t][e]);
+                    }
                 }
             }
+        }
     };
     if (splits == 1) {
+        load_epilogue(0);
         emit(acc);
         return;
     }
@@ -381,6 +405,7 @@ __global__ __launch_bounds__(kSkThreads, 1) void skinny_kernel(const half_t* __r
                  splits - 1;
     __syncthreads();
     if (!s_last) return;
+    load_epilogue(0);
     float4_t sum[MB][2];
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb)
@@ -409,6 +434,26 @@ __global__ __launch_bounds__(kSkThreads, 1) void skinny_kernel(const half_t* __r
     }
     emit(sum);
     if (tid == 0) __hip_atomic_store(&counters[tile], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+template <int MB, int WPL, int FORM>
+__global__ __launch_bounds__(kSkThreads, 1) void skinny_kernel(const half_t* __restrict__ x,
+                                                              const uint32_t* __restrict__ qweight,
+                                                              const half_t* __restrict__ scales,
+                                                              const half_t* __restrict__ zeros,
+                                                              half_t* __restrict__ y, int N, int K, uint32_t msp,
+                                                              float* __restrict__ partials,
+                                                              int* __restrict__ counters) {
+    skinny_body<MB, WPL, FORM>(x, qweight, scales, zeros, y, N, K, msp, partials, counters);
+}
+template <int MB, int WPL, int FORM>
+__global__ __launch_bounds__(kSkThreads, 1) void skinny_fused_kernel(const half_t* __restrict__ x,
+                                                                    const uint32_t* __restrict__ qweight,
+                                                                    const half_t* __restrict__ scales,
+                                                                    const half_t* __restrict__ zeros, half_t* y, int N,
+                                                                    int K, uint32_t msp, float* __restrict__ partials,
+                                                                    int* __restrict__ counters, Epilogue epi) {
+    skinny_body<MB, WPL, FORM, Epilogue>(x, qweight, scales, zeros, y, N, K, msp, partials, counters, epi);
 }
 
 int64_t sk_tiles(int64_t N) { return (N + kSkBN - 1) / kSkBN; }
@@ -469,16 +514,26 @@ bool sk_plan(int64_t M, int64_t N, int64_t K, int group_size, bool have_workspac
 template <int MB, int WPL, int FORM>
 awq_status launch_form(const half_t* x, const uint32_t* qweight, const half_t* scales, const half_t* zeros, int M,
                        int N, int K, half_t* y, int splits, int pg, float* partials, int* counters, size_t lds,
-                       hipStream_t stream) {
-    static bool attr_set = false;
+                       hipStream_t stream, const Epilogue* epilogue) {
+    static bool attr_sets[2] = {false, false};
+    bool& attr_set = attr_sets[epilogue != nullptr];
     if (!attr_set) {
-        if (hipFuncSetAttribute(reinterpret_cast<const void*>(&skinny_kernel<MB, WPL, FORM>),
-                                hipFuncAttributeMaxDynamicSharedMemorySize, kSkLds) != hipSuccess)
+        const void* kern = epilogue ? reinterpret_cast<const void*>(&skinny_fused_kernel<MB, WPL, FORM>)
+                                    : reinterpret_cast<const void*>(&skinny_kernel<MB, WPL, FORM>);
+        if (hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, kSkLds) != hipSuccess)
             return AWQ_ERR_HIP;
         attr_set = true;
     }
     if (M >= 128 || splits >= 512 || pg >= 65536) return AWQ_ERR_SHAPE;   // the packed msp fields
     const int64_t blocks = sk_tiles(N) * splits;
+    if (epilogue) {
+        hipLaunchKernelGGL((skinny_fused_kernel<MB, WPL, FORM>), dim3(static_cast<unsigned>(blocks)), dim3(kSkThreads),
+                           lds, stream, x, qweight, scales, zeros, y, N, K,
+                           static_cast<uint32_t>(M) | (static_cast<uint32_t>(splits) << 7) |
+                               (static_cast<uint32_t>(pg) << 16),
+                           partials, counters, *epilogue);
+        return last_launch_status();
+    }
     hipLaunchKernelGGL((skinny_kernel<MB, WPL, FORM>), dim3(static_cast<unsigned>(blocks)), dim3(kSkThreads), lds,
                        stream, x, qweight, scales, zeros, y, N, K,
                        static_cast<uint32_t>(M) | (static_cast<uint32_t>(splits) << 7) |
@@ -489,7 +544,7 @@ awq_status launch_form(const half_t* x, const uint32_t* qweight, const half_t* s
 
 template <int MB, int WPL>
 awq_status launch_cfg(const half_t* x, const uint32_t* qweight, const half_t* scales, const half_t* zeros, int M,
-                      int N, int K, half_t* y, void* workspace, hipStream_t stream) {
+                      int N, int K, half_t* y, void* workspace, hipStream_t stream, const Epilogue* epilogue) {
     int splits = 0, pg = 0;
     if (!sk_plan(M, N, K, WPL * 32, workspace != nullptr, splits, pg)) return AWQ_ERR_CONFIG;
     float* partials = nullptr;
@@ -508,21 +563,21 @@ awq_status launch_cfg(const half_t* x, const uint32_t* qweight, const half_t* sc
     };
     if (fits(0))
         return launch_form<MB, WPL, 0>(x, qweight, scales, zeros, M, N, K, y, splits, pg, partials, counters, lds,
-                                          stream);
+                                          stream, epilogue);
     if (fits(1))
         return launch_form<MB, WPL, 1>(x, qweight, scales, zeros, M, N, K, y, splits, pg, partials, counters, lds,
-                                          stream);
+                                          stream, epilogue);
     return launch_form<MB, WPL, 2>(x, qweight, scales, zeros, M, N, K, y, splits, pg, partials, counters, lds,
-                                      stream);
+                                      stream, epilogue);
 }
 
 template <int WPL>
 awq_status launch_wpl(const half_t* x, const uint32_t* qweight, const half_t* scales, const half_t* zeros, int M,
-                      int N, int K, half_t* y, void* workspace, hipStream_t stream) {
+                      int N, int K, half_t* y, void* workspace, hipStream_t stream, const Epilogue* epilogue) {
     switch (sk_mb(M)) {
-        case 1: return launch_cfg<1, WPL>(x, qweight, scales, zeros, M, N, K, y, workspace, stream);
-        case 2: return launch_cfg<2, WPL>(x, qweight, scales, zeros, M, N, K, y, workspace, stream);
-        default: return launch_cfg<4, WPL>(x, qweight, scales, zeros, M, N, K, y, workspace, stream);
+        case 1: return launch_cfg<1, WPL>(x, qweight, scales, zeros, M, N, K, y, workspace, stream, epilogue);
+        case 2: return launch_cfg<2, WPL>(x, qweight, scales, zeros, M, N, K, y, workspace, stream, epilogue);
+        default: return launch_cfg<4, WPL>(x, qweight, scales, zeros, M, N, K, y, workspace, stream, epilogue);
     }
 }
 
@@ -551,15 +606,15 @@ size_t skinny_workspace_bytes(int64_t M, int64_t N, int64_t K) {
 
 awq_status launch_skinny(const half_t* x, const uint32_t* qweight, const half_t* scales, const half_t* zeros,
                          int64_t M, int64_t N, int64_t K, int group_size, half_t* y, void* workspace,
-                         hipStream_t stream) {
+                         hipStream_t stream, const Epilogue* epilogue) {
     if (M == 0 || N == 0) return AWQ_OK;
     if (!skinny_supported(M, N, K, group_size, workspace != nullptr)) return AWQ_ERR_CONFIG;
     const int m = static_cast<int>(M), n = static_cast<int>(N), k = static_cast<int>(K);
     switch (group_size) {
-        case 32: return launch_wpl<1>(x, qweight, scales, zeros, m, n, k, y, workspace, stream);
-        case 64: return launch_wpl<2>(x, qweight, scales, zeros, m, n, k, y, workspace, stream);
-        case 128: return launch_wpl<4>(x, qweight, scales, zeros, m, n, k, y, workspace, stream);
-        case 256: return launch_wpl<8>(x, qweight, scales, zeros, m, n, k, y, workspace, stream);
+        case 32: return launch_wpl<1>(x, qweight, scales, zeros, m, n, k, y, workspace, stream, epilogue);
+        case 64: return launch_wpl<2>(x, qweight, scales, zeros, m, n, k, y, workspace, stream, epilogue);
+        case 128: return launch_wpl<4>(x, qweight, scales, zeros, m, n, k, y, workspace, stream, epilogue);
+        case 256: return launch_wpl<8>(x, qweight, scales, zeros, m, n, k, y, workspace, stream, epilogue);
         default: return AWQ_ERR_CONFIG;
     }
 }
