@@ -542,7 +542,9 @@ awq_status awq_gemm_w8(const void* x_f16, const uint32_t* qweight,
  *                   otherwise it must not overlap any input.
  *   path, workspace, the other arguments   as awq_gemm_ex (bits 4) or
  *                   awq_gemm_w8 (bits 8)
- * The kernel and the sums are those of the call without an epilogue.
+ * The sums are those of the call without an epilogue, up to fp32 summation
+ * order from M = 33 (bits 8: M = 9) up, where a few hundred rows take a
+ * smaller tile. With nothing to fuse the call is the plain one.
  */
 enum { AWQ_ACT_NONE = 0, AWQ_ACT_RELU = 1, AWQ_ACT_SILU = 2, AWQ_ACT_GELU = 3, AWQ_ACT_GELU_TANH = 4 };
 awq_status awq_gemm_fused(const void* x_f16, const uint32_t* qweight,

@@ -580,20 +580,52 @@ def awq_gemm_w8(x, qweight, scales, zeros, group_size: int = 128, path: int = PA
 
 # ---------------------------------------------------------------- the linear layer with its epilogue
 
-def _need_rows(name: str, t, M: int, N: int, device) -> int:
-    """fp16 [M, N] with contiguous rows on `device`; returns its row stride."""
+def _need_on(name: str, t, dtype, index: int) -> None:
+    _need_gpu(name, t, dtype)
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on GPU {index}")
+
+
+def _workspace(t, index: int):
+    """Address and bytes of a uint8 workspace on GPU `index`, or of none."""
+    if t is None:
+        return None, 0
+    _need_on("workspace", t, _torch().uint8, index)
+    return t.data_ptr(), t.numel()
+
+
+def _rows(name: str, t, shape, dtype, index: int):
+    """Address and row stride of fp16 [M, N] with contiguous rows, or of none."""
+    if t is None:
+        return None, 0
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.float16:
-        raise TypeError(f"{name} must be torch.float16, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    if tuple(t.shape) != (M, N):
-        raise ValueError(f"{name} must be [{M}, {N}], got {list(t.shape)}")
-    if N > 1 and t.stride(1) != 1:
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on GPU {index}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    row, col = t.stride()
+    if shape[1] > 1 and col != 1:
         raise ValueError(f"{name}'s rows must be contiguous")
-    return t.stride(0) if M > 1 else N
+    return t.data_ptr(), row if shape[0] > 1 else shape[1]
+
+
+def _explain_layer(x, qweight, scales, zeros, group_size) -> None:
+    """Raises what is wrong with a linear layer's tensors."""
+    torch = _torch()
+    _need_gpu("x", x, torch.float16)
+    index = x.get_device()
+    _need_on("qweight", qweight, torch.int32, index)
+    _need_on("scales", scales, torch.float16, index)
+    _need_on("zeros", zeros, torch.float16, index)
+    if x.dim() != 2 or qweight.dim() != 2:
+        raise ValueError("x and qweight must be 2-D")
+    if not isinstance(group_size, int) or group_size < 1:
+        raise ValueError("group_size must be a positive integer")
+    raise ValueError("scales/zeros must be [N, K/group_size]")
 
 
 def awq_gemm_fused(x, qweight, scales, zeros, group_size: int = 128, bias=None, activation: str = "none", mul=None,
@@ -605,45 +637,42 @@ def awq_gemm_fused(x, qweight, scales, zeros, group_size: int = 128, bias=None, 
     activation one of ACTIVATIONS. out may be residual or mul itself (when
     packed). workspace: gemm_workspace(M, N, K)."""
     torch = _torch()
-    _need_gpu("x", x, torch.float16)
-    _need_gpu("qweight", qweight, torch.int32)
-    _need_gpu("scales", scales, torch.float16)
-    _need_gpu("zeros", zeros, torch.float16)
-    if x.dim() != 2 or qweight.dim() != 2:
-        raise ValueError("x and qweight must be 2-D")
-    if activation not in ACTIVATIONS:
-        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
-    M, K = x.shape
-    N, words = qweight.shape
+    half = torch.float16
+    try:
+        (M, K), (N, words), index = x.shape, qweight.shape, x.get_device()
+        layer = (N, K // group_size)
+        ok = x.dtype is half and x.is_contiguous() and qweight.dtype is torch.int32 and qweight.is_contiguous() and \
+            scales.dtype is half and scales.is_contiguous() and zeros.dtype is half and zeros.is_contiguous() and \
+            scales.shape == layer and zeros.shape == layer and \
+            index == qweight.get_device() == scales.get_device() == zeros.get_device() and index >= 0
+    except (AttributeError, TypeError, ValueError, ZeroDivisionError):
+        ok = False
+    if not ok:
+        _explain_layer(x, qweight, scales, zeros, group_size)
     bits = 4 if words * 8 == K else 8
     if words * 32 != K * bits:
         raise ValueError(f"qweight has {words} words per row, K={K} needs {K // 8} (INT4) or {K // 4} (W8)")
-    if scales.shape != (N, K // group_size) or zeros.shape != scales.shape:
-        raise ValueError("scales/zeros must be [N, K/group_size]")
-    dev = x.device
-    if not (qweight.device == scales.device == zeros.device == dev):
-        raise ValueError(f"the layer's tensors must be on {dev}")
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
+    bias_p = None
     if bias is not None:
-        _need_gpu("bias", bias, torch.float16)
-        if tuple(bias.shape) != (N,) or bias.device != dev:
-            raise ValueError(f"bias must be [{N}] on {dev}")
-    mul_stride = _need_rows("mul", mul, M, N, dev) if mul is not None else 0
-    residual_stride = _need_rows("residual", residual, M, N, dev) if residual is not None else 0
+        _need_on("bias", bias, half, index)
+        if bias.shape != (N,):
+            raise ValueError(f"bias must be [{N}]")
+        bias_p = bias.data_ptr()
+    shape = (M, N)
+    mul_p, mul_stride = _rows("mul", mul, shape, half, index)
+    res_p, res_stride = _rows("residual", residual, shape, half, index)
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float16, device=dev)
-    else:
-        _need_gpu("out", out, torch.float16)
-        if tuple(out.shape) != (M, N) or out.device != dev:
-            raise ValueError(f"out must be [{M}, {N}] on {dev}")
-    nbytes = 0
-    if workspace is not None:
-        _need_gpu("workspace", workspace, torch.uint8)
-        if workspace.device != dev:
-            raise ValueError(f"workspace must be on {dev}")
-        nbytes = workspace.numel()
-    st = _on_device(dev, load().awq_gemm_fused, x.data_ptr(), qweight.data_ptr(), scales.data_ptr(), zeros.data_ptr(),
-                    M, N, K, group_size, bits, _ptr(bias), ACTIVATIONS[activation], _ptr(mul), mul_stride,
-                    _ptr(residual), residual_stride, out.data_ptr(), path, _ptr(workspace), nbytes)
+        out = torch.empty(shape, dtype=half, device=x.device)
+    elif out.dtype is not half or out.shape != shape or not out.is_contiguous() or out.get_device() != index:
+        _need_on("out", out, half, index)
+        raise ValueError(f"out must be [{M}, {N}]")
+    ws, nbytes = _workspace(workspace, index)
+    st = _on_device(index, (_lib or load()).awq_gemm_fused, x.data_ptr(), qweight.data_ptr(), scales.data_ptr(),
+                    zeros.data_ptr(), M, N, K, group_size, bits, bias_p, act, mul_p, mul_stride, res_p, res_stride,
+                    out.data_ptr(), path, ws, nbytes)
     if st != AWQ_OK:
         _check("awq_gemm_fused", st)
     return out
@@ -676,7 +705,7 @@ class KVCache:
             raise ValueError("the cache's tensors must be on one device")
         self.k_codes, self.v_codes, self.k_scales, self.v_scales, self.fmt = k_codes, v_codes, k_scales, v_scales, fmt
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = pages, heads, page, dc * 16
-        self.device = k_codes.device
+        self.device, self.index, self.half = k_codes.device, k_codes.get_device(), torch.float16
         self._struct = _KVCacheStruct(_ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), pages, heads, page,
                                       dc * 16, KV_FORMATS[fmt])
         self._ref = ctypes.addressof(self._struct)
@@ -725,30 +754,47 @@ class KVSeqs:
             max_len = int(kv_len.max()) if n else 0
         self.block_table, self.cu_tokens, self.kv_len = block_table, cu_tokens, kv_len
         self.max_tokens, self.max_len, self.n_seqs = int(max_tokens), int(max_len), n
-        self.device = kv_len.device
+        self.device, self.index = kv_len.device, kv_len.get_device()
         stride = block_table.stride(0) if n > 1 else block_table.shape[1]
         self._struct = _KVSeqsStruct(_ptr(block_table), _ptr(cu_tokens), _ptr(kv_len), stride, block_table.shape[1], n,
                                      self.max_tokens, self.max_len)
         self._ref = ctypes.addressof(self._struct)
 
 
-def _on_device(device, fn, *args):
-    """fn(*args, stream) with `device` current, on its current stream."""
+_torch_c = None        # (current device index, raw current stream of an index)
+
+
+def _torch_calls():
+    """torch's current device and the raw handle of a device's current stream,
+    by its C entry points where this torch has them: the public Stream object
+    costs 2 us a call, a third of a small launch."""
+    global _torch_c
     torch = _torch()
-    if torch.cuda.current_device() == device.index:
-        return fn(*args, torch.cuda.current_stream(device).cuda_stream)
-    with torch.cuda.device(device):
-        return fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    get = getattr(torch._C, "_cuda_getDevice", None)
+    _torch_c = (get or torch.cuda.current_device,
+                raw or (lambda i: torch.cuda.current_stream(i).cuda_stream))
+    return _torch_c
+
+
+def _on_device(index: int, fn, *args) -> int:
+    """fn(*args, stream) with GPU `index` current, on its current stream."""
+    current, raw = _torch_c or _torch_calls()
+    if current() == index:
+        return fn(*args, raw(index))
+    with _torch().cuda.device(index):
+        return fn(*args, raw(index))
 
 
 def _need_tokens(name: str, t, cache, heads: int | None) -> None:
-    """fp16 [T, heads, D] with contiguous channels on the cache's device."""
+    """Raises what is wrong with t as fp16 [T, heads, D] with contiguous
+    channels on the cache's device."""
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != torch.float16:
         raise TypeError(f"{name} must be torch.float16, got {t.dtype}")
-    if t.device != cache.device:
+    if t.get_device() != cache.index:
         raise ValueError(f"{name} must be on {cache.device}")
     if t.dim() != 3 or t.shape[2] != cache.head_dim or (heads is not None and t.shape[1] != heads):
         raise ValueError(f"{name} must be [tokens, {'heads' if heads is None else heads}, {cache.head_dim}]")
@@ -756,13 +802,23 @@ def _need_tokens(name: str, t, cache, heads: int | None) -> None:
         raise ValueError(f"{name}'s channels must be contiguous")
 
 
-def _strides(t):
-    """Token and head strides; an extent of one has none."""
-    return t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0
+def _tokens(name: str, t, cache, heads: int | None):
+    """Checks t (see _need_tokens); its tokens, heads, and the strides of
+    both (0 where there is one)."""
+    try:
+        T, h, D = t.shape
+        st, sh, sd = t.stride()
+        ok = sd == 1 and D == cache.head_dim and (heads is None or h == heads) and t.dtype is cache.half and \
+            t.get_device() == cache.index
+    except (AttributeError, TypeError, ValueError):
+        ok = False
+    if not ok:
+        _need_tokens(name, t, cache, heads)
+    return T, h, st if T > 1 else 0, sh if h > 1 else 0
 
 
 def _need_seqs(cache, seqs) -> None:
-    if seqs.device != cache.device:
+    if seqs.index != cache.index:
         raise ValueError(f"seqs must be on {cache.device}")
 
 
@@ -770,13 +826,12 @@ def awq_kv_write(cache: KVCache, seqs: KVSeqs, k, v) -> None:
     """awq_kv_write: quantizes the batch's new tokens k, v (fp16 [T, heads, D],
     any token and head strides that are multiples of 8) into the cache."""
     _need_seqs(cache, seqs)
-    _need_tokens("k", k, cache, cache.n_kv_heads)
-    _need_tokens("v", v, cache, cache.n_kv_heads)
-    T = k.shape[0]
-    if v.shape[0] != T:
+    T, _, k_token, k_head = _tokens("k", k, cache, cache.n_kv_heads)
+    T2, _, v_token, v_head = _tokens("v", v, cache, cache.n_kv_heads)
+    if T2 != T:
         raise ValueError("k and v must hold the same tokens")
-    st = _on_device(cache.device, load().awq_kv_write, cache._ref, seqs._ref, k.data_ptr(), *_strides(k),
-                    v.data_ptr(), *_strides(v), T)
+    st = _on_device(cache.index, (_lib or load()).awq_kv_write, cache._ref, seqs._ref, k.data_ptr(), k_token, k_head,
+                    v.data_ptr(), v_token, v_head, T)
     if st != AWQ_OK:
         _check("awq_kv_write", st)
 
@@ -797,17 +852,17 @@ def awq_kv_read(cache: KVCache, seqs: KVSeqs, n_tokens: int | None = None, out=N
     for name, t in (("k", k), ("v", v)):
         if t is None:
             continue
-        _need_tokens(name, t, cache, cache.n_kv_heads)
+        rows = _tokens(name, t, cache, cache.n_kv_heads)[0]
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-        if T is not None and t.shape[0] != T:
+        if T is not None and rows != T:
             raise ValueError("k and v must hold the same tokens")
-        T = t.shape[0]
+        T = rows
     if T is None:
         return k, v
     if n_tokens is not None and n_tokens != T:
         raise ValueError(f"out must hold {n_tokens} tokens")
-    st = _on_device(cache.device, load().awq_kv_read, cache._ref, seqs._ref, _ptr(k), _ptr(v), T)
+    st = _on_device(cache.index, (_lib or load()).awq_kv_read, cache._ref, seqs._ref, _ptr(k), _ptr(v), T)
     if st != AWQ_OK:
         _check("awq_kv_read", st)
     return k, v
@@ -837,27 +892,20 @@ def awq_kv_attention(q, cache: KVCache, seqs: KVSeqs, scale: float | None = None
     sequence are 0."""
     torch = _torch()
     _need_seqs(cache, seqs)
-    _need_tokens("q", q, cache, None)
-    T, heads, D = q.shape
+    T, heads, q_token, q_head = _tokens("q", q, cache, None)
     if out is None:
-        out = torch.zeros((T, heads, D), dtype=torch.float16, device=q.device)
-    else:
-        _need_tokens("out", out, cache, heads)
-        if out.shape[0] != T:
-            raise ValueError(f"out must be [{T}, {heads}, {D}]")
+        out = torch.zeros((T, heads, cache.head_dim), dtype=torch.float16, device=q.device)
+    T2, _, out_token, out_head = _tokens("out", out, cache, heads)
+    if T2 != T:
+        raise ValueError(f"out must be [{T}, {heads}, {cache.head_dim}]")
     if lse is not None:
         _need_gpu("lse", lse, torch.float32)
         if tuple(lse.shape) != (T, heads) or lse.device != q.device:
             raise ValueError(f"lse must be [{T}, {heads}] on {q.device}")
-    nbytes = 0
-    if workspace is not None:
-        _need_gpu("workspace", workspace, torch.uint8)
-        if workspace.device != q.device:
-            raise ValueError(f"workspace must be on {q.device}")
-        nbytes = workspace.numel()
-    st = _on_device(cache.device, load().awq_kv_attention, cache._ref, seqs._ref, q.data_ptr(), *_strides(q), T,
-                    heads, D ** -0.5 if scale is None else scale, 1 if causal else 0, window, out.data_ptr(),
-                    *_strides(out), _ptr(lse), _ptr(workspace), nbytes)
+    ws, nbytes = _workspace(workspace, cache.index)
+    st = _on_device(cache.index, (_lib or load()).awq_kv_attention, cache._ref, seqs._ref, q.data_ptr(), q_token, q_head,
+                    T, heads, cache.head_dim ** -0.5 if scale is None else scale, 1 if causal else 0, window,
+                    out.data_ptr(), out_token, out_head, _ptr(lse), ws, nbytes)
     if st != AWQ_OK:
         _check("awq_kv_attention", st)
     return out

@@ -280,8 +280,11 @@ awq_status gemm_dispatch(const void* x_f16, const uint32_t* qweight, const void*
     const half_t* sc = static_cast<const half_t*>(scales_f16);
     const half_t* zr = static_cast<const half_t*>(zeros_f16);
     half_t* y = static_cast<half_t*>(y_f16);
-    const int chosen = choose_path(M, N, K, group_size, path, workspace != nullptr || library_scratch);
+    int chosen = choose_path(M, N, K, group_size, path, workspace != nullptr || library_scratch);
     if (chosen < 0) return AWQ_ERR_CONFIG;
+    if (epilogue && path == 0 && chosen == 3 && M > kColTileMaxM &&
+        gemm_fused_mid(M, N, K, group_size, workspace != nullptr))
+        chosen = 2;
     const bool use_skinny = chosen == 3;
     if (chosen == 4) return launch_coltile(x, qweight, sc, zr, M, N, K, group_size, y, stream, epilogue);
     if (chosen == 1) return launch_gemv(x, qweight, sc, zr, M, N, K, group_size, y, stream, 4, epilogue);
@@ -774,6 +777,9 @@ awq_status awq_gemm_fused(const void* x_f16, const uint32_t* qweight, const void
     e.mul_stride = mul_stride;
     e.residual_stride = residual_stride;
     e.act = activation;
+    e.vectors = N % 8 == 0 && aligned16(y_f16) && aligned16(bias_f16) && aligned16(mul_f16) &&
+                aligned16(residual_f16) && (!mul_f16 || mul_stride % 8 == 0) &&
+                (!residual_f16 || residual_stride % 8 == 0);
     // nothing to fuse: the plain kernels
     const bool plain = !bias_f16 && !mul_f16 && !residual_f16 && activation == AWQ_ACT_NONE;
     const Epilogue* epilogue = plain ? nullptr : &e;

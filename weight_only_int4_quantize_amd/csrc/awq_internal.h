@@ -51,6 +51,7 @@ struct Epilogue {
     const half_t* residual = nullptr;
     int64_t mul_stride = 0, residual_stride = 0;
     int act = AWQ_ACT_NONE;
+    bool vectors = false;   // eight elements of a row make one aligned 16-byte access, y's too
 };
 
 // ---- launchers (each returns after enqueueing on `stream`) ----
@@ -178,6 +179,8 @@ size_t gemm_workspace_bytes(int64_t M, int64_t N);
 awq_status launch_gemm(const GemmArgs& args, GemmB b, GemmOut out, hipStream_t stream,
                        void* workspace = nullptr);
 // quantized B, fp16 output behind the epilogue
+// whether it runs 64-row tiles, which also beat the skinny kernel above 32 rows
+bool gemm_fused_mid(int64_t M, int64_t N, int64_t K, int group_size, bool have_workspace);
 awq_status launch_gemm_fused(const GemmFusedArgs& args, GemmB b, hipStream_t stream, void* workspace);
 
 // Skinny MFMA GEMM for 4 < M <= 64 (decode batches): 16x16x32 MFMAs whose B

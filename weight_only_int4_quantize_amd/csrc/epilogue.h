@@ -23,23 +23,69 @@ struct EpilogueBits {
 __device__ inline float epilogue_sigmoid(float x) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * x));
 }
-__device__ inline float epilogue_act(float v, int act) {
+// Phi(v) = 0.5 (1 + erf(v / sqrt 2)), by its tail H(a) = 0.5 erfc(a / sqrt 2),
+// a = |v|: H(a) e^(a^2 / 2) is smooth in t = 1 / (1 + 0.36 a), and the
+// coefficients are a weighted least-squares fit of it for a up to 14 (relative
+// error 9e-7; with the fp32 steps below 2^-18 for v > -6). The library's erfc
+// is several times the code, of which the kernels hold many copies.
+__device__ inline float epilogue_phi(float v) {
+    const float a = fabsf(v);
+    const float t = __builtin_amdgcn_rcpf(1.0f + 0.36f * a);
+    float p = 0.04706965759396553f;
+    p = p * t - 0.1798105090856552f;
+    p = p * t + 0.18101643025875092f;
+    p = p * t + 0.026506338268518448f;
+    p = p * t + 0.13973495364189148f;
+    p = p * t + 0.14176958799362183f;
+    p = p * t + 0.14371325075626373f;
+    const float h = p * t * __builtin_amdgcn_exp2f(-0.72134752f * a * a);
+    return v < 0.f ? h : 1.0f - h;
+}
+// v[0 .. N) in place; the choice of the activation is outside the elements
+template <int N>
+__device__ inline void epilogue_act(float (&v)[N], int act) {
     switch (act) {
-        case AWQ_ACT_RELU: return fmaxf(v, 0.f);
-        case AWQ_ACT_SILU: return v * epilogue_sigmoid(v);
-        // 0.5 (1 + erf(v / sqrt 2)) by the complement: exact to the last bits
-        // where the sum would cancel
-        case AWQ_ACT_GELU: return 0.5f * v * erfcf(-0.70710678f * v);
+        case AWQ_ACT_RELU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = fmaxf(v[i], 0.f);
+            break;
+        case AWQ_ACT_SILU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] *= epilogue_sigmoid(v[i]);
+            break;
+        case AWQ_ACT_GELU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] *= epilogue_phi(v[i]);
+            break;
         // 0.5 (1 + tanh u) = sigmoid(2 u)
-        case AWQ_ACT_GELU_TANH: return v * epilogue_sigmoid(1.59576912f * (v + 0.044715f * v * v * v));
-        default: return v;
+        case AWQ_ACT_GELU_TANH:
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                v[i] *= epilogue_sigmoid(1.59576912f * (v[i] + 0.044715f * v[i] * v[i] * v[i]));
+            break;
+        default: break;
     }
 }
 __device__ inline float epilogue_f(uint16_t b) { return static_cast<float>(__builtin_bit_cast(half_t, b)); }
+// v[0 .. N) to the outputs, in place
+template <int N>
+__device__ inline void epilogue_apply(const Epilogue& e, float (&v)[N], const EpilogueBits (&b)[N], half_t (&y)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += epilogue_f(b[i].bias);
+    epilogue_act(v, e.act);
+    if (e.mul != nullptr) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] *= epilogue_f(b[i].mul);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) y[i] = static_cast<half_t>(v[i] + epilogue_f(b[i].residual));
+}
 __device__ inline half_t epilogue_apply(const Epilogue& e, float v, const EpilogueBits& b) {
-    v = epilogue_act(v + epilogue_f(b.bias), e.act);
-    if (e.mul != nullptr) v *= epilogue_f(b.mul);
-    return static_cast<half_t>(v + epilogue_f(b.residual));
+    float vv[1] = {v};
+    const EpilogueBits bb[1] = {b};
+    half_t y[1];
+    epilogue_apply(e, vv, bb, y);
+    return y[0];
 }
 
 // The operands of element (m, n), n < N: plain loads under uniform branches.
@@ -49,6 +95,35 @@ __device__ inline EpilogueBits epilogue_load(const Epilogue& e, int64_t m, int64
     if (e.mul != nullptr) b.mul = __builtin_bit_cast(uint16_t, e.mul[m * e.mul_stride + n]);
     if (e.residual != nullptr) b.residual = __builtin_bit_cast(uint16_t, e.residual[m * e.residual_stride + n]);
     return b;
+}
+
+// The same for eight neighbouring elements of a row, (m, n) .. (m, n + 7),
+// by 16-byte accesses: only where e.vectors (N and the strides whole eights,
+// every address a multiple of 16).
+struct EpilogueRun {
+    half8_t mul, residual;
+};
+__device__ inline EpilogueRun epilogue_load8(const Epilogue& e, int64_t m, int64_t n, int M, int N) {
+    EpilogueRun r{};
+    if (m >= M || n >= N) return r;
+    if (e.mul != nullptr) r.mul = *reinterpret_cast<const half8_t*>(e.mul + m * e.mul_stride + n);
+    if (e.residual != nullptr)
+        r.residual = *reinterpret_cast<const half8_t*>(e.residual + m * e.residual_stride + n);
+    return r;
+}
+__device__ inline void epilogue_store8(const Epilogue& e, float (&v)[8], const half8_t& bias, const EpilogueRun& r,
+                                       half_t* y, int64_t m, int64_t n, int M, int N) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += static_cast<float>(bias[j]);
+    epilogue_act(v, e.act);
+    if (e.mul != nullptr) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= static_cast<float>(r.mul[j]);
+    }
+    half8_t h;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = static_cast<half_t>(v[j] + static_cast<float>(r.residual[j]));
+    if (m < M && n < N) *reinterpret_cast<half8_t*>(y + m * N + n) = h;
 }
 
 }  // namespace awq

@@ -645,9 +645,6 @@ __global__ __launch_bounds__(NT, 512 / NT) void gemm_kernel(ArgsOf<OMODE> args, 
         if (m < M && n < N) {
             if constexpr (OMODE == GemmOut::kF16) {
                 args.y16[static_cast<int64_t>(m) * N + n] = static_cast<half_t>(v);
-            } else if constexpr (OMODE == GemmOut::kFused) {
-                args.y16[static_cast<int64_t>(m) * N + n] =
-                    epilogue_apply(args.epilogue, v, epilogue_load(args.epilogue, m, n));
             } else if constexpr (OMODE == GemmOut::kF32) {
                 args.y32[ref_offset(m, n, ref_tiles_n)] = v;
             } else {
@@ -672,6 +669,76 @@ __global__ __launch_bounds__(NT, 512 / NT) void gemm_kernel(ArgsOf<OMODE> args, 
             __syncthreads();
         }
     };
+    // ---- the fused epilogue of sub-tile ij (32 x 32) ----
+    // It goes through LDS (the wave's own 4 KB of the A stages, which every
+    // wave is done with), so that a lane holds eight neighbouring outputs of
+    // a row and the operands and the result are 16-byte accesses. One element
+    // at a time, with the activation's code once per element, the epilogue
+    // took 134 us of the 328 us of 2048 x 11008 x 4096 (SiLU, mul); this one
+    // 11 of 206. Float4 chunk c of row r lies at c ^ (r % 8).
+    static_assert(2 * LDS_A * 2 >= NT / kWave * 4096, "4 KB per wave");
+    [[maybe_unused]] float* const fbuf = reinterpret_cast<float*>(&As[0][0]) + wave * 1024;
+    // (lane numbers the compiler cannot follow: it would keep the epilogue's
+    // per-lane offsets in registers across the main loop, which has none left)
+    [[maybe_unused]] auto opaque = [](int v) {
+        asm volatile("" : "+v"(v));
+        return v;
+    };
+    [[maybe_unused]] auto fused_load = [&](int tm, int tn, int ij, EpilogueRun (&r)[2]) {
+        if constexpr (OMODE == GemmOut::kFused) {
+            if (!args.epilogue.vectors) return;
+            const int ln = opaque(lane);
+#pragma unroll
+            for (int it = 0; it < 2; ++it)
+                r[it] = epilogue_load8(args.epilogue, tm + wm + ij / TN * 32 + it * 16 + (ln >> 2),
+                                       tn + wn + ij % TN * 32 + (ln & 3) * 8, M, N);
+        }
+    };
+    [[maybe_unused]] auto fused_store = [&](int tm, int tn, int ij, const float16_t& a, const EpilogueRun (&er)[2]) {
+        if constexpr (OMODE == GemmOut::kFused) {
+            const Epilogue& epi = args.epilogue;
+            const int ln = opaque(lane), fcol = ln & 31, frow4 = (ln >> 5) * 4;
+            const int m0 = tm + wm + ij / TN * 32, n0 = tn + wn + ij % TN * 32;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int r = (e >> 2) * 8 + frow4 + (e & 3);
+                fbuf[r * 32 + (((fcol >> 2) ^ (r & 7)) << 2) + (fcol & 3)] = a[e];
+            }
+            __builtin_amdgcn_wave_barrier();            // one wave's LDS accesses run in order
+            if (epi.vectors) {
+                const int n = n0 + (ln & 3) * 8;
+                half8_t bias{};
+                if (epi.bias != nullptr && n < N) bias = *reinterpret_cast<const half8_t*>(epi.bias + n);
+#pragma unroll
+                for (int it = 0; it < 2; ++it) {
+                    const int r = it * 16 + (ln >> 2), c = (ln & 3) * 2;
+                    float v[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = fbuf[r * 32 + (((c + (j >> 2)) ^ (r & 7)) << 2) + (j & 3)];
+                    epilogue_store8(epi, v, bias, er[it], args.y16, m0 + r, n, M, N);
+                }
+            } else {
+                // odd rows or addresses: a lane takes single elements of its column
+#pragma unroll 1
+                for (int it = 0; it < 4; ++it) {
+                    EpilogueBits eb[4] = {};
+                    float v[4];
+                    half_t h[4];
+                    const int r0 = it * 8 + frow4, n = n0 + fcol;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (m0 + r0 + k < M && n < N) eb[k] = epilogue_load(epi, m0 + r0 + k, n);
+                        v[k] = fbuf[(r0 + k) * 32 + (((fcol >> 2) ^ ((r0 + k) & 7)) << 2) + (fcol & 3)];
+                    }
+                    epilogue_apply(epi, v, eb, h);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (m0 + r0 + k < M && n < N) args.y16[static_cast<int64_t>(m0 + r0 + k) * N + n] = h[k];
+                }
+            }
+            __builtin_amdgcn_wave_barrier();
+        }
+    };
     auto finish_tile = [&](int tile, int tm, int tn) {
         float sq = 0.f;
         if constexpr (OMODE == GemmOut::kF16) {
@@ -682,31 +749,15 @@ __global__ __launch_bounds__(NT, 512 / NT) void gemm_kernel(ArgsOf<OMODE> args, 
 #pragma unroll
                     for (int e = 0; e < 16; ++e) emit(tm, tn, i, j, e, acc[i][j][e], sq);
         } else if constexpr (OMODE == GemmOut::kFused) {
-            // a sub-tile's operands are loaded while the one before it is
-            // finished and stored
-            EpilogueBits eb[2][16];
-            auto load = [&](int ij, EpilogueBits (&b)[16]) {
-                const int n = tn + wn + ij % TN * 32 + lcol;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int m = tm + wm + ij / TN * 32 + (e >> 2) * 8 + lrow4 + (e & 3);
-                    b[e] = EpilogueBits{0, 0, 0};
-                    if (m < M && n < N) b[e] = epilogue_load(args.epilogue, m, n);
-                }
-            };
-            load(0, eb[0]);
+            // the next sub-tile's operands are loaded ahead
+            EpilogueRun er[2][2];
+            fused_load(tm, tn, 0, er[0]);
 #pragma unroll
             for (int ij = 0; ij < TM * TN; ++ij) {
-                if (ij + 1 < TM * TN) load(ij + 1, eb[(ij + 1) & 1]);
-                const int n = tn + wn + ij % TN * 32 + lcol;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int m = tm + wm + ij / TN * 32 + (e >> 2) * 8 + lrow4 + (e & 3);
-                    if (m < M && n < N)
-                        args.y16[static_cast<int64_t>(m) * N + n] =
-                            epilogue_apply(args.epilogue, acc[ij / TN][ij % TN][e], eb[ij & 1][e]);
-                }
+                if (ij + 1 < TM * TN) fused_load(tm, tn, ij + 1, er[(ij + 1) & 1]);
+                fused_store(tm, tn, ij, acc[ij / TN][ij % TN], er[ij & 1]);
             }
+            if constexpr (STREAMK) __syncthreads();     // the next segment stages A again
         } else {
             // tiled layout: a lane's 16 values of a sub-tile are contiguous.
             // Sub-tiles that start inside [0, M) x [0, N) lie inside the
@@ -822,12 +873,47 @@ __global__ __launch_bounds__(NT, 512 / NT) void gemm_kernel(ArgsOf<OMODE> args, 
                                                 __HIP_MEMORY_SCOPE_AGENT) == b_last - b_first;
             __syncthreads();
             if (!s_flag) continue;
+            if constexpr (OMODE == GemmOut::kFused) {
+                // the parts of one sub-tile at a time, four parts in flight
+                // (parts past the last read nothing and add zero), in segment
+                // order; not unrolled, the epilogue's code is long
+#pragma unroll 1
+                for (int ij = 0; ij < TM * TN; ++ij) {
+                    EpilogueRun er[2];
+                    fused_load(tm, tn, ij, er);
+                    float16_t sum;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) sum[e] = 0.f;
+                    for (int b0 = b_first; b0 <= b_last; b0 += 4) {
+                        float4_t v[4][4];
+#pragma unroll
+                        for (int f = 0; f < 4; ++f) {
+                            const int bb = uniform(min(b0 + f, b_last));
+                            const auto rs = partial_rsrc(slot_of(bb), b0 + f <= b_last ? BM * BN * 4 : 0);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                v[f][q] = __builtin_bit_cast(float4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                                                           rs, tid * 16, (ij * 4 + q) * NT * 16, kSc1));
+                        }
+#pragma unroll
+                        for (int f = 0; f < 4; ++f)
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                                for (int r = 0; r < 4; ++r) sum[4 * q + r] += v[f][q][r];
+                    }
+                    fused_store(tm, tn, ij, sum, er);
+                }
+                __syncthreads();        // the next segment stages A again
+                if (tid == 0) __hip_atomic_store(&sk.counters[tile], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                continue;
+            }
             // Every part, this block's own included, is read back and summed
             // in segment order, eight float4 chunks (32 outputs) at a time,
             // each chunk's four outputs written as soon as they are complete.
             {
                 constexpr int kChunks = TM * TN * 4;
-                constexpr int kBatch = OMODE == GemmOut::kFused ? 4 : 8;   // fewer: the operands take registers too
+                constexpr int kBatch = 8;
                 float sq = 0.f;
 #pragma unroll
                 for (int c0 = 0; c0 < kChunks; c0 += kBatch) {
@@ -869,6 +955,10 @@ struct Geometry {
 };
 constexpr Geometry kNarrowTile{256, 128, 256, 2};
 constexpr Geometry kWideTile{256, 256, 512, 1};
+// The fused call's tile for a few hundred rows, where a layer has too few of
+// the large tiles for the GPU (see use_mid).
+constexpr Geometry kMidTile{64, 128, 256, 2};
+constexpr bool is_mid(const Geometry& g) { return g.bm == kMidTile.bm; }
 
 constexpr int kMinSteps = 8;        // K steps per block at least
 
@@ -911,8 +1001,18 @@ bool use_hybrid(const Geometry& g, int64_t tiles, int64_t steps) {
 
 int stream_k_grid(const Geometry& g, int64_t tiles, int64_t steps) {
     const int64_t total = tiles * steps;
-    int64_t gr = std::min(resident_slots(g), tiles * max_split(steps));
-    gr = std::min(gr, std::max<int64_t>(1, total / kMinSteps));
+    int64_t gr, least = kMinSteps;
+    if (is_mid(g)) {
+        // one block per CU where there are few tiles, two from a quarter of
+        // the CUs up; up to 8 segments of 4 steps and more (us, N x K, M, 256
+        // against 512 blocks: 4096 x 4096, 128, 17.5 / 19.9; 256, 27.5 /
+        // 24.3; 4096 x 11008, 128, 31.8 / 37.9; 256, 54.2 / 45.5)
+        gr = std::min<int64_t>(cu_count() * (tiles * 4 <= cu_count() ? 1 : 2), tiles * 8);
+        least = 4;
+    } else {
+        gr = std::min(resident_slots(g), tiles * max_split(steps));
+    }
+    gr = std::min(gr, std::max<int64_t>(1, total / least));
     return static_cast<int>(gr);
 }
 
@@ -957,7 +1057,7 @@ void launch_cfg(const ArgsOf<OMODE>& args, void* workspace, hipStream_t stream) 
                                static_cast<int>(tiles_n), sk);
         return;
     }
-    if constexpr (DIRECT && kHalfOut) {
+    if constexpr (DIRECT && kHalfOut && !is_mid(GEO)) {
         if (workspace != nullptr && use_hybrid(GEO, tiles, steps)) {
             sk.dp_tiles = static_cast<int>(tiles / resident_slots(GEO) * resident_slots(GEO));
             const int64_t tail = tiles - sk.dp_tiles;
@@ -1007,11 +1107,34 @@ bool use_wide(const GemmArgs& args, bool have_workspace) {
     return wide_rounds_cost(t) < narrow_rounds_cost(tiles_of(kNarrowTile, args.M, args.N));
 }
 
+// The fused call takes 64 x 128 tiles where they are at most 60 Ki K steps in
+// all (with a workspace, splitting them), or one round of the GPU (without).
+// Measured against the choice above (us, INT4, residual; with a workspace):
+// M = 203 on 1000 x 4096 16 against 52, 4096 x 4096 24 / 53, 4096 x 11008
+// 45 / 96, 11008 x 4096 48 / 57; M = 512 on 4096 x 11008 81 / 101; M = 128
+// on 8192 x 28672 105 / 165. Past it they lose: M = 768 on 11008 x 4096
+// 119 / 98, on 4096 x 11008 128 / 111. Without one: M = 512 on 4096 x 11008
+// 112 / 184, M = 768 on 11008 x 4096 120 / 99. Against the skinny kernel at
+// M = 64: 1000 x 4096 14 / 19, 11008 x 4096 22 / 29, 8192 x 28672 58 / 381
+// (without a workspace 30 / 51, 40 / 56, 273 / 379). The plain call keeps
+// its kernels and so its bits.
+bool use_mid(const GemmArgs& args, bool have_workspace) {
+    const int64_t tiles = tiles_of(kMidTile, args.M, args.N);
+    if (!have_workspace) return tiles <= resident_slots(kMidTile);
+    return tiles * (args.K / BKD) <= 60 * 1024;
+}
+
 // The loss form stays on the 256 x 128 tile: its epilogue streams an fp32
 // reference tile, which two blocks per CU overlap with each other's MFMAs
 // (the full-size scale search measured 153 ms there against 156 ms wide).
 template <GemmB BMODE, GemmOut OMODE>
 void launch_direct(const ArgsOf<OMODE>& args, void* workspace, hipStream_t stream) {
+    if constexpr (OMODE == GemmOut::kFused) {
+        if (use_mid(args, workspace != nullptr)) {
+            launch_cfg<kMidTile, BMODE, OMODE, true, kDirectWgm>(args, workspace, stream);
+            return;
+        }
+    }
     if constexpr (OMODE != GemmOut::kLoss) {
         if (use_wide(args, workspace != nullptr)) {
             launch_cfg<kWideTile, BMODE, OMODE, true, kDirectWgm>(args, workspace, stream);
@@ -1033,6 +1156,15 @@ void launch_int4(const ArgsOf<OMODE>& args, void* workspace, hipStream_t stream)
 }  // namespace
 
 int64_t gemm_tile_count(int64_t M, int64_t N) { return tiles_of(kNarrowTile, M, N); }
+
+bool gemm_fused_mid(int64_t M, int64_t N, int64_t K, int group_size, bool have_workspace) {
+    GemmArgs a;
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.group_size = group_size;
+    return K % BKD == 0 && direct_ok(a) && use_mid(a, have_workspace);
+}
 
 bool gemm_tiled_ok(int64_t K, int group_size) {
     GemmArgs a;

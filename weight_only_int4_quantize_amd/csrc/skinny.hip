@@ -366,15 +366,16 @@ __device__ __forceinline__ void skinny_body(const half_t* __restrict__ x, const 
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const int n = n_base + 16 * t + col;
+                [[maybe_unused]] half_t h[4];
+                if constexpr (kEpi) {
+                    float f[4] = {v[mb][t][0], v[mb][t][1], v[mb][t][2], v[mb][t][3]};
+                    epilogue_apply(epi, f, eb[mb & 1][t], h);
+                }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int m = 16 * mb + 4 * lg + e;
-                    if constexpr (kEpi) {
-                        if (m < M && n < N)
-                            y[static_cast<int64_t>(m) * N + n] = epilogue_apply(epi, v[mb][t][e], eb[mb & 1][t][e]);
-                    } else if (m < M && n < N) {
-                        y[static_cast<int64_t>(m) * N + n] = static_cast<half_t>(v[mb][t][e]);
-                    }
+                    if (m < M && n < N)
+                        y[static_cast<int64_t>(m) * N + n] = kEpi ? h[e] : static_cast<half_t>(v[mb][t][e]);
                 }
             }
         }
