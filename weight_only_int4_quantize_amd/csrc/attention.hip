@@ -40,10 +40,38 @@ struct Split {
     float* partials;    // per (row tile, split): [rows][D] outputs, [rows] maxima, [rows] sums
     int* counters;      // per row tile, zero between launches
 };
+// The rows of one kv head that a block has summed up, and where the other
+// blocks park their parts of them.
+struct Rows {
+    int kv_head, row0, rows;
+    int parts;              // 1: the block has all of it
+    int mine;               // this block's part
+    float* base;            // part p's floats at base + offset(p)
+    int64_t bytes;          // of the whole region
+    int* counter;
+};
 
 __device__ inline __amdgpu_buffer_rsrc_t rsrc(const void* p, uint32_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), static_cast<short>(0), static_cast<int>(bytes),
                                              0x00020000);
+}
+
+// The larger of a value and its copies half a wave and a quarter away, by the
+// wave's swaps (v_permlane32_swap, v_permlane16_swap). Elements are taken out
+// of the result as integers first: a bit cast of a vector element reads
+// element 0.
+typedef uint32_t swap_t __attribute__((ext_vector_type(2)));
+__device__ inline float larger_of(swap_t v) {
+    const uint32_t a = v[0], b = v[1];
+    return fmaxf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b));
+}
+__device__ inline float across_halves_max(float v) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    return larger_of(__builtin_amdgcn_permlane32_swap(u, u, false, false));
+}
+__device__ inline float across_quarters_max(float v) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, across_halves_max(v));
+    return larger_of(__builtin_amdgcn_permlane16_swap(u, u, false, false));
 }
 
 // The positions rows [row0, row0 + rows) of a kv head see.
@@ -77,20 +105,27 @@ __device__ inline half_t* out_row(const KvAttentionArgs& a, const KvSeq& sq, int
     return a.out + (static_cast<int64_t>(sq.row0) + token) * a.out_token + head * a.out_head;
 }
 
+typedef half_t half4_t __attribute__((ext_vector_type(4)));
+constexpr int kJoin = 4096;     // floats of the join's weights and sums: 2 splits rows
+constexpr int max_splits(int rows) { return kJoin / 2 / rows; }
+constexpr int part_floats(int rows, int dim) { return rows * (dim + 2); }
+// floats of LDS the join takes (over the outputs, which are parked by then)
+constexpr int join_floats(int rows, int threads) { return kJoin + rows + threads * 4; }
+
 // A block's rows are complete: so [ROWS][D] outputs in true units, sm and sl
 // their maxima and sums, all in LDS. With one split they are divided and
 // stored; otherwise parked, and the last of the tile's blocks to arrive adds
 // the splits in order (deterministic; nobody waits on anybody).
-template <int D, int ROWS, int NT>
-__device__ inline void finish_rows(const KvAttentionArgs& a, const KvSeq& sq, const Split& sp, int kv_head, int row0,
-                                   int rows, int tile, int split, int n_splits, int first_split, int last_split,
-                                   const float* so, int so_stride, const float* sm, const float* sl, int* s_flag) {
+template <int D, int ROWS, int NT, class Offset>
+__device__ inline void finish_rows(const KvAttentionArgs& a, const KvSeq& sq, const Rows& rw, const Offset& offset,
+                                   const float* so, int so_stride, const float* sm, const float* sl, float* scratch,
+                                   int* s_flag) {
     const int tid = threadIdx.x;
-    if (first_split >= last_split) {
+    const int kv_head = rw.kv_head, row0 = rw.row0, rows = rw.rows;
+    if (rw.parts <= 1) {
         for (int i = tid; i < rows * (D / 4); i += NT) {
             const int r = i / (D / 4), d = i % (D / 4) * 4;
             const float inv = sl[r] > 0.f ? 1.0f / sl[r] : 0.f;
-            typedef half_t half4_t __attribute__((ext_vector_type(4)));
             half4_t v;
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[j] = static_cast<half_t>(so[r * so_stride + d + j] * inv);
@@ -99,10 +134,8 @@ __device__ inline void finish_rows(const KvAttentionArgs& a, const KvSeq& sq, co
         for (int r = tid; r < rows; r += NT) store_lse(a, sq, kv_head, row0 + r, sm[r], sl[r]);
         return;
     }
-    constexpr int kFloats = ROWS * D + 2 * ROWS;
-    float* mine = sp.partials + static_cast<int64_t>(tile) * n_splits * kFloats;
-    const auto rs = rsrc(mine, static_cast<uint32_t>(n_splits) * kFloats * 4u);
-    const int base = split * kFloats * 4;
+    const auto rs = rsrc(rw.base, static_cast<uint32_t>(rw.bytes));
+    const int base = offset(rw.mine) * 4;
     for (int i = tid; i < rows * (D / 4); i += NT) {
         const int r = i / (D / 4), d = i % (D / 4) * 4;
         const float4_t v = *reinterpret_cast<const float4_t*>(so + r * so_stride + d);
@@ -118,37 +151,91 @@ __device__ inline void finish_rows(const KvAttentionArgs& a, const KvSeq& sq, co
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
     if (tid == 0)
-        *s_flag = __hip_atomic_fetch_add(&sp.counters[tile], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-                  last_split - first_split;
+        *s_flag = __hip_atomic_fetch_add(rw.counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == rw.parts - 1;
     __syncthreads();
     if (!*s_flag) return;
-    auto part = [&](int s, int word) {
-        return __builtin_bit_cast(float,
-                                  __builtin_amdgcn_raw_buffer_load_b32(rs, word * 4, s * (kFloats * 4), kSc1));
-    };
-    for (int i = tid; i < rows * (D / 4); i += NT) {
-        const int r = i / (D / 4), d = i % (D / 4) * 4;
-        float m = kNone;
-        for (int s = first_split; s <= last_split; ++s) m = fmaxf(m, part(s, ROWS * D + r));
-        float sum = 0.f;
-        float4_t o = {0.f, 0.f, 0.f, 0.f};
-        for (int s = first_split; s <= last_split; ++s) {
-            const float w = __builtin_amdgcn_exp2f(part(s, ROWS * D + r) - m);
-            sum += w * part(s, ROWS * D + ROWS + r);
-            const float4_t v = __builtin_bit_cast(
-                float4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, (r * D + d) * 4, s * (kFloats * 4), kSc1));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[j] += w * v[j];
+    // ---- the last block: every split's maxima and sums first (all at once),
+    // from them the splits' weights, then the outputs, eight splits' loads in
+    // flight and the splits shared out over the threads there are beyond one
+    // per four outputs. One split after the other, a join of 64 splits took
+    // 60 us of a 110 us call (2 x 131072 tokens, 8 heads of 128).
+    const int n = rw.parts;
+    float* wt = scratch;                    // [n][ROWS] maxima, then weights
+    float* ls = scratch + kJoin / 2;        // [n][ROWS] sums
+    for (int i = tid; i < n * ROWS; i += NT) {
+        const int s = i / ROWS, r = i % ROWS;
+        if (r < rows) {
+            // (per-lane split: a vector offset)
+            const int at = (offset(s) + ROWS * D + r) * 4;
+            wt[i] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, at, 0, kSc1));
+            ls[i] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, at + ROWS * 4, 0, kSc1));
         }
-        const float inv = sum > 0.f ? 1.0f / sum : 0.f;
-        typedef half_t half4_t __attribute__((ext_vector_type(4)));
-        half4_t h;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) h[j] = static_cast<half_t>(o[j] * inv);
-        *reinterpret_cast<half4_t*>(out_row(a, sq, kv_head, row0 + r) + d) = h;
-        if (d == 0) store_lse(a, sq, kv_head, row0 + r, m, sum);
     }
-    if (tid == 0) __hip_atomic_store(&sp.counters[tile], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    constexpr int TPR = NT / ROWS;          // threads per row
+    const int jr = tid / TPR, jl = tid % TPR;
+    float jm = kNone, jsum = 0.f;
+    if (jr < rows)
+        for (int s = jl; s < n; s += TPR) jm = fmaxf(jm, wt[s * ROWS + jr]);
+#pragma unroll
+    for (int o = 1; o < TPR; o <<= 1) jm = fmaxf(jm, __shfl_xor(jm, o));
+    if (jr < rows)
+        for (int s = jl; s < n; s += TPR) {
+            const float w = __builtin_amdgcn_exp2f(wt[s * ROWS + jr] - jm);
+            wt[s * ROWS + jr] = w;
+            jsum += w * ls[s * ROWS + jr];
+        }
+#pragma unroll
+    for (int o = 1; o < TPR; o <<= 1) jsum += __shfl_xor(jsum, o);
+    float* total = scratch + kJoin;         // [ROWS] 1 / sum
+    if (jr < rows && jl == 0) {
+        total[jr] = jsum > 0.f ? 1.0f / jsum : 0.f;
+        store_lse(a, sq, kv_head, row0 + jr, jm, jsum);
+    }
+    __syncthreads();
+    const int items = rows * (D / 4);
+    const int groups = items < NT ? NT / items : 1;
+    float4_t* red = reinterpret_cast<float4_t*>(total + ROWS);      // [groups][items], groups > 1
+    for (int i0 = 0; i0 < items; i0 += NT) {
+        const int i = groups > 1 ? tid % items : i0 + tid;
+        const int g = groups > 1 ? tid / items : 0;
+        const bool mine = i < items && g < groups;
+        const int r = mine ? i / (D / 4) : 0, d = mine ? i % (D / 4) * 4 : 0;
+        float4_t o = {0.f, 0.f, 0.f, 0.f};
+        for (int s0 = mine ? g : n; s0 < n; s0 += 8 * groups) {
+            float4_t v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int s = min(s0 + k * groups, n - 1);
+                v[k] = __builtin_bit_cast(
+                    float4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, (offset(s) + r * D + d) * 4, 0, kSc1));
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float w = s0 + k * groups < n ? wt[(s0 + k * groups) * ROWS + r] : 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[j] += w * v[k][j];
+            }
+        }
+        if (groups > 1) {
+            if (mine) red[tid] = o;
+            __syncthreads();
+            if (g == 0)
+                for (int k = 1; k < groups; ++k) {
+                    const float4_t v = red[k * items + i];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[j] += v[j];
+                }
+        }
+        if (mine && g == 0) {
+            const float inv = total[r];
+            half4_t h;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[j] = static_cast<half_t>(o[j] * inv);
+            *reinterpret_cast<half4_t*>(out_row(a, sq, kv_head, row0 + r) + d) = h;
+        }
+    }
+    if (tid == 0) __hip_atomic_store(rw.counter, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 // ---------------------------------------------------------------- few rows
@@ -167,13 +254,17 @@ constexpr int kTile = 64;
 
 // NP: pages a 64-token tile spans (2 for pages of 32, else 1)
 template <int D, int FORMAT, int NP>
-__global__ __launch_bounds__(kDecodeWaves* kWave) void kv_decode_kernel(KvAttentionArgs a, Split sp, int n_splits) {
+__global__ __launch_bounds__(kDecodeWaves* kWave, D <= 64 ? 4 : D <= 96 ? 3 : D <= 192 ? 2 : 1) void kv_decode_kernel(
+    KvAttentionArgs a, Split sp, int n_splits) {
     constexpr int DC = D / 16;              // channel pieces of a key
     constexpr int KC = (DC + 3) / 4;        // of them per lane
     constexpr int DT = D / 16;              // 16-channel tiles of the output
     constexpr int NT = kDecodeWaves * kWave;
     constexpr int SO = D + 4;
-    __shared__ __attribute__((aligned(16))) float so[kDecodeWaves][kDecodeRows][SO];
+    constexpr int kFloats = part_floats(kDecodeRows, D);
+    __shared__ __attribute__((aligned(16))) float so_all[std::max(kDecodeWaves * kDecodeRows * SO,
+                                                                 join_floats(kDecodeRows, NT))];
+    float(*so)[kDecodeRows][SO] = reinterpret_cast<float(*)[kDecodeRows][SO]>(so_all);
     __shared__ float sm[kDecodeWaves][kDecodeRows], sl[kDecodeWaves][kDecodeRows];
     __shared__ int s_flag;
 
@@ -186,7 +277,7 @@ __global__ __launch_bounds__(kDecodeWaves* kWave) void kv_decode_kernel(KvAttent
     const int b = blockIdx.z;
     const int kv_head = blockIdx.y % c.heads;
     const int row0 = blockIdx.y / c.heads * kDecodeRows;
-    const KvSeq sq = kv_seq(c, b);
+    const KvSeq sq = kv_seq_shared(c, b);
     const int all_rows = sq.n * a.ratio;
     if (row0 >= all_rows) return;
     const int rows = min(kDecodeRows, all_rows - row0);
@@ -195,6 +286,10 @@ __global__ __launch_bounds__(kDecodeWaves* kWave) void kv_decode_kernel(KvAttent
     const int first_split = span.begin < span.end ? span.begin / sp.tokens : 0;
     const int last_split = span.begin < span.end ? (span.end - 1) / sp.tokens : 0;
     if (split < first_split || split > last_split) return;
+    const int page_mask = (1 << c.log2_page) - 1;
+    const int64_t page_bytes = static_cast<int64_t>(D) << c.log2_page;
+    const int from = max(span.begin, split * sp.tokens) / kTile;
+    const int to = (min(static_cast<int64_t>(span.end), (static_cast<int64_t>(split) + 1) * sp.tokens) + kTile - 1) / kTile;
 
     // ---- queries: k-slots of step 2 i + h are channels 16 (quarter + 4 i) + 8 h .. + 7 ----
     const int row = row0 + col;
@@ -220,111 +315,143 @@ __global__ __launch_bounds__(kDecodeWaves* kWave) void kv_decode_kernel(KvAttent
 #pragma unroll
     for (int t = 0; t < DT; ++t) acc[t] = float4_t{0.f, 0.f, 0.f, 0.f};
 
-    const int page_mask = (1 << c.log2_page) - 1;
-    const int64_t page_bytes = static_cast<int64_t>(D) << c.log2_page;
-    const int from = max(span.begin, split * sp.tokens) / kTile;
-    const int to = (min(static_cast<int64_t>(span.end), (static_cast<int64_t>(split) + 1) * sp.tokens) + kTile - 1) / kTile;
-    for (int tile = from + wave; tile < to; tile += kDecodeWaves) {
-        const int tb = tile * kTile;
-        // ---- this tile's pages ----
+    // The pages of a tile: one or two, by scalar loads. A page past the
+    // sequence's end counts as not held, whatever its entry.
+    struct Pages {
         int64_t block[NP];
         bool held[NP];
-        float ks[NP], vs[NP];
+    };
+    auto pages_of = [&](int tile) {
+        Pages g;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            const int p = (tb >> c.log2_page) + i;
-            // a page past the sequence's end counts as not held, whatever its entry
-            const int id = (p << c.log2_page) < sq.len ? kv_page(c, b, p) : -1;
-            held[i] = id >= 0;
-            block[i] = static_cast<int64_t>(max(id, 0)) * c.heads + kv_head;
-            ks[i] = held[i] ? c.k_scales[block[i]] : 0.f;
-            vs[i] = held[i] ? fmaxf(c.v_scales[block[i]], kTinyScale) : kTinyScale;
+            const int p = (tile * kTile >> c.log2_page) + i;
+            const int id = (p << c.log2_page) < sq.len ? kv_page_shared(c, b, p) : -1;
+            g.held[i] = id >= 0;
+            g.block[i] = static_cast<int64_t>(max(id, 0)) * c.heads + kv_head;
         }
-        const int kp = NP == 2 ? col >> 3 : 0, vp = NP == 2 ? quarter >> 1 : 0;
-        const uint8_t* kbase = c.k_codes + (kp ? block[NP - 1] : block[0]) * page_bytes;
-        const uint8_t* vbase = c.v_codes + (vp ? block[NP - 1] : block[0]) * page_bytes;
-        const int slot0 = NP == 2 ? 16 * ((col >> 2) & 1) + (col & 3) : (tb & page_mask) + 16 * (col >> 2) + (col & 3);
-        const int piece0 = NP == 2 ? quarter & 1 : ((tb & page_mask) >> 4) + quarter;
-        kv_u32x4 kr[4][KC], vr[DT];
+        return g;
+    };
+    kv_u32x4 kr[4][KC], vr[DT];
+    auto load_k = [&](int tile, const Pages& g) {
+        const int slot = tile * kTile & page_mask;
+        const uint8_t* base = c.k_codes + (NP == 2 && (col >> 3) ? g.block[NP - 1] : g.block[0]) * page_bytes;
+        const int slot0 = NP == 2 ? 16 * ((col >> 2) & 1) + (col & 3) : slot + 16 * (col >> 2) + (col & 3);
 #pragma unroll
         for (int s4 = 0; s4 < 4; ++s4)
 #pragma unroll
             for (int i = 0; i < KC; ++i) {
                 const int piece = min(quarter + 4 * i, DC - 1);     // past D: the queries' slots are 0
-                kr[s4][i] = *reinterpret_cast<const kv_u32x4*>(
-                    kbase + ((piece << c.log2_page) + slot0 + 4 * s4) * 16);
+                kr[s4][i] = *reinterpret_cast<const kv_u32x4*>(base + ((piece << c.log2_page) + slot0 + 4 * s4) * 16);
             }
+    };
+    auto load_v = [&](int tile, const Pages& g) {
+        const int slot = tile * kTile & page_mask;
+        const uint8_t* base = c.v_codes + (NP == 2 && (quarter >> 1) ? g.block[NP - 1] : g.block[0]) * page_bytes;
+        const int piece0 = NP == 2 ? quarter & 1 : (slot >> 4) + quarter;
 #pragma unroll
         for (int t = 0; t < DT; ++t)
-            vr[t] = *reinterpret_cast<const kv_u32x4*>(vbase + (piece0 * D + 16 * t + col) * 16);
+            vr[t] = *reinterpret_cast<const kv_u32x4*>(base + (piece0 * D + 16 * t + col) * 16);
+    };
 
-        // ---- logits ----
-        float s[16];
-        const float kscale = (NP == 2 && quarter >= 2 ? ks[NP - 1] : ks[0]) * a.scale_log2;
+    // A tile's keys are in flight while the one before it is in its softmax
+    // and second product, its values from the end of that product on; the
+    // registers are those the tile before has just given up. The last tile's
+    // wave asks for its own again (from the cache).
+    int tile = from + wave;
+    if (tile < to) {
+        Pages now = pages_of(tile);
+        load_k(tile, now);
+        load_v(tile, now);
+        for (; tile < to; tile += kDecodeWaves) {
+            const int tb = tile * kTile;
+            const int next = tile + kDecodeWaves < to ? tile + kDecodeWaves : tile;
+            const Pages then = pages_of(next);
+            float ks[NP], vs[NP];
 #pragma unroll
-        for (int s4 = 0; s4 < 4; ++s4) {
-            float4_t x = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < KC; ++i) {
-                x = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv_unpack8<FORMAT>(kr[s4][i][0], kr[s4][i][1]), qf[2 * i], x,
-                                                           0, 0, 0);
-                x = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv_unpack8<FORMAT>(kr[s4][i][2], kr[s4][i][3]),
-                                                           qf[2 * i + 1], x, 0, 0, 0);
+            for (int i = 0; i < NP; ++i) {
+                ks[i] = now.held[i] ? kv_shared_load(c.k_scales + now.block[i]) : 0.f;
+                vs[i] = now.held[i] ? fmaxf(kv_shared_load(c.v_scales + now.block[i]), kTinyScale) : kTinyScale;
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[4 * s4 + e] = x[e] * kscale;
-        }
-        bool whole = tb >= span.all_begin && tb + kTile <= span.all_end;
-#pragma unroll
-        for (int i = 0; i < NP; ++i) whole = whole && held[i];
-        if (!whole) {
-            const bool ok = NP == 2 && quarter >= 2 ? held[NP - 1] : held[0];
-            const int j0 = tb + 16 * quarter;
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                s[i] = ok && j0 + i >= lo && j0 + i < hi ? s[i] : -__builtin_huge_valf();
-            // bytes past the sequence's end may be anything, fp8 NaN among them
-            const int n = ok ? min(max(sq.len - j0, 0), 16) : 0;
-            kv_u32x4 keep;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int k = min(max(n - 4 * j, 0), 4);
-                keep[j] = k == 4 ? 0xFFFFFFFFu : (1u << (8 * k)) - 1u;
-            }
-#pragma unroll
-            for (int t = 0; t < DT; ++t) vr[t] &= keep;
-        }
 
-        // ---- softmax ----
-        float top = s[0];
+            // ---- logits ----
+            float s[16];
+            const float kscale = (NP == 2 && quarter >= 2 ? ks[NP - 1] : ks[0]) * a.scale_log2;
 #pragma unroll
-        for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float mn = fmaxf(m, top);
-        const float unit_new = fmaxf(unit, NP == 2 ? fmaxf(vs[0], vs[NP - 1]) : vs[0]);
-        const float unit_inv = __builtin_amdgcn_rcpf(unit_new);
-        const float shrink = __builtin_amdgcn_exp2f(m - mn);
-        const float vscale = (NP == 2 && quarter >= 2 ? vs[NP - 1] : vs[0]) * unit_inv * kWeightUnit;
-        const float carry = shrink * (unit * unit_inv);
-        sum *= shrink;
-        half8_t pf[2];
+            for (int s4 = 0; s4 < 4; ++s4) {
+                float4_t x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float p = __builtin_amdgcn_exp2f(s[i] - mn);
-            sum += p;
-            pf[i >> 3][i & 7] = static_cast<half_t>(p * vscale);
-        }
-        m = mn;
-        unit = unit_new;
+                for (int i = 0; i < KC; ++i) {
+                    x = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv_unpack8<FORMAT>(kr[s4][i][0], kr[s4][i][1]),
+                                                               qf[2 * i], x, 0, 0, 0);
+                    x = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv_unpack8<FORMAT>(kr[s4][i][2], kr[s4][i][3]),
+                                                               qf[2 * i + 1], x, 0, 0, 0);
+                }
 #pragma unroll
-        for (int t = 0; t < DT; ++t) {
+                for (int e = 0; e < 4; ++e) s[4 * s4 + e] = x[e] * kscale;
+            }
+            load_k(next, then);
+            __builtin_amdgcn_sched_barrier(0);
+            bool whole = tb >= span.all_begin && tb + kTile <= span.all_end;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[t][e] *= carry;
-            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv_unpack8<FORMAT>(vr[t][0], vr[t][1]), pf[0], acc[t], 0, 0,
-                                                            0);
-            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv_unpack8<FORMAT>(vr[t][2], vr[t][3]), pf[1], acc[t], 0, 0,
-                                                            0);
+            for (int i = 0; i < NP; ++i) whole = whole && now.held[i];
+            if (!whole) {
+                const bool ok = NP == 2 && quarter >= 2 ? now.held[NP - 1] : now.held[0];
+                const int j0 = tb + 16 * quarter;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    s[i] = ok && j0 + i >= lo && j0 + i < hi ? s[i] : -__builtin_huge_valf();
+                // bytes past the sequence's end may be anything, fp8 NaN among them
+                const int n = ok ? min(max(sq.len - j0, 0), 16) : 0;
+                kv_u32x4 keep;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int k = min(max(n - 4 * j, 0), 4);
+                    keep[j] = k == 4 ? 0xFFFFFFFFu : (1u << (8 * k)) - 1u;
+                }
+#pragma unroll
+                for (int t = 0; t < DT; ++t) vr[t] &= keep;
+            }
+
+            // ---- softmax ----
+            float top = s[0];
+#pragma unroll
+            for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+            top = across_quarters_max(top);
+            const float mn = fmaxf(m, top);
+            const float unit_new = fmaxf(unit, NP == 2 ? fmaxf(vs[0], vs[NP - 1]) : vs[0]);
+            const float unit_inv = __builtin_amdgcn_rcpf(unit_new);
+            const float shrink = __builtin_amdgcn_exp2f(m - mn);
+            const float vscale = (NP == 2 && quarter >= 2 ? vs[NP - 1] : vs[0]) * unit_inv * kWeightUnit;
+            const float carry = shrink * (unit * unit_inv);
+            // A weight goes into the second product as two fp16 numbers, its
+            // rounding and what that left: the product's matrix time is free
+            // here, and the rounding of one would add as much error as the
+            // output's own.
+            half8_t pf[2], pl[2];
+            sum *= shrink;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float p = __builtin_amdgcn_exp2f(s[i] - mn), w = p * vscale;
+                sum += p;
+                pf[i >> 3][i & 7] = static_cast<half_t>(w);
+                pl[i >> 3][i & 7] = static_cast<half_t>(w - static_cast<float>(pf[i >> 3][i & 7]));
+            }
+            m = mn;
+            unit = unit_new;
+#pragma unroll
+            for (int t = 0; t < DT; ++t) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[t][e] *= carry;
+                const half8_t v0 = kv_unpack8<FORMAT>(vr[t][0], vr[t][1]), v1 = kv_unpack8<FORMAT>(vr[t][2], vr[t][3]);
+                acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pf[0], acc[t], 0, 0, 0);
+                acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pf[1], acc[t], 0, 0, 0);
+                acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pl[0], acc[t], 0, 0, 0);
+                acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pl[1], acc[t], 0, 0, 0);
+            }
+            load_v(next, then);
+            __builtin_amdgcn_sched_barrier(0);
+            now = then;
         }
     }
 
@@ -361,9 +488,12 @@ __global__ __launch_bounds__(kDecodeWaves* kWave) void kv_decode_kernel(KvAttent
         sl[0][tid] = ll;
     }
     __syncthreads();
-    const int tile_id = b * static_cast<int>(gridDim.y) + static_cast<int>(blockIdx.y);
-    finish_rows<D, kDecodeRows, NT>(a, sq, sp, kv_head, row0, rows, tile_id, split, n_splits, first_split, last_split,
-                                    &so[0][0][0], SO, &sm[0][0], &sl[0][0], &s_flag);
+    const int64_t tile_id = static_cast<int64_t>(b) * gridDim.y + blockIdx.y;
+    const Rows rw{kv_head, row0, rows, last_split - first_split + 1, split - first_split,
+                  sp.partials + tile_id * n_splits * kFloats, static_cast<int64_t>(n_splits) * kFloats * 4,
+                  sp.counters + tile_id};
+    finish_rows<D, kDecodeRows, NT>(a, sq, rw, [&](int p) { return (first_split + p) * kFloats; }, so_all, SO, &sm[0][0],
+                                    &sl[0][0], so_all, &s_flag);
 }
 
 // ---------------------------------------------------------------- many rows
@@ -414,7 +544,7 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv_pre
     // the last rows of a causal chunk see the most: first
     const int row_tile = row_tiles - 1 - blockIdx.x / n_splits;
     const int row0 = row_tile * kPrefillRows;
-    const KvSeq sq = kv_seq(c, b);
+    const KvSeq sq = kv_seq_shared(c, b);
     const int all_rows = sq.n * a.ratio;
     if (row0 >= all_rows) return;
     const int rows = min(kPrefillRows, all_rows - row0);
@@ -457,11 +587,11 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv_pre
         for (int i = 0; i < NP; ++i) {
             const int p = (tb >> c.log2_page) + i;
             // a page past the sequence's end counts as not held, whatever its entry
-            const int id = (p << c.log2_page) < sq.len ? kv_page(c, b, p) : -1;
+            const int id = (p << c.log2_page) < sq.len ? kv_page_shared(c, b, p) : -1;
             pg.held[i] = id >= 0;
             block[i] = static_cast<int64_t>(max(id, 0)) * c.heads + kv_head;
-            pg.ks[i] = pg.held[i] ? c.k_scales[block[i]] : 0.f;
-            pg.vs[i] = pg.held[i] ? fmaxf(c.v_scales[block[i]], kTinyScale) : kTinyScale;
+            pg.ks[i] = pg.held[i] ? kv_shared_load(c.k_scales + block[i]) : 0.f;
+            pg.vs[i] = pg.held[i] ? fmaxf(kv_shared_load(c.v_scales + block[i]), kTinyScale) : kTinyScale;
         }
         const int slot0 = NP == 2 ? 0 : tb & page_mask;
 #pragma unroll
@@ -547,7 +677,7 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv_pre
         for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int e = 0; e < 16; ++e) top = fmaxf(top, s[u][e]);
-        top = fmaxf(top, __shfl_xor(top, 32));
+        top = across_halves_max(top);
         const float mn = fmaxf(m, top);
         const float unit_new = fmaxf(unit, NP == 2 ? fmaxf(pg.vs[0], pg.vs[NP - 1]) : pg.vs[0]);
         const float unit_inv = __builtin_amdgcn_rcpf(unit_new);
@@ -614,9 +744,14 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv_pre
         sl[wrow] = sum;
     }
     __syncthreads();
-    const int tile_id = (b * c.heads + kv_head) * row_tiles + row_tile;
-    finish_rows<D, kPrefillRows, NT>(a, sq, sp, kv_head, row0, rows, tile_id, split, n_splits, first_split, last_split,
-                                     so, SO, sm, sl, &s_flag);
+    const int64_t tile_id = (static_cast<int64_t>(b) * c.heads + kv_head) * row_tiles + row_tile;
+    constexpr int kFloats = part_floats(kPrefillRows, D);
+    const Rows rw{kv_head, row0, rows, last_split - first_split + 1, split - first_split,
+                  sp.partials + tile_id * n_splits * kFloats, static_cast<int64_t>(n_splits) * kFloats * 4,
+                  sp.counters + tile_id};
+    finish_rows<D, kPrefillRows, NT>(a, sq, rw, [&](int p) { return (first_split + p) * kFloats; }, so, SO, sm, sl, so,
+                                     &s_flag);
+    static_assert(kBytes >= join_floats(kPrefillRows, NT) * 4, "room for the join");
 }
 
 // ---------------------------------------------------------------- launch
@@ -628,37 +763,49 @@ constexpr size_t kCounterBytes = kCounters * sizeof(int);
 
 struct Plan {
     bool decode;
-    int rows;               // query rows per block
     int64_t row_tiles;      // per sequence and kv head
     int splits;
     int tokens;             // positions per split
 };
 
-// Few query rows per kv head: the decode kernel. The keys are split until the
-// blocks fill the GPU a few times over, each split at least one tile per wave.
+// Up to 32 query rows per kv head go to the decode kernel, longer runs to the
+// prefill kernel. The keys are split until the blocks fill the GPU: two
+// blocks per CU (what the decode kernel's registers allow at 128 channels) of
+// at least 1024 positions, which cover what a block costs apart from its
+// tiles (some 8 us: its first loads, and the join); short launches of under a
+// block per CU split down to 256 positions, a tile per wave. Measured (us):
+// 16 x 4096 tokens, 4 heads of 256: 23 at 1024 positions, 33 at 512, 45 at
+// 256; 1 x 131072, 8 heads of 128: 54 at 2048, 62 at 1024; 1 x 1000, 32
+// heads: 10.1 at 256, 11.0 whole. Dealing the tiles of all sequences out
+// evenly to 512 blocks instead, which a ragged batch would ask for, was
+// slower on every shape (64 x 8192 to 2048: 145 against 134), as a block then
+// pays for two or more pieces.
 Plan plan_for(int n_seqs, int kv_heads, int ratio, int64_t max_tokens, int64_t max_len, bool have_workspace) {
     Plan p;
     const int64_t rows = max_tokens * ratio;
     p.decode = rows <= 2 * kDecodeRows;
-    p.rows = p.decode ? kDecodeRows : kPrefillRows;
-    p.row_tiles = ceil_div(rows, p.rows);
+    const int per_block = p.decode ? kDecodeRows : kPrefillRows;
+    p.row_tiles = ceil_div(rows, per_block);
     const int64_t tiles = p.row_tiles * n_seqs * kv_heads;
-    const int64_t unit = p.decode ? kTile * kDecodeWaves : kTile * 8;
-    const int64_t units = std::max<int64_t>(1, ceil_div(max_len, unit));
-    int64_t splits = 1;
+    const int64_t most = max_splits(per_block), cu = cu_count();
+    int64_t splits = 1, unit = p.decode ? 1024 : kTile * 8;
     if (have_workspace && tiles <= kCounters) {
-        const int64_t want = static_cast<int64_t>(p.decode ? 4 : 2) * cu_count();
-        splits = std::max<int64_t>(1, std::min(units, want / tiles));
+        splits = std::min({ceil_div(max_len, unit), 2 * cu / tiles, most});
+        if (p.decode && splits * tiles < cu) {
+            unit = kTile * kDecodeWaves;
+            splits = std::min({ceil_div(max_len, unit), cu / tiles, most});
+        }
+        splits = std::max<int64_t>(1, splits);
     }
-    const int64_t per = ceil_div(units, splits);
-    p.tokens = static_cast<int>(std::min<int64_t>(per * unit, INT32_MAX / kTile * kTile));
+    const int64_t units = std::max<int64_t>(1, ceil_div(max_len, unit));
+    p.tokens = static_cast<int>(std::min<int64_t>(ceil_div(units, splits) * unit, INT32_MAX / 1024 * 1024));
     p.splits = static_cast<int>(std::max<int64_t>(1, ceil_div(max_len, p.tokens)));
     return p;
 }
 
 size_t plan_bytes(const Plan& p, int n_seqs, int kv_heads, int head_dim) {
     const size_t tiles = static_cast<size_t>(p.row_tiles) * n_seqs * kv_heads;
-    const size_t floats = static_cast<size_t>(p.rows) * (head_dim + 2);
+    const size_t floats = part_floats(p.decode ? kDecodeRows : kPrefillRows, head_dim);
     return kCounterBytes + (p.splits > 1 ? tiles * p.splits * floats * sizeof(float) : 0);
 }
 
@@ -696,7 +843,7 @@ size_t kv_attention_workspace_bytes(int n_seqs, int kv_heads, int ratio, int hea
 
 awq_status launch_kv_attention(const KvAttentionArgs& a, void* workspace, hipStream_t stream) {
     const Plan p = plan_for(a.n_seqs, a.c.heads, a.ratio, a.max_tokens, a.c.max_len, workspace != nullptr);
-    if (p.row_tiles * p.splits >= (int64_t{1} << 31) || p.row_tiles * a.c.heads > (p.decode ? 65535 : INT64_MAX))
+    if (p.row_tiles * p.splits >= (int64_t{1} << 31) || (p.decode && p.row_tiles * a.c.heads > 65535))
         return AWQ_ERR_SHAPE;
     Split sp;
     sp.tokens = p.tokens;

@@ -45,9 +45,37 @@ __device__ inline KvSeq kv_seq(const KvPages& c, int b) {
     return s;
 }
 
+// A load that the whole wave shares, through the scalar cache: it neither
+// waits for the vector loads in flight nor makes them wait. Only for tensors
+// no kernel of this launch writes.
+template <typename T>
+__device__ inline T kv_shared_load(const T* p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    return *(const __attribute__((address_space(4))) T*)(uintptr_t)p;
+#else
+    return *p;
+#endif
+}
+
 // Page number p of sequence b, or -1 when the cache does not hold it.
 __device__ inline int kv_page(const KvPages& c, int b, int p) {
     const int id = c.table[static_cast<int64_t>(b) * c.table_stride + p];
+    return id >= 0 && id < c.n_pages ? id : -1;
+}
+
+// kv_seq and kv_page for wave-uniform arguments (attention only: the write
+// changes what it would read)
+__device__ inline KvSeq kv_seq_shared(const KvPages& c, int b) {
+    KvSeq s;
+    s.row0 = min(max(kv_shared_load(c.cu + b), 0), c.n_tokens);
+    s.n = min(max(kv_shared_load(c.cu + b + 1), s.row0), c.n_tokens) - s.row0;
+    const int64_t held = static_cast<int64_t>(c.max_pages) << c.log2_page;
+    s.len = min(max(kv_shared_load(c.len + b), 0), static_cast<int>(held < c.max_len ? held : c.max_len));
+    s.start = s.len - s.n;
+    return s;
+}
+__device__ inline int kv_page_shared(const KvPages& c, int b, int p) {
+    const int id = kv_shared_load(c.table + static_cast<int64_t>(b) * c.table_stride + p);
     return id >= 0 && id < c.n_pages ? id : -1;
 }
 
