@@ -636,6 +636,24 @@ def awq_gemm_fused(x, qweight, scales, zeros, group_size: int = 128, bias=None, 
     bias fp16 [N]; mul and residual fp16 [M, N], rows any stride apart;
     activation one of ACTIVATIONS. out may be residual or mul itself (when
     packed). workspace: gemm_workspace(M, N, K)."""
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
+    ext, entry, *_ = _fast or _fast_calls()
+    if ext is not None:
+        try:
+            index = x.get_device()
+            y = x.new_empty((x.shape[0], qweight.shape[0])) if out is None else out
+            stream = _stream_on(index)
+        except (AttributeError, IndexError, TypeError, ValueError):
+            stream = None
+        if stream is not None:
+            st = ext.gemm_fused(entry, stream, index, x, qweight, scales, zeros, group_size, bias, act, mul, residual,
+                                path, y, workspace)
+            if st == AWQ_OK:
+                return y
+            if st is not None:
+                _check("awq_gemm_fused", st)
     torch = _torch()
     half = torch.float16
     try:
@@ -652,9 +670,6 @@ def awq_gemm_fused(x, qweight, scales, zeros, group_size: int = 128, bias=None, 
     bits = 4 if words * 8 == K else 8
     if words * 32 != K * bits:
         raise ValueError(f"qweight has {words} words per row, K={K} needs {K // 8} (INT4) or {K // 4} (W8)")
-    act = ACTIVATIONS.get(activation)
-    if act is None:
-        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
     bias_p = None
     if bias is not None:
         _need_on("bias", bias, half, index)
@@ -777,6 +792,36 @@ def _torch_calls():
     return _torch_c
 
 
+_fast = None           # (extension or None, addresses of the library's entry points)
+
+
+def _fast_calls():
+    """The call extension (csrc/calls.cpp) and the entry points it calls; the
+    wrappers below marshal in Python where it has not been built."""
+    global _fast
+    _torch()
+    entries = {n: ctypes.cast(getattr(load(), "awq_" + n), ctypes.c_void_p).value
+               for n in ("gemm_fused", "kv_write", "kv_read", "kv_attention")}
+    ext = None
+    path = os.path.join(HERE, "_calls.so")
+    if os.path.exists(path):
+        import importlib.machinery
+        import importlib.util
+        loader = importlib.machinery.ExtensionFileLoader("_calls", path)
+        ext = importlib.util.module_from_spec(importlib.util.spec_from_loader("_calls", loader))
+        loader.exec_module(ext)
+    _fast = (ext, *entries.values())
+    return _fast
+
+
+def _stream_on(index) -> int | None:
+    """The current stream of GPU `index` if that is the current device, else None."""
+    if index < 0:       # a CPU tensor
+        return None
+    current, raw = _torch_c or _torch_calls()
+    return raw(index) if current() == index else None
+
+
 def _on_device(index: int, fn, *args) -> int:
     """fn(*args, stream) with GPU `index` current, on its current stream."""
     current, raw = _torch_c or _torch_calls()
@@ -826,6 +871,14 @@ def awq_kv_write(cache: KVCache, seqs: KVSeqs, k, v) -> None:
     """awq_kv_write: quantizes the batch's new tokens k, v (fp16 [T, heads, D],
     any token and head strides that are multiples of 8) into the cache."""
     _need_seqs(cache, seqs)
+    ext, _, entry, *_ = _fast or _fast_calls()
+    stream = _stream_on(cache.index) if ext is not None else None
+    if stream is not None:
+        st = ext.kv_write(entry, stream, cache.index, cache._ref, seqs._ref, cache.n_kv_heads, cache.head_dim, k, v)
+        if st == AWQ_OK:
+            return
+        if st is not None:
+            _check("awq_kv_write", st)
     T, _, k_token, k_head = _tokens("k", k, cache, cache.n_kv_heads)
     T2, _, v_token, v_head = _tokens("v", v, cache, cache.n_kv_heads)
     if T2 != T:
@@ -848,6 +901,14 @@ def awq_kv_read(cache: KVCache, seqs: KVSeqs, n_tokens: int | None = None, out=N
         out = tuple(torch.zeros((T, cache.n_kv_heads, cache.head_dim), dtype=torch.float16, device=cache.device)
                     for _ in range(2))
     k, v = out
+    ext, _, _, entry, _ = _fast or _fast_calls()
+    stream = _stream_on(cache.index) if ext is not None and n_tokens is None else None
+    if stream is not None:
+        st = ext.kv_read(entry, stream, cache.index, cache._ref, seqs._ref, cache.n_kv_heads, cache.head_dim, k, v)
+        if st == AWQ_OK:
+            return k, v
+        if st is not None:
+            _check("awq_kv_read", st)
     T = None
     for name, t in (("k", k), ("v", v)):
         if t is None:
@@ -892,6 +953,17 @@ def awq_kv_attention(q, cache: KVCache, seqs: KVSeqs, scale: float | None = None
     sequence are 0."""
     torch = _torch()
     _need_seqs(cache, seqs)
+    if scale is None:
+        scale = cache.head_dim ** -0.5
+    ext, *_, entry = _fast or _fast_calls()
+    stream = _stream_on(cache.index) if ext is not None and out is not None else None
+    if stream is not None:
+        st = ext.kv_attention(entry, stream, cache.index, cache._ref, seqs._ref, cache.head_dim, q, scale, causal,
+                              window, out, lse, workspace)
+        if st == AWQ_OK:
+            return out
+        if st is not None:
+            _check("awq_kv_attention", st)
     T, heads, q_token, q_head = _tokens("q", q, cache, None)
     if out is None:
         out = torch.zeros((T, heads, cache.head_dim), dtype=torch.float16, device=q.device)
@@ -904,7 +976,7 @@ def awq_kv_attention(q, cache: KVCache, seqs: KVSeqs, scale: float | None = None
             raise ValueError(f"lse must be [{T}, {heads}] on {q.device}")
     ws, nbytes = _workspace(workspace, cache.index)
     st = _on_device(cache.index, (_lib or load()).awq_kv_attention, cache._ref, seqs._ref, q.data_ptr(), q_token, q_head,
-                    T, heads, cache.head_dim ** -0.5 if scale is None else scale, 1 if causal else 0, window,
+                    T, heads, scale, 1 if causal else 0, window,
                     out.data_ptr(), out_token, out_head, _ptr(lse), ws, nbytes)
     if st != AWQ_OK:
         _check("awq_kv_attention", st)

@@ -1,4 +1,5 @@
-"""Builds libawq_mi355x.so (all HIP sources, gfx950) in the package folder.
+"""Builds libawq_mi355x.so (all HIP sources, gfx950) and the binding's call
+extension _calls.so (csrc/calls.cpp) in the package folder.
 
     python -m weight_only_int4_quantize_amd.build
 """
@@ -96,5 +97,33 @@ def build(verbose: bool = False, extra_flags=None, out_path: str = LIB_PATH, obj
     return out_path
 
 
+CALLS_PATH = os.path.join(HERE, "_calls.so")
+
+
+def build_calls(verbose: bool = False) -> str:
+    """Compile the call extension (g++, this interpreter's and this torch's
+    headers); returns its path."""
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    lib = os.path.join(root, "lib")
+    tmp = CALLS_PATH + ".tmp"
+    proc = _run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+                 f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                 f"-I{os.path.join(root, 'include')}",
+                 f"-I{os.path.join(root, 'include', 'torch', 'csrc', 'api', 'include')}",
+                 f"-I{sysconfig.get_paths()['include']}", os.path.join(CSRC, "calls.cpp"), "-o", tmp, f"-L{lib}",
+                 "-ltorch_python", "-ltorch_cpu", "-lc10", f"-Wl,-rpath,{lib}"], verbose)
+    out, err = proc.communicate()
+    if proc.returncode != 0:
+        sys.stderr.write(out + err)
+        raise RuntimeError(f"g++ failed with exit code {proc.returncode}")
+    os.replace(tmp, CALLS_PATH)
+    return CALLS_PATH
+
+
 if __name__ == "__main__":
     print(build(verbose=True))
+    print(build_calls(verbose=True))
