@@ -274,3 +274,45 @@ def test_decoder_layer_run():
         near(mid, act64(h1 @ ref["gate"].T, "silu") * host(up).astype(np.float64), h, "gate")
         fused(mid, "down", residual=h, out=h)
         near(h, h1 + host(mid).astype(np.float64) @ ref["down"].T, mid, "down")
+
+
+def test_wrong_tensors_are_refused():
+    x, q, t = layer(3, 64, 256, 64, 4, [41])
+    x, qw, sc, zr = t
+    ok = torch.zeros(3, 64, dtype=torch.float16, device="cuda")
+    f = awq.awq_gemm_fused
+    for kw in (dict(bias=ok[0, :63]), dict(bias=ok[0].float()), dict(mul=ok[:2]), dict(mul=ok.float()),
+               dict(residual=ok.t()), dict(residual=ok.cpu()), dict(out=ok[:, :32]), dict(out=ok.float()),
+               dict(out=ok.t().contiguous().t()), dict(workspace=ok), dict(activation="tanh")):
+        with pytest.raises((TypeError, ValueError)):
+            f(x, qw, sc, zr, 64, **kw)
+    for bad in ((x.float(), qw, sc, zr), (x, qw.float(), sc, zr), (x, qw[:, :-1].contiguous(), sc, zr),
+                (x, qw, sc[:, :1].contiguous(), zr), (x, qw, sc, zr.float()), (x[:, ::2], qw, sc, zr),
+                (x.cpu(), qw, sc, zr), (x[0], qw, sc, zr)):
+        with pytest.raises((TypeError, ValueError)):
+            f(*bad, 64, out=ok)
+    with pytest.raises((awq.AwqError, ValueError)):
+        f(x, qw, sc, zr, 96)
+    y = f(x, qw, sc, zr, 64, activation="relu", out=ok)
+    assert y is ok
+
+
+def test_two_streams_at_once():
+    """Two layers on two streams with a workspace each, split kernels both."""
+    sets = []
+    for i, (M, N, K) in enumerate(((64, 1024, 4096), (203, 1000, 4096))):
+        x, q, t = layer(M, N, K, 128, 4, [42, i])
+        ws = awq.gemm_workspace(M, N, K)
+        res = torch.ones(M, N, dtype=torch.float16, device="cuda")
+        call = lambda t=t, res=res, ws=ws: awq.awq_gemm_fused(*t, 128, activation="gelu", residual=res, workspace=ws)  # noqa: E731
+        sets.append((call, host(call()), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(8):
+        for i, (call, _, stream) in enumerate(sets):
+            with torch.cuda.stream(stream):
+                outs[i].append(call())
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o in outs[i]:
+            np.testing.assert_array_equal(host(o), sets[i][1])

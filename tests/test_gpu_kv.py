@@ -12,10 +12,12 @@ u = 2^-24, S the largest scale * sum |q_d k_d| of a row:
     N weights and the rescaling per 64 keys round N + N / 16 times: together
     e = 2 ((D + 4) u S + 2^-21 + 2 N u), once in the numerator, once in the
     denominator;
-  * a weight is rounded to fp16, half a step 2^-11 of it; in the unit 2^-14
-    its subnormal half step is 2^-39 of the largest scale, under e;
+  * a weight is rounded to fp16, half a step 2^-11 of it; in its unit (2^-14
+    of the largest scale in decode, 2^-10 of up to twice it in prefill) the
+    subnormal half step is 2^-34 of the largest page scale V at most, on N
+    values of up to `top` steps: N 2^-34 top V;
   * the output is rounded to fp16: 2^-11 |o|, or 2^-25 for a subnormal.
-so |err| <= (e + 2^-11) A + 2^-11 |o| + 2^-25, and |err lse| <= e + 2^-22 |lse|.
+so |err| <= (e + 2^-11) A + N 2^-34 top V + 2^-11 |o| + 2^-25, and |err lse| <= e + 2^-22 |lse|.
 """
 
 import ctypes
@@ -118,7 +120,8 @@ class Model:
         o, lse, (eo, elog, spread, mass) = got
         u = 2.0 ** -24
         e = 2 * ((self.dim + 4) * u * mass + 2.0 ** -21 + 2 * n_keys * u)
-        tol = (e[..., None] + 2.0 ** -11) * spread + 2.0 ** -11 * np.abs(eo) + 2.0 ** -25
+        tol = (e[..., None] + 2.0 ** -11) * spread + 2.0 ** -11 * np.abs(eo) + 2.0 ** -25 + \
+            n_keys * 2.0 ** -34 * float(kv_oracle.TOP[self.fmt]) * float(self.vs.max(initial=0))
         err = np.abs(o.astype(np.float64) - eo)
         assert np.isfinite(o).all()
         assert (err <= tol).all(), f"worst {np.max(err / tol):.3f} of the bound"
@@ -421,3 +424,118 @@ def test_steps_in_a_graph():
         assert (np.abs(got - want[0]) <= tol).all()
         out2 = awq.awq_kv_attention(q, m.cache, s)      # eager, without a workspace
         assert (np.abs(host(out2) - want[0]) <= tol).all()
+
+
+@pytest.mark.parametrize("new", [2, 60])
+def test_attention_scale_of_any_sign(new):
+    m = Model([20, new], 2, 2, 64, 64, "int8", 200)
+    m.append([200, 90])
+    q = m.rng.standard_normal((2 * new, 4, 64)).astype(np.float16)
+    for scale in (-0.2, 0.0, 1e-6, 3.0):
+        m.assert_attention(m.attend(q, [new, new], scale=scale), 200)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_workspace_counts_the_loose_bound(new):
+    """A workspace sized for a bound on the new tokens serves calls of fewer
+    rows than the bound, on either side of the kernels' border."""
+    m = Model([21, new], 1, 1, 64, 64, "int8", 2000)
+    m.append([2000])
+    q = m.rng.standard_normal((new, 2, 64)).astype(np.float16)
+    for bound in (new, 16, 17, 500, 4000):
+        if bound >= new:
+            m.assert_attention(m.attend(q, [new], max_tokens=bound), 2000)
+
+
+def test_far_pages():
+    """Pages past 4 GiB of codes: writes, reads and attention address them."""
+    heads, dim, page = 8, 128, 64
+    per = heads * dim * page                    # bytes of a page's keys
+    pages = (5 << 30) // per
+    cache = awq.KVCache.empty(pages, heads, dim, page, "int8")
+    rng = np.random.default_rng(22)
+    ids = np.array([[pages - 1, 3, pages - 2], [0, pages // 2, pages - 7]], np.int32)
+    lens = np.array([150, 170], np.int32)
+    cu = np.array([0, 150, 320], np.int32)
+    k, v = (rng.standard_normal((320, heads, dim)).astype(np.float16) for _ in range(2))
+    s = awq.KVSeqs(dev(ids), dev(cu), dev(lens), 170, 170)
+    awq.awq_kv_write(cache, s, dev(k), dev(v))
+    gk, gv = awq.awq_kv_read(cache, s)
+    # the oracle's cache holds the six pages alone
+    small = np.arange(6, dtype=np.int32).reshape(2, 3)
+    kc, vc = np.zeros((6, heads, page, dim)), np.zeros((6, heads, page, dim))
+    ks, vs = np.zeros((6, heads), np.float32), np.zeros((6, heads), np.float32)
+    kv_oracle.write(kc, ks, k, small, cu, lens, "int8")
+    kv_oracle.write(vc, vs, v, small, cu, lens, "int8")
+    for got, codes, scales in ((gk, kc, ks), (gv, vc, vs)):
+        want = np.zeros(got.shape, np.float16)
+        kv_oracle.read(codes, scales, want, small, cu, lens)
+        np.testing.assert_array_equal(host(got), want)
+    for n in (1, 50):
+        cu2 = np.array([0, n, 2 * n], np.int32)
+        q = rng.standard_normal((2 * n, 16, dim)).astype(np.float16)
+        s2 = awq.KVSeqs(dev(ids), dev(cu2), dev(lens), n, 170)
+        o = host(awq.awq_kv_attention(dev(q), cache, s2, workspace=awq.kv_attention_workspace(cache, s2, 16)))
+        eo, _, spread, mass = kv_oracle.attention(q, kc, ks, vc, vs, small, cu2, lens, dim ** -0.5)
+        tol = (2 * ((dim + 4) * 2.0 ** -24 * mass + 2.0 ** -20)[..., None] + 2.0 ** -11) * spread + \
+            2.0 ** -11 * np.abs(eo) + 2.0 ** -24
+        assert (np.abs(o - eo) <= tol).all()
+
+
+def test_two_streams_at_once():
+    """Two batches over one cache, on two streams with a workspace each."""
+    m = Model([23], 2, 2, 128, 64, "e4m3", 3000)
+    m.append([3000, 2500])
+    sets = []
+    for new in (1, 48):
+        q = dev(m.rng.standard_normal((2 * new, 4, 128)).astype(np.float16))
+        s = m.seqs([new, new])[0]
+        ws = awq.kv_attention_workspace(m.cache, s, 4)
+        sets.append((q, s, ws, host(awq.awq_kv_attention(q, m.cache, s, workspace=ws)), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(8):
+        for i, (q, s, ws, _, stream) in enumerate(sets):
+            with torch.cuda.stream(stream):
+                outs[i].append(awq.awq_kv_attention(q, m.cache, s, workspace=ws))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o in outs[i]:
+            np.testing.assert_array_equal(host(o), sets[i][3])
+
+
+def test_wrong_tensors_are_refused():
+    m = Model([24], 1, 2, 64, 32, "int8", 32)
+    m.append([5])
+    s, *_ = m.seqs([1])
+    q = torch.zeros(1, 4, 64, dtype=torch.float16, device="cuda")
+    kv = torch.zeros(1, 2, 64, dtype=torch.float16, device="cuda")
+    attend, write, read = awq.awq_kv_attention, awq.awq_kv_write, awq.awq_kv_read
+    for bad, err in ((q.float(), TypeError), (q.cpu(), ValueError), (q[..., :32], ValueError), (q[0], ValueError),
+                     (q.transpose(1, 2), ValueError), ([1], TypeError)):
+        with pytest.raises(err):
+            attend(bad, m.cache, s)
+    with pytest.raises(awq.AwqError):
+        attend(torch.zeros(1, 3, 64, dtype=torch.float16, device="cuda"), m.cache, s, out=torch.zeros(
+            1, 3, 64, dtype=torch.float16, device="cuda"))
+    with pytest.raises(ValueError):
+        attend(q, m.cache, s, out=q[:, :2])
+    with pytest.raises(ValueError):
+        attend(q, m.cache, s, lse=torch.zeros(1, 2, device="cuda"))
+    with pytest.raises(TypeError):
+        attend(q, m.cache, s, workspace=torch.zeros(99, device="cuda"))
+    with pytest.raises(awq.AwqError):
+        attend(q, m.cache, s, causal=False, window=3, out=torch.zeros_like(q))
+    for bad in (kv.double(), kv[:, :1], kv.cpu()):
+        with pytest.raises((TypeError, ValueError)):
+            write(m.cache, s, bad, kv)
+        with pytest.raises((TypeError, ValueError)):
+            read(m.cache, s, out=(kv, bad))
+    with pytest.raises(ValueError):
+        write(m.cache, s, kv, torch.zeros(2, 2, 64, dtype=torch.float16, device="cuda"))
+    with pytest.raises(ValueError):
+        read(m.cache, s, n_tokens=3, out=(kv, kv.clone()))
+    odd = torch.zeros(1 * 2 * 68 + 4, dtype=torch.float16, device="cuda").as_strided((1, 2, 64), (136, 68, 1))
+    with pytest.raises(awq.AwqError):       # a head stride that is not a multiple of 8
+        write(m.cache, s, odd, kv)
+    m.check()                               # nothing was written

@@ -97,6 +97,8 @@ def test_attention_checks(L):
     c, s = cache(), seqs()
     assert attend(L, c, s, heads=0) == SHAPE and attend(L, c, s, heads=3) == SHAPE
     assert attend(L, c, s, n=2 ** 30) == SHAPE          # rows x heads past 32 bits
+    assert attend(L, c, seqs(max_tokens=2 ** 30)) == SHAPE
+    assert L.awq_kv_attention_workspace_bytes(ctypes.byref(c), ctypes.byref(seqs(max_tokens=2 ** 30)), 4) == 0
     assert attend(L, c, s, qs=(4, 128)) == SHAPE and attend(L, c, s, qs=(512, -8)) == SHAPE
     assert attend(L, c, s, os=(4, 128)) == SHAPE and attend(L, c, s, os=(512, 12)) == SHAPE
     for bad in (float("nan"), float("inf")):

@@ -891,7 +891,9 @@ size_t awq_kv_attention_workspace_bytes(const awq_kv_cache* cache, const awq_kv_
     KvPages c{};
     bool empty = false;
     if (kv_pages(cache, seqs, 1, &c, &empty) != AWQ_OK) return 0;
-    if (n_heads < 1 || n_heads % cache->n_kv_heads != 0) return 0;
+    if (n_heads < 1 || n_heads % cache->n_kv_heads != 0 ||
+        seqs->max_tokens * (n_heads / cache->n_kv_heads) > INT32_MAX - 256)
+        return 0;
     if (empty) return 256;
     return kv_attention_workspace_bytes(seqs->n_seqs, cache->n_kv_heads, n_heads / cache->n_kv_heads, cache->head_dim,
                                         seqs->max_tokens, seqs->max_len);
@@ -906,7 +908,9 @@ awq_status awq_kv_attention(const awq_kv_cache* cache, const awq_kv_seqs* seqs, 
     bool empty = false;
     const awq_status st = kv_pages(cache, seqs, n_tokens, &a.c, &empty);
     if (st != AWQ_OK) return st;
-    if (n_heads < 1 || n_heads % cache->n_kv_heads != 0 || n_tokens * n_heads > INT32_MAX) return AWQ_ERR_SHAPE;
+    if (n_heads < 1 || n_heads % cache->n_kv_heads != 0 || n_tokens * n_heads > INT32_MAX ||
+        seqs->max_tokens * (n_heads / cache->n_kv_heads) > INT32_MAX - 256)
+        return AWQ_ERR_SHAPE;
     if (!strides_ok(q_token_stride, q_head_stride) || !strides_ok(out_token_stride, out_head_stride))
         return AWQ_ERR_SHAPE;
     if (!std::isfinite(scale) || (causal != 0 && causal != 1) || window < 0 || (window > 0 && !causal))
@@ -925,7 +929,7 @@ awq_status awq_kv_attention(const awq_kv_cache* cache, const awq_kv_seqs* seqs, 
     a.n_seqs = seqs->n_seqs;
     a.format = cache->format;
     a.ratio = n_heads / cache->n_kv_heads;
-    a.max_tokens = std::min(seqs->max_tokens, n_tokens);
+    a.max_tokens = seqs->max_tokens;        // as the workspace query counts
     a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     a.causal = causal != 0;
     a.window = static_cast<int>(std::min<int64_t>(window, INT32_MAX));

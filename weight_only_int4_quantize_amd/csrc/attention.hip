@@ -29,6 +29,8 @@ namespace {
 
 constexpr float kNone = -1.0e38f;       // running maximum before any visible key
 constexpr float kWeightUnit = 16384.0f; // 2^14, the unit of the rounded weights
+constexpr float kPrefillUnit = 1024.0f; // 2^10, the same in prefill
+constexpr float kSlack = 4.0f;          // log2 of the largest weight there
 constexpr float kTinyScale = 1.0e-20f;  // scales at or below it count as it
 constexpr int kSc1 = 16;                // cache-policy bit sc1 (device scope)
 constexpr float kLn2 = 0.69314718056f;
@@ -537,12 +539,16 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv_pre
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 31, half = lane >> 5;
-    const int split = blockIdx.x % n_splits;
+    // Heads run fastest over the blocks, which go to the 8 XCDs in turn: with a
+    // multiple of 8 heads the row tiles of one head share an XCD, and its L2
+    // the head's keys and values. The last rows of a causal chunk see the
+    // most: first.
     const int b = blockIdx.z;
-    const int kv_head = blockIdx.y;
-    const int row_tiles = gridDim.x / n_splits;
-    // the last rows of a causal chunk see the most: first
-    const int row_tile = row_tiles - 1 - blockIdx.x / n_splits;
+    const int kv_head = blockIdx.x % c.heads;
+    const int rest = blockIdx.x / c.heads;
+    const int split = rest % n_splits;
+    const int row_tiles = gridDim.x / c.heads / n_splits;
+    const int row_tile = row_tiles - 1 - rest / n_splits;
     const int row0 = row_tile * kPrefillRows;
     const KvSeq sq = kv_seq_shared(c, b);
     const int all_rows = sq.n * a.ratio;
@@ -564,8 +570,12 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv_pre
         const half_t* q = a.q + (static_cast<int64_t>(sq.row0) + token) * a.q_token +
                           (kv_head * a.ratio + (row0 + wrow) % a.ratio) * a.q_head;
 #pragma unroll
-        for (int i = 0; i < DC; ++i) qf[i] = *reinterpret_cast<const half8_t*>(q + 16 * i + 8 * half);
+        for (int i = 0; i < DC; ++i) {
+            qf[i] = *reinterpret_cast<const half8_t*>(q + 16 * i + 8 * half);
+            if (a.scale_log2 < 0.f) qf[i] = -qf[i];
+        }
     }
+    const float qscale = fabsf(a.scale_log2);
     // what this wave's rows see
     const Span wspan = wave * 32 < rows ? row_span(a, sq, row0 + wave * 32, min(32, rows - wave * 32))
                                         : Span{0, 0, 0, 0};
@@ -579,6 +589,8 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv_pre
         bool held[NP];
         float ks[NP], vs[NP];
     };
+    // token of a 32-token unit that S^T row r holds
+    auto token_of = [](int r) { return 16 * ((r >> 2) & 1) + 4 * (r >> 3) + (r & 3); };
     kv_u32x4 kr[PIECES], vr[PIECES];
     auto load = [&](int tile, Pages& pg) {
         const int tb = tile * kTile;
@@ -598,7 +610,9 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv_pre
         for (int i = 0; i < PIECES; ++i) {
             const int e = tid + i * NT;
             if (TILE_PIECES % NT != 0 && e >= TILE_PIECES) break;
-            const int t = e % kTile, ch = e / kTile;            // key piece: token t, channels 16 ch ..
+            // key piece: the token of S^T row e % 64 (so that both the LDS write
+            // and the operand reads are of neighbouring pieces), channels 16 ch ..
+            const int t = (e & 32) + token_of(e & 31), ch = e / kTile;
             const int kslot = NP == 2 ? t & 31 : slot0 + t;
             kr[i] = *reinterpret_cast<const kv_u32x4*>(c.k_codes + (NP == 2 && t >= 32 ? block[NP - 1] : block[0]) * page_bytes +
                                                        ((ch << c.log2_page) + kslot) * 16);
@@ -642,7 +656,6 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv_pre
     for (int t = 0; t < DT; ++t)
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[t][e] = 0.f;
-    const int krow = 16 * ((col >> 2) & 1) + 4 * (col >> 3) + (col & 3);
 
     auto compute = [&](int tile, const Pages& pg, const half8_t* ks, const half8_t* vs) {
         const int tb = tile * kTile;
@@ -654,11 +667,8 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv_pre
             for (int e = 0; e < 16; ++e) s[u][e] = 0.f;
 #pragma unroll
             for (int i = 0; i < DC; ++i)
-                s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ks[(2 * i + half) * kTile + 32 * u + krow], qf[i], s[u], 0,
+                s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ks[(2 * i + half) * kTile + 32 * u + col], qf[i], s[u], 0,
                                                               0, 0);
-            const float kscale = pg.ks[NP == 2 ? u : 0] * a.scale_log2;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) s[u][e] *= kscale;
         }
         bool whole = tb >= wspan.all_begin && tb + kTile <= wspan.all_end;
 #pragma unroll
@@ -672,42 +682,58 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv_pre
                     s[u][e] = pg.held[NP == 2 ? u : 0] && j >= lo && j < hi ? s[u][e] : -__builtin_huge_valf();
                 }
         }
-        float top = s[0][0];
+        // ---- softmax: the logits stay unscaled, the page's scale (over 0, the
+        // sign of `scale` is in the queries) goes into the exponent's fma, and
+        // so do the values' scale and the weights' unit:
+        //   2^(x kscale - m + log2(vs / unit 2^10))
+        float top[2], ksc[2];
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u) {
+            ksc[u] = fmaxf(pg.ks[NP == 2 ? u : 0] * qscale, kTinyScale);
+            top[u] = s[u][0];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) top = fmaxf(top, s[u][e]);
-        top = across_halves_max(top);
-        const float mn = fmaxf(m, top);
-        const float unit_new = fmaxf(unit, NP == 2 ? fmaxf(pg.vs[0], pg.vs[NP - 1]) : pg.vs[0]);
-        const float unit_inv = __builtin_amdgcn_rcpf(unit_new);
-        const float shrink = __builtin_amdgcn_exp2f(m - mn);
-        const float carry = shrink * (unit * unit_inv);
-        sum *= shrink;
+            for (int e = 1; e < 16; ++e) top[u] = fmaxf(top[u], s[u][e]);
+            top[u] *= ksc[u];
+        }
+        const float mt = across_halves_max(fmaxf(top[0], top[1]));
+        const float vmax = NP == 2 ? fmaxf(pg.vs[0], pg.vs[NP - 1]) : pg.vs[0];
+        // The running maximum and the unit move only when a weight would pass
+        // 2^4 or a scale twice the unit (weights stay below 2^15): rarely
+        // after the first tiles, and the outputs need no rescaling until then.
+        if (__any(mt > m + kSlack) || vmax > 2.0f * unit) {
+            const float mn = fmaxf(m, mt), unit_new = fmaxf(unit, vmax);
+            const float shrink = __builtin_amdgcn_exp2f(m - mn);
+            const float carry = shrink * (unit * __builtin_amdgcn_rcpf(unit_new));
+            sum *= shrink;
+#pragma unroll
+            for (int t = 0; t < DT; ++t)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[t][e] *= carry;
+            m = mn;
+            unit = unit_new;
+        }
         half8_t pf[2][2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const float vscale = pg.vs[NP == 2 ? u : 0] * unit_inv * kWeightUnit;
+            const float vscale = pg.vs[NP == 2 ? u : 0] * __builtin_amdgcn_rcpf(unit) * kPrefillUnit;
+            const float shift = __builtin_amdgcn_logf(vscale) - m;
+            float part = 0.f;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-                const float p = __builtin_amdgcn_exp2f(s[u][e] - mn);
-                sum += p;
-                pf[u][e >> 3][e & 7] = static_cast<half_t>(p * vscale);
+                const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][e], ksc[u], shift));
+                part += w;
+                pf[u][e >> 3][e & 7] = static_cast<half_t>(w);
             }
+            sum = __builtin_fmaf(part, __builtin_amdgcn_rcpf(vscale), sum);
         }
-        m = mn;
-        unit = unit_new;
 #pragma unroll
-        for (int t = 0; t < DT; ++t) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) acc[t][e] *= carry;
+        for (int t = 0; t < DT; ++t)
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
                     acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vs[(4 * u + 2 * half + k) * D + 32 * t + col],
                                                                     pf[u][k], acc[t], 0, 0, 0);
-        }
     };
 
     if (from < to) {
@@ -730,7 +756,7 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv_pre
     __syncthreads();        // the stages are free: the outputs take their place
 
     sum += __shfl_xor(sum, 32);
-    const float true_unit = unit * (1.0f / kWeightUnit);
+    const float true_unit = unit * (1.0f / kPrefillUnit);
     float* so = reinterpret_cast<float*>(lds);
 #pragma unroll
     for (int t = 0; t < DT; ++t)
@@ -818,7 +844,7 @@ void launch_np(const KvAttentionArgs& a, const Plan& p, const Split& sp, hipStre
                            dim3(kDecodeWaves * kWave), 0, stream, a, sp, p.splits);
     else
         hipLaunchKernelGGL((kv_prefill_kernel<D, FORMAT, NP>),
-                           dim3(static_cast<unsigned>(p.row_tiles * p.splits), static_cast<unsigned>(a.c.heads),
+                           dim3(static_cast<unsigned>(p.row_tiles * p.splits * a.c.heads), 1,
                                 static_cast<unsigned>(a.n_seqs)),
                            dim3(kPrefillWaves * kWave), 0, stream, a, sp, p.splits);
 }
@@ -843,7 +869,7 @@ size_t kv_attention_workspace_bytes(int n_seqs, int kv_heads, int ratio, int hea
 
 awq_status launch_kv_attention(const KvAttentionArgs& a, void* workspace, hipStream_t stream) {
     const Plan p = plan_for(a.n_seqs, a.c.heads, a.ratio, a.max_tokens, a.c.max_len, workspace != nullptr);
-    if (p.row_tiles * p.splits >= (int64_t{1} << 31) || (p.decode && p.row_tiles * a.c.heads > 65535))
+    if (p.row_tiles * p.splits * a.c.heads >= (int64_t{1} << 31) || (p.decode && p.row_tiles * a.c.heads > 65535))
         return AWQ_ERR_SHAPE;
     Split sp;
     sp.tokens = p.tokens;
