@@ -97,7 +97,10 @@ awq_status launch_gemv_grouped(const half_t* x, const GemvLayers& layers, int64_
 
 // MFMA GEMM. The B operand is INT4 or W8 (qweight/scales/zeros) or fp16 W[N, K].
 enum class GemmB { kInt4, kF16, kInt8 };
-enum class GemmOut { kF16, kF32, kLoss, kFused };    // kFused: fp16 behind the epilogue
+// kFused, kFusedOdd: fp16 behind the epilogue, in 16-byte accesses
+// (Epilogue::vectors) or element by element
+enum class GemmOut { kF16, kF32, kLoss, kFused, kFusedOdd };
+constexpr bool is_fused(GemmOut o) { return o == GemmOut::kFused || o == GemmOut::kFusedOdd; }
 // The searches' fp32 reference output (kF32 results, kLoss references) is
 // kept in the accumulator order of v_mfma_f32_32x32x16: 256 x 128 tiles
 // (row-major over ceil(N / 128) tile columns), each of 32 sub-tiles of

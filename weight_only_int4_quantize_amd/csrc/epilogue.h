@@ -16,8 +16,9 @@ namespace awq {
 struct NoEpilogue {};
 
 // the operands of one output element, as stored (0 where there is none)
+// (a register each: two halves in one would make loads wait for each other)
 struct EpilogueBits {
-    uint16_t bias, mul, residual;
+    uint32_t bias, mul, residual;
 };
 
 __device__ inline float epilogue_sigmoid(float x) {
@@ -66,7 +67,10 @@ __device__ inline void epilogue_act(float (&v)[N], int act) {
         default: break;
     }
 }
-__device__ inline float epilogue_f(uint16_t b) { return static_cast<float>(__builtin_bit_cast(half_t, b)); }
+__device__ inline float epilogue_f(uint32_t b) {
+    return static_cast<float>(__builtin_bit_cast(half_t, static_cast<uint16_t>(b)));
+}
+__device__ inline uint32_t epilogue_bits(const half_t* p) { return *reinterpret_cast<const uint16_t*>(p); }
 // v[0 .. N) to the outputs, in place
 template <int N>
 __device__ inline void epilogue_apply(const Epilogue& e, float (&v)[N], const EpilogueBits (&b)[N], half_t (&y)[N]) {
@@ -91,9 +95,9 @@ __device__ inline half_t epilogue_apply(const Epilogue& e, float v, const Epilog
 // The operands of element (m, n), n < N: plain loads under uniform branches.
 __device__ inline EpilogueBits epilogue_load(const Epilogue& e, int64_t m, int64_t n) {
     EpilogueBits b{0, 0, 0};
-    if (e.bias != nullptr) b.bias = __builtin_bit_cast(uint16_t, e.bias[n]);
-    if (e.mul != nullptr) b.mul = __builtin_bit_cast(uint16_t, e.mul[m * e.mul_stride + n]);
-    if (e.residual != nullptr) b.residual = __builtin_bit_cast(uint16_t, e.residual[m * e.residual_stride + n]);
+    if (e.bias != nullptr) b.bias = epilogue_bits(e.bias + n);
+    if (e.mul != nullptr) b.mul = epilogue_bits(e.mul + m * e.mul_stride + n);
+    if (e.residual != nullptr) b.residual = epilogue_bits(e.residual + m * e.residual_stride + n);
     return b;
 }
 

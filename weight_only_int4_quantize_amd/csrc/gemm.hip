@@ -237,7 +237,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t partial_rsrc(float* p, int byt
 // one contiguous 1 KB piece per 16 bytes a lane takes (8 cache lines against
 // 32 for row-major B).
 template <GemmOut OMODE>
-using ArgsOf = std::conditional_t<OMODE == GemmOut::kFused, GemmFusedArgs, GemmArgs>;
+using ArgsOf = std::conditional_t<is_fused(OMODE), GemmFusedArgs, GemmArgs>;
 template <int BM, int BN, GemmB BMODE, GemmOut OMODE, bool STREAMK, bool DIRECT, int WGM = 2, int NT = kThreads,
           bool SKDMA = false, bool TILEDB = false>
 __global__ __launch_bounds__(NT, 512 / NT) void gemm_kernel(ArgsOf<OMODE> args, int tiles_n, StreamK sk) {
@@ -684,28 +684,59 @@ __global__ __launch_bounds__(NT, 512 / NT) void gemm_kernel(ArgsOf<OMODE> args, 
         asm volatile("" : "+v"(v));
         return v;
     };
-    [[maybe_unused]] auto fused_load = [&](int tm, int tn, int ij, EpilogueRun (&r)[2]) {
-        if constexpr (OMODE == GemmOut::kFused) {
-            if (!args.epilogue.vectors) return;
+    // kFusedOdd (rows or addresses that make no aligned 16-byte pieces): a lane
+    // keeps its column's elements and takes the operands one by one, from
+    // registers and without LDS.
+    struct OddRun {
+        EpilogueBits bits[16];
+    };
+    struct VectorRun {
+        EpilogueRun half[2];        // rows lane / 4 and 16 further
+    };
+    using FusedRun = std::conditional_t<OMODE == GemmOut::kFusedOdd, OddRun, VectorRun>;
+    [[maybe_unused]] auto fused_load = [&](int tm, int tn, int ij, FusedRun& r) {
+        if constexpr (is_fused(OMODE)) {
             const int ln = opaque(lane);
+            const int m0 = tm + wm + ij / TN * 32, n0 = tn + wn + ij % TN * 32;
+            if constexpr (OMODE == GemmOut::kFused) {
 #pragma unroll
-            for (int it = 0; it < 2; ++it)
-                r[it] = epilogue_load8(args.epilogue, tm + wm + ij / TN * 32 + it * 16 + (ln >> 2),
-                                       tn + wn + ij % TN * 32 + (ln & 3) * 8, M, N);
+                for (int it = 0; it < 2; ++it)
+                    r.half[it] = epilogue_load8(args.epilogue, m0 + it * 16 + (ln >> 2), n0 + (ln & 3) * 8, M, N);
+            } else {
+                // positions past the last row or column read that one's
+                // operands (in bounds, never used): no branch per element
+                const Epilogue& epi = args.epilogue;
+                const int64_t n = min(n0 + (ln & 31), N - 1);
+                auto row = [&](int e) {
+                    return static_cast<int64_t>(min(m0 + (e >> 2) * 8 + (ln >> 5) * 4 + (e & 3), M - 1));
+                };
+                const uint32_t bias = epi.bias != nullptr ? epilogue_bits(epi.bias + n) : 0;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) r.bits[e] = EpilogueBits{bias, 0, 0};
+                if (epi.mul != nullptr) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) r.bits[e].mul = epilogue_bits(epi.mul + row(e) * epi.mul_stride + n);
+                }
+                if (epi.residual != nullptr) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        r.bits[e].residual = epilogue_bits(epi.residual + row(e) * epi.residual_stride + n);
+                }
+            }
         }
     };
-    [[maybe_unused]] auto fused_store = [&](int tm, int tn, int ij, const float16_t& a, const EpilogueRun (&er)[2]) {
-        if constexpr (OMODE == GemmOut::kFused) {
+    [[maybe_unused]] auto fused_store = [&](int tm, int tn, int ij, const float16_t& a, const FusedRun& run) {
+        if constexpr (is_fused(OMODE)) {
             const Epilogue& epi = args.epilogue;
             const int ln = opaque(lane), fcol = ln & 31, frow4 = (ln >> 5) * 4;
             const int m0 = tm + wm + ij / TN * 32, n0 = tn + wn + ij % TN * 32;
+            if constexpr (OMODE == GemmOut::kFused) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int r = (e >> 2) * 8 + frow4 + (e & 3);
-                fbuf[r * 32 + (((fcol >> 2) ^ (r & 7)) << 2) + (fcol & 3)] = a[e];
-            }
-            __builtin_amdgcn_wave_barrier();            // one wave's LDS accesses run in order
-            if (epi.vectors) {
+                for (int e = 0; e < 16; ++e) {
+                    const int r = (e >> 2) * 8 + frow4 + (e & 3);
+                    fbuf[r * 32 + (((fcol >> 2) ^ (r & 7)) << 2) + (fcol & 3)] = a[e];
+                }
+                __builtin_amdgcn_wave_barrier();        // one wave's LDS accesses run in order
                 const int n = n0 + (ln & 3) * 8;
                 half8_t bias{};
                 if (epi.bias != nullptr && n < N) bias = *reinterpret_cast<const half8_t*>(epi.bias + n);
@@ -715,28 +746,21 @@ __global__ __launch_bounds__(NT, 512 / NT) void gemm_kernel(ArgsOf<OMODE> args, 
                     float v[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[j] = fbuf[r * 32 + (((c + (j >> 2)) ^ (r & 7)) << 2) + (j & 3)];
-                    epilogue_store8(epi, v, bias, er[it], args.y16, m0 + r, n, M, N);
+                    epilogue_store8(epi, v, bias, run.half[it], args.y16, m0 + r, n, M, N);
                 }
+                __builtin_amdgcn_wave_barrier();
             } else {
-                // odd rows or addresses: a lane takes single elements of its column
-#pragma unroll 1
-                for (int it = 0; it < 4; ++it) {
-                    EpilogueBits eb[4] = {};
-                    float v[4];
-                    half_t h[4];
-                    const int r0 = it * 8 + frow4, n = n0 + fcol;
+                float v[16];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (m0 + r0 + k < M && n < N) eb[k] = epilogue_load(epi, m0 + r0 + k, n);
-                        v[k] = fbuf[(r0 + k) * 32 + (((fcol >> 2) ^ ((r0 + k) & 7)) << 2) + (fcol & 3)];
-                    }
-                    epilogue_apply(epi, v, eb, h);
+                for (int e = 0; e < 16; ++e) v[e] = a[e];
+                half_t h[16];
+                epilogue_apply(epi, v, run.bits, h);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (m0 + r0 + k < M && n < N) args.y16[static_cast<int64_t>(m0 + r0 + k) * N + n] = h[k];
+                for (int e = 0; e < 16; ++e) {
+                    const int m = m0 + (e >> 2) * 8 + frow4 + (e & 3), n = n0 + fcol;
+                    if (m < M && n < N) args.y16[static_cast<int64_t>(m) * N + n] = h[e];
                 }
             }
-            __builtin_amdgcn_wave_barrier();
         }
     };
     auto finish_tile = [&](int tile, int tm, int tn) {
@@ -748,9 +772,9 @@ __global__ __launch_bounds__(NT, 512 / NT) void gemm_kernel(ArgsOf<OMODE> args, 
                 for (int j = 0; j < TN; ++j)
 #pragma unroll
                     for (int e = 0; e < 16; ++e) emit(tm, tn, i, j, e, acc[i][j][e], sq);
-        } else if constexpr (OMODE == GemmOut::kFused) {
+        } else if constexpr (is_fused(OMODE)) {
             // the next sub-tile's operands are loaded ahead
-            EpilogueRun er[2][2];
+            FusedRun er[2];
             fused_load(tm, tn, 0, er[0]);
 #pragma unroll
             for (int ij = 0; ij < TM * TN; ++ij) {
@@ -873,13 +897,13 @@ __global__ __launch_bounds__(NT, 512 / NT) void gemm_kernel(ArgsOf<OMODE> args, 
                                                 __HIP_MEMORY_SCOPE_AGENT) == b_last - b_first;
             __syncthreads();
             if (!s_flag) continue;
-            if constexpr (OMODE == GemmOut::kFused) {
+            if constexpr (is_fused(OMODE)) {
                 // the parts of one sub-tile at a time, four parts in flight
                 // (parts past the last read nothing and add zero), in segment
                 // order; not unrolled, the epilogue's code is long
 #pragma unroll 1
                 for (int ij = 0; ij < TM * TN; ++ij) {
-                    EpilogueRun er[2];
+                    FusedRun er;
                     fused_load(tm, tn, ij, er);
                     float16_t sum;
 #pragma unroll
@@ -1025,7 +1049,7 @@ size_t partials_bytes() {
 
 template <const Geometry& GEO, GemmB BMODE, GemmOut OMODE, bool DIRECT, int WGM = 2>
 void launch_cfg(const ArgsOf<OMODE>& args, void* workspace, hipStream_t stream) {
-    constexpr bool kHalfOut = OMODE == GemmOut::kF16 || OMODE == GemmOut::kFused;
+    constexpr bool kHalfOut = OMODE == GemmOut::kF16 || is_fused(OMODE);
     if constexpr (((OMODE == GemmOut::kLoss && BMODE == GemmB::kInt4) ||
                    (OMODE == GemmOut::kF32 && BMODE == GemmB::kF16)) && DIRECT && GEO.bn == 128) {
         if (args.b_tiled) {
@@ -1129,7 +1153,7 @@ bool use_mid(const GemmArgs& args, bool have_workspace) {
 // (the full-size scale search measured 153 ms there against 156 ms wide).
 template <GemmB BMODE, GemmOut OMODE>
 void launch_direct(const ArgsOf<OMODE>& args, void* workspace, hipStream_t stream) {
-    if constexpr (OMODE == GemmOut::kFused) {
+    if constexpr (is_fused(OMODE)) {
         if (use_mid(args, workspace != nullptr)) {
             launch_cfg<kMidTile, BMODE, OMODE, true, kDirectWgm>(args, workspace, stream);
             return;
@@ -1226,7 +1250,8 @@ awq_status launch_gemm(const GemmArgs& args, GemmB b, GemmOut out, hipStream_t s
             case GemmOut::kF16: launch_int4<GemmOut::kF16>(args, workspace, stream); break;
             case GemmOut::kF32: launch_int4<GemmOut::kF32>(args, workspace, stream); break;
             case GemmOut::kLoss: launch_int4<GemmOut::kLoss>(args, workspace, stream); break;
-            case GemmOut::kFused: return AWQ_ERR_CONFIG;    // launch_gemm_fused
+            case GemmOut::kFused:
+            case GemmOut::kFusedOdd: return AWQ_ERR_CONFIG;     // launch_gemm_fused
         }
     } else {
         switch (out) {
@@ -1241,7 +1266,8 @@ awq_status launch_gemm(const GemmArgs& args, GemmB b, GemmOut out, hipStream_t s
                     launch_cfg<kNarrowTile, GemmB::kF16, GemmOut::kF32, false>(args, workspace, stream);
                 break;
             case GemmOut::kLoss:
-            case GemmOut::kFused: return AWQ_ERR_CONFIG;
+            case GemmOut::kFused:
+            case GemmOut::kFusedOdd: return AWQ_ERR_CONFIG;
         }
     }
     return last_launch_status();
@@ -1252,9 +1278,11 @@ awq_status launch_gemm_fused(const GemmFusedArgs& args, GemmB b, hipStream_t str
     if (args.b_tiled || b == GemmB::kF16) return AWQ_ERR_CONFIG;
     if (b == GemmB::kInt8) {
         if (!direct_ok(args)) return AWQ_ERR_CONFIG;
-        launch_direct<GemmB::kInt8, GemmOut::kFused>(args, workspace, stream);
+        if (args.epilogue.vectors) launch_direct<GemmB::kInt8, GemmOut::kFused>(args, workspace, stream);
+        else launch_direct<GemmB::kInt8, GemmOut::kFusedOdd>(args, workspace, stream);
     } else {
-        launch_int4<GemmOut::kFused>(args, workspace, stream);
+        if (args.epilogue.vectors) launch_int4<GemmOut::kFused>(args, workspace, stream);
+        else launch_int4<GemmOut::kFusedOdd>(args, workspace, stream);
     }
     return last_launch_status();
 }
