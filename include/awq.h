@@ -576,7 +576,7 @@ awq_status awq_gemm_fused(const void* x_f16, const uint32_t* qweight,
  *                16]: 16 consecutive channels of a token are adjacent
  *   v_codes      device, uint8 [n_pages, n_kv_heads, page_size / 16, head_dim,
  *                16]: 16 consecutive tokens of a channel are adjacent
- *   k_scales, v_scales   device, fp32 [n_pages, n_kv_heads], finite and >= 0
+ *   k_scales, v_scales   device, fp32 [n_pages, n_kv_heads], 0 .. 65504
  * Codes 16-byte aligned, scales 4-byte aligned. A page need not be
  * initialised before the first write to it.
  */
@@ -650,8 +650,8 @@ typedef struct {
  *   n_tokens         rows of k and v; rows outside [0, n_tokens) and
  *                    positions below 0 are skipped
  * A page shared by several sequences may be read by all, but written through
- * one of them only in a call. Asynchronous on `stream`; results are the same
- * on every run.
+ * one of them only in a call, and at one place of its table row. Asynchronous
+ * on `stream`; results are the same on every run.
  */
 awq_status awq_kv_write(const awq_kv_cache* cache, const awq_kv_seqs* seqs,
                         const void* k_f16, int64_t k_token_stride, int64_t k_head_stride,
@@ -680,7 +680,11 @@ awq_status awq_kv_read(const awq_kv_cache* cache, const awq_kv_seqs* seqs,
  * with causal != 0 those with j <= p, and with window > 0 only the last
  * `window` of them (j > p - window). A query that sees no position gets
  * o = 0 and lse = -infinity. Logits, softmax statistics and sums are fp32;
- * the weights enter the second product rounded to fp16.
+ * the weights enter the second product as two fp16 numbers (a weight's
+ * rounding and what that left) where a kv head has at most 32 query rows in
+ * a sequence (max_tokens * r <= 32), rounded to fp16 where it has more. A
+ * query with a NaN that sees a position gets NaN (o and lse); no other row
+ * is touched by it, or by an infinity.
  *
  *   q_f16        device, fp16 [n_tokens, n_heads, head_dim], channels
  *                contiguous, 16-byte aligned, strides in halves, multiples
@@ -689,8 +693,8 @@ awq_status awq_kv_read(const awq_kv_cache* cache, const awq_kv_seqs* seqs,
  *   scale        finite
  *   causal       0 or 1; window 0 (none) or > 0 (causal only)
  *   out_f16      device, fp16 [n_tokens, n_heads, head_dim] (output, same
- *                rules as q; must not alias the inputs). Rows of no sequence
- *                are left as they were.
+ *                rules as q, and strides of at least head_dim; must not alias
+ *                the inputs). Rows of no sequence are left as they were.
  *   lse          device, fp32 [n_tokens, n_heads] or NULL (output): the
  *                natural logarithm of the softmax denominator
  *   workspace    device memory of at least

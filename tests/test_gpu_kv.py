@@ -539,3 +539,31 @@ def test_wrong_tensors_are_refused():
     with pytest.raises(awq.AwqError):       # a head stride that is not a multiple of 8
         write(m.cache, s, odd, kv)
     m.check()                               # nothing was written
+
+
+@pytest.mark.parametrize("split", [True, False])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("new", [2, 70])
+def test_attention_query_not_finite(new, bad, split):
+    """A query with a NaN gets NaN, in the output and in lse; neither it nor an
+    infinity reaches another row, the ones of its block included."""
+    m = Model([31, new], 2, 2, 128, 64, "int8", 1500)
+    m.append([1500, 900])
+    q = m.rng.standard_normal((2 * new, 4, 128)).astype(np.float16)
+    clean = q.copy()
+    q[1, 2, 77] = bad
+    s, cu, lens, table = m.seqs([new, new])
+    ws = awq.kv_attention_workspace(m.cache, s, 4) if split else None
+    lse = torch.zeros(q.shape[:2], device="cuda")
+    o = host(awq.awq_kv_attention(dev(q), m.cache, s, lse=lse, workspace=ws))
+    lse = host(lse)
+    if np.isnan(bad):
+        assert np.isnan(o[1, 2]).all() and np.isnan(lse[1, 2])
+    eo, el, spread, mass = kv_oracle.attention(clean, m.kc, m.ks, m.vc, m.vs, table, cu, lens, 128 ** -0.5)
+    e = 2 * (132 * 2.0 ** -24 * mass + 2.0 ** -21 + 3000 * 2.0 ** -24)
+    tol = (e[..., None] + 2.0 ** -11) * spread + 2.0 ** -11 * np.abs(eo) + 2.0 ** -25 + \
+        1500 * 2.0 ** -34 * 127 * float(m.vs.max())
+    others = np.ones(q.shape[:2], bool)
+    others[1, 2] = False
+    assert (np.abs(o - eo) <= tol)[others].all()
+    assert (np.abs(lse - el) <= e + 2.0 ** -22 * np.abs(el))[others].all()

@@ -113,6 +113,24 @@ def test_attention_checks(L):
     assert need > 0 and attend(L, c, s, ws=FAKE, nbytes=need - 1) == WORKSPACE
 
 
+def test_outputs_that_share_memory(L):
+    c, s = cache(), seqs()
+    assert attend(L, c, s, os=(0, 128)) == SHAPE and attend(L, c, s, os=(512, 0)) == SHAPE
+    assert attend(L, c, s, os=(64, 1920)) == SHAPE
+
+
+def test_more_blocks_than_a_launch_takes(L):
+    q = L.awq_kv_attention_workspace_bytes
+    many = cache(n_kv_heads=40000)          # two row tiles of 40000 heads
+    assert q(ctypes.byref(many), ctypes.byref(seqs(max_tokens=20)), 40000) == 0
+    assert attend(L, many, seqs(max_tokens=20), heads=40000) == SHAPE
+    loose = seqs(max_tokens=2 ** 30, n_seqs=1)
+    assert q(ctypes.byref(cache(n_kv_heads=2)), ctypes.byref(loose), 2) == 0
+    assert attend(L, cache(n_kv_heads=2), loose, heads=2) == SHAPE
+    pages = seqs(max_tokens=2 ** 31 - 1, max_len=1 << 30, max_pages=1 << 25, table_stride=1 << 25, n_seqs=1)
+    assert write(L, cache(page_size=32), pages, n=2 ** 31 - 1) == SHAPE
+
+
 def test_workspace_query(L):
     q = L.awq_kv_attention_workspace_bytes
     c = cache()

@@ -913,6 +913,9 @@ awq_status awq_kv_attention(const awq_kv_cache* cache, const awq_kv_seqs* seqs, 
         return AWQ_ERR_SHAPE;
     if (!strides_ok(q_token_stride, q_head_stride) || !strides_ok(out_token_stride, out_head_stride))
         return AWQ_ERR_SHAPE;
+    // rows of the output that share memory would be written by several blocks
+    if ((n_tokens > 1 && out_token_stride < cache->head_dim) || (n_heads > 1 && out_head_stride < cache->head_dim))
+        return AWQ_ERR_SHAPE;
     if (!std::isfinite(scale) || (causal != 0 && causal != 1) || window < 0 || (window > 0 && !causal))
         return AWQ_ERR_CONFIG;
     if (empty) return AWQ_OK;

@@ -5,10 +5,12 @@
 // from the exact fp16 numbers kc of the stored bytes; with the running
 // maximum m the weights are p = 2^(t - m), and sums and outputs carried from
 // earlier tiles are multiplied by 2^(m_old - m). The values' page scale vs
-// goes into the weights: the outputs are kept in units of r, the largest vs
-// so far, and p * (vs / r) * 2^14 is rounded to fp16 for the second product
-// (vs / r <= 1, so it stays below 2^14, and the 2^14 keeps a page of a
-// scale far below the largest out of fp16's subnormal range).
+// goes into the weights: the outputs are kept in units of the largest vs so
+// far, `unit`, and p * (vs / unit) times a power of two (2^14 in decode, 2^10
+// in prefill, where p may reach 2^4 and vs / unit 2) is what enters the
+// second product in fp16. The power keeps pages whose scale is far below the
+// largest out of fp16's subnormal range. Logits, maxima, sums and outputs are
+// fp32.
 //
 // Both kernels compute the transposed products: S^T = K . Q^T and
 // O^T = V^T . P^T. A lane then owns one query (a column), so the softmax's
@@ -100,7 +102,7 @@ __device__ inline void store_lse(const KvAttentionArgs& a, const KvSeq& sq, int 
     if (a.lse == nullptr) return;
     const int token = row / a.ratio, head = kv_head * a.ratio + row % a.ratio;
     a.lse[(static_cast<int64_t>(sq.row0) + token) * (static_cast<int64_t>(a.c.heads) * a.ratio) + head] =
-        sum > 0.f ? (m + __builtin_amdgcn_logf(sum)) * kLn2 : -__builtin_huge_valf();
+        sum == 0.f ? -__builtin_huge_valf() : (m + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 __device__ inline half_t* out_row(const KvAttentionArgs& a, const KvSeq& sq, int kv_head, int row) {
     const int token = row / a.ratio, head = kv_head * a.ratio + row % a.ratio;
@@ -249,7 +251,18 @@ __device__ inline void finish_rows(const KvAttentionArgs& a, const KvSeq& sq, co
 // 8 (l / 16) .. + 7, and holds results 4 (l / 16) + e of column l % 16.
 // S^T row r of sub-tile s4 (0 .. 3) is token 16 (r / 4) + 4 s4 + r % 4 of the
 // tile: quarter q of the wave then holds the 16 tokens 16 q .. of its query,
-// whose values are one 16-byte piece per channel.
+// whose values are one 16-byte piece per channel. (A load thus takes 64-byte
+// runs of keys; whole kilobytes in a copy of the loop without the arithmetic
+// read no faster, 6.0 against 6.1 TB/s.)
+// Bound by HBM: 2 D bytes per cached token and kv head. Measured (one MI355X,
+// int8, 128 channels): 64 sequences of 8192 down to 2048 tokens, 64 heads on
+// 8, 680 MB, 126-134 us, 5.1-5.4 TB/s, the ragged lengths leaving few waves
+// at the end; 32 of 2048 down, 32 heads, 63 us, 5.4 TB/s; 2 of 131072 and
+// 81920 (e4m3, 8 heads) 84-88 us, 5.0-5.2 TB/s; a plain read reaches 6.1 to
+// 6.2. Two blocks per CU at 128 channels (190 VGPRs); holding them to 168 for
+// a third spilled and was slower (139 against 134 us), non-temporal loads
+// gained 7% on the 680 MB case and lost as much on caches that the 256 MB
+// last-level cache holds.
 constexpr int kDecodeRows = 16;
 constexpr int kDecodeWaves = 4;
 constexpr int kTile = 64;
@@ -509,6 +522,12 @@ __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 64 ? 4 : D <= 96 ? 3 : D 
 // 8 (l / 32) .. + 7, and holds results 8 (i / 4) + 4 (l / 32) + i % 4 of
 // column l % 32. S^T row r is token 16 ((r / 4) % 2) + 4 (r / 8) + r % 4 of a
 // 32-token unit, so half h of the wave holds tokens 16 h + i.
+// Bound by the VALU and the matrix cores together: per wave and tile some 200
+// vector instructions (32 exponentials, 64 to unpack) against 32 MFMAs, the
+// counters reading 52% and 38% of the time, from two waves per SIMD (222
+// VGPRs). Measured (int8, 32 heads of 128 on 8, causal): 2 x 2048 tokens of
+// 4096 185-203 us, 744-816 TFLOP/s; 8192 of 8192 603 us, 913; e4m3, whose
+// unpack is half, 189 us; a large fp16 matrix product reaches 1158.
 constexpr int kPrefillWaves = 4;
 constexpr int kPrefillRows = 32 * kPrefillWaves;
 
@@ -835,6 +854,12 @@ size_t plan_bytes(const Plan& p, int n_seqs, int kv_heads, int head_dim) {
     return kCounterBytes + (p.splits > 1 ? tiles * p.splits * floats * sizeof(float) : 0);
 }
 
+// a launch takes 65535 blocks along y and 2^32 threads along x
+bool launchable(const Plan& p, int kv_heads) {
+    return p.decode ? p.row_tiles * kv_heads <= 65535
+                    : p.row_tiles * p.splits * kv_heads < (int64_t{1} << 32) / (kPrefillWaves * kWave);
+}
+
 template <int D, int FORMAT, int NP>
 void launch_np(const KvAttentionArgs& a, const Plan& p, const Split& sp, hipStream_t stream) {
     if (p.decode)
@@ -864,13 +889,13 @@ void launch_d(const KvAttentionArgs& a, const Plan& p, const Split& sp, hipStrea
 
 size_t kv_attention_workspace_bytes(int n_seqs, int kv_heads, int ratio, int head_dim, int64_t max_tokens,
                                     int64_t max_len) {
-    return plan_bytes(plan_for(n_seqs, kv_heads, ratio, max_tokens, max_len, true), n_seqs, kv_heads, head_dim);
+    const Plan p = plan_for(n_seqs, kv_heads, ratio, max_tokens, max_len, true);
+    return launchable(p, kv_heads) ? plan_bytes(p, n_seqs, kv_heads, head_dim) : 0;
 }
 
 awq_status launch_kv_attention(const KvAttentionArgs& a, void* workspace, hipStream_t stream) {
     const Plan p = plan_for(a.n_seqs, a.c.heads, a.ratio, a.max_tokens, a.c.max_len, workspace != nullptr);
-    if (p.row_tiles * p.splits * a.c.heads >= (int64_t{1} << 31) || (p.decode && p.row_tiles * a.c.heads > 65535))
-        return AWQ_ERR_SHAPE;
+    if (!launchable(p, a.c.heads)) return AWQ_ERR_SHAPE;
     Split sp;
     sp.tokens = p.tokens;
     sp.counters = static_cast<int*>(workspace);

