@@ -8,7 +8,9 @@
 // Old codes are touched only when the scale grew. The kernel is bound by
 // memory: 2 bytes read and 1 written per value. Measured: 11776 tokens of 32
 // heads of 128, keys and values, 86 us, 289 MB, 3.4 TB/s (a copy reaches
-// 4.9); one token of 64 sequences, 8 heads, 4.4 us, a launch's length.
+// 4.9); one token of 64 sequences, 8 heads, 4.4 us, a launch's length. Values
+// kept in registers between the passes were slower (write and read 167 us
+// against 154): the first pass then loads 4 bytes at a time in place of 16.
 //
 // Keys are stored 16 channels to a piece (a thread's 16-byte store), values
 // 16 tokens to a piece: a thread takes two channels of 16 tokens, so its
