@@ -4,13 +4,16 @@
 // Mathematics. A tile of keys gives logits t = ks * (q . kc) * scale * log2 e
 // from the exact fp16 numbers kc of the stored bytes; with the running
 // maximum m the weights are p = 2^(t - m), and sums and outputs carried from
-// earlier tiles are multiplied by 2^(m_old - m). The values' page scale vs
-// goes into the weights: the outputs are kept in units of the largest vs so
-// far, `unit`, and p * (vs / unit) times a power of two (2^14 in decode, 2^10
-// in prefill, where p may reach 2^4 and vs / unit 2) is what enters the
-// second product in fp16. The power keeps pages whose scale is far below the
-// largest out of fp16's subnormal range. Logits, maxima, sums and outputs are
-// fp32.
+// earlier tiles are multiplied by 2^(m_old - m). The values' page scale
+// vs = f 2^e (1/2 <= f < 1) goes into the weights: the outputs have a maximum
+// of their own, M, a whole number that is at least every t + e seen by the
+// row, and f 2^(t + e - M) times a power of two (2^15 in decode, 2^11 in
+// prefill, where t + e may pass M by 4) is what enters the second product in
+// fp16. A row's largest weight times scale is thus at least 2^13 (2^9) there,
+// and what fp16's subnormals lose is below 2^-38 (2^-34) of it for each key,
+// however far the pages' scales lie apart and whatever scales the masked
+// pages have. (Both exponents stay whole where scales enter, so no bits go
+// with them.) Logits, maxima, sums and outputs are fp32.
 //
 // Both kernels compute the transposed products: S^T = K . Q^T and
 // O^T = V^T . P^T. A lane then owns one query (a column), so the softmax's
@@ -30,9 +33,9 @@ namespace awq {
 namespace {
 
 constexpr float kNone = -1.0e38f;       // running maximum before any visible key
-constexpr float kWeightUnit = 16384.0f; // 2^14, the unit of the rounded weights
-constexpr float kPrefillUnit = 1024.0f; // 2^10, the same in prefill
-constexpr float kSlack = 4.0f;          // log2 of the largest weight there
+constexpr float kWeightUnit = 15.0f;    // log2 of the unit of the rounded weights
+constexpr float kPrefillUnit = 11.0f;   // the same in prefill
+constexpr float kSlack = 4.0f;          // what t and t + e may pass their maxima by there
 constexpr float kTinyScale = 1.0e-20f;  // scales at or below it count as it
 constexpr int kSc1 = 16;                // cache-policy bit sc1 (device scope)
 constexpr float kLn2 = 0.69314718056f;
@@ -325,7 +328,7 @@ __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 64 ? 4 : D <= 96 ? 3 : D 
             }
     }
 
-    float m = kNone, sum = 0.f, unit = 0.f;
+    float m = kNone, om = kNone, sum = 0.f;     // om: the outputs' maximum
     float4_t acc[DT];
 #pragma unroll
     for (int t = 0; t < DT; ++t) acc[t] = float4_t{0.f, 0.f, 0.f, 0.f};
@@ -429,31 +432,35 @@ __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 64 ? 4 : D <= 96 ? 3 : D 
             }
 
             // ---- softmax ----
+            const float scale = NP == 2 && quarter >= 2 ? vs[NP - 1] : vs[0];
+            const float vm = __builtin_amdgcn_frexp_mantf(scale);
+            const float ve = static_cast<float>(__builtin_amdgcn_frexp_expf(scale));
             float top = s[0];
 #pragma unroll
             for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+            const float out_top = NP == 2 ? across_quarters_max(top + ve) : 0.f;
             top = across_quarters_max(top);
             const float mn = fmaxf(m, top);
-            const float unit_new = fmaxf(unit, NP == 2 ? fmaxf(vs[0], vs[NP - 1]) : vs[0]);
-            const float unit_inv = __builtin_amdgcn_rcpf(unit_new);
+            const float on = fmaxf(om, __builtin_ceilf(NP == 2 ? out_top : top + ve));
             const float shrink = __builtin_amdgcn_exp2f(m - mn);
-            const float vscale = (NP == 2 && quarter >= 2 ? vs[NP - 1] : vs[0]) * unit_inv * kWeightUnit;
-            const float carry = shrink * (unit * unit_inv);
+            const float carry = __builtin_amdgcn_exp2f(om - on);
+            const float shift = ve + kWeightUnit - on;
             // A weight goes into the second product as two fp16 numbers, its
             // rounding and what that left: the product's matrix time is free
             // here, and the rounding of one would add as much error as the
             // output's own.
             half8_t pf[2], pl[2];
-            sum *= shrink;
+            float part = 0.f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const float p = __builtin_amdgcn_exp2f(s[i] - mn), w = p * vscale;
-                sum += p;
+                const float p = __builtin_amdgcn_exp2f(s[i] + shift), w = p * vm;
+                part += p;
                 pf[i >> 3][i & 7] = static_cast<half_t>(w);
                 pl[i >> 3][i & 7] = static_cast<half_t>(w - static_cast<float>(pf[i >> 3][i & 7]));
             }
+            sum = __builtin_fmaf(part, __builtin_amdgcn_exp2f(on - mn - (ve + kWeightUnit)), sum * shrink);
             m = mn;
-            unit = unit_new;
+            om = on;
 #pragma unroll
             for (int t = 0; t < DT; ++t) {
 #pragma unroll
@@ -473,7 +480,7 @@ __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 64 ? 4 : D <= 96 ? 3 : D 
     // ---- the waves' results, in true units ----
     sum += __shfl_xor(sum, 16);
     sum += __shfl_xor(sum, 32);
-    const float true_unit = unit * (1.0f / kWeightUnit);
+    const float true_unit = __builtin_amdgcn_exp2f(om - m - kWeightUnit);
 #pragma unroll
     for (int t = 0; t < DT; ++t) *reinterpret_cast<float4_t*>(&so[wave][col][16 * t + 4 * quarter]) = acc[t] * true_unit;
     if (quarter == 0) {
@@ -669,7 +676,7 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv_pre
         }
     };
 
-    float m = kNone, sum = 0.f, unit = 0.f;
+    float m = kNone, om = kNone, sum = 0.f;     // om: the outputs' maximum
     float16_t acc[DT];
 #pragma unroll
     for (int t = 0; t < DT; ++t)
@@ -704,38 +711,38 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv_pre
         // ---- softmax: the logits stay unscaled, the page's scale (over 0, the
         // sign of `scale` is in the queries) goes into the exponent's fma, and
         // so do the values' scale and the weights' unit:
-        //   2^(x kscale - m + log2(vs / unit 2^10))
-        float top[2], ksc[2];
+        //   2^(x kscale + log2 f + (e + 11 - M)), the bracket exact
+        float top[2], ksc[2], vm[2], ve[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             ksc[u] = fmaxf(pg.ks[NP == 2 ? u : 0] * qscale, kTinyScale);
+            vm[u] = __builtin_amdgcn_frexp_mantf(pg.vs[NP == 2 ? u : 0]);
+            ve[u] = static_cast<float>(__builtin_amdgcn_frexp_expf(pg.vs[NP == 2 ? u : 0]));
             top[u] = s[u][0];
 #pragma unroll
             for (int e = 1; e < 16; ++e) top[u] = fmaxf(top[u], s[u][e]);
             top[u] *= ksc[u];
         }
         const float mt = across_halves_max(fmaxf(top[0], top[1]));
-        const float vmax = NP == 2 ? fmaxf(pg.vs[0], pg.vs[NP - 1]) : pg.vs[0];
-        // The running maximum and the unit move only when a weight would pass
-        // 2^4 or a scale twice the unit (weights stay below 2^15): rarely
-        // after the first tiles, and the outputs need no rescaling until then.
-        if (__any(mt > m + kSlack) || vmax > 2.0f * unit) {
-            const float mn = fmaxf(m, mt), unit_new = fmaxf(unit, vmax);
-            const float shrink = __builtin_amdgcn_exp2f(m - mn);
-            const float carry = shrink * (unit * __builtin_amdgcn_rcpf(unit_new));
-            sum *= shrink;
+        const float ot = NP == 2 ? across_halves_max(fmaxf(top[0] + ve[0], top[1] + ve[1])) : mt + ve[0];
+        // The maxima move only when one would be passed by 4 (weights stay
+        // below 2^15): rarely after the first tiles, and the outputs need no
+        // rescaling until then.
+        if (__any(mt > m + kSlack || ot > om + kSlack)) {
+            const float mn = fmaxf(m, mt), on = fmaxf(om, __builtin_ceilf(ot));
+            const float carry = __builtin_amdgcn_exp2f(om - on);
+            sum *= __builtin_amdgcn_exp2f(m - mn);
 #pragma unroll
             for (int t = 0; t < DT; ++t)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) acc[t][e] *= carry;
             m = mn;
-            unit = unit_new;
+            om = on;
         }
         half8_t pf[2][2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const float vscale = pg.vs[NP == 2 ? u : 0] * __builtin_amdgcn_rcpf(unit) * kPrefillUnit;
-            const float shift = __builtin_amdgcn_logf(vscale) - m;
+            const float shift = __builtin_amdgcn_logf(vm[u]) + (ve[u] + kPrefillUnit - om);
             float part = 0.f;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
@@ -743,7 +750,8 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv_pre
                 part += w;
                 pf[u][e >> 3][e & 7] = static_cast<half_t>(w);
             }
-            sum = __builtin_fmaf(part, __builtin_amdgcn_rcpf(vscale), sum);
+            const float back = __builtin_amdgcn_exp2f(om - m - (ve[u] + kPrefillUnit)) * __builtin_amdgcn_rcpf(vm[u]);
+            sum = __builtin_fmaf(part, back, sum);
         }
 #pragma unroll
         for (int t = 0; t < DT; ++t)
@@ -775,7 +783,7 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv_pre
     __syncthreads();        // the stages are free: the outputs take their place
 
     sum += __shfl_xor(sum, 32);
-    const float true_unit = unit * (1.0f / kPrefillUnit);
+    const float true_unit = __builtin_amdgcn_exp2f(om - m - kPrefillUnit);
     float* so = reinterpret_cast<float*>(lds);
 #pragma unroll
     for (int t = 0; t < DT; ++t)
