@@ -681,8 +681,7 @@ awq_status awq_kv_read(const awq_kv_cache* cache, const awq_kv_seqs* seqs,
  * `window` of them (j > p - window). A query that sees no position gets
  * o = 0 and lse = -infinity. Logits, softmax statistics and sums are fp32;
  * the weights enter the second product as two fp16 numbers (a weight's
- * rounding and what that left) where a kv head has at most 32 query rows in
- * a sequence (max_tokens * r <= 32), rounded to fp16 where it has more. A
+ * rounding and what that left). A
  * query with a NaN that sees a position gets NaN (o and lse); no other row
  * is touched by it, or by an infinity.
  *

@@ -88,3 +88,31 @@ def test_small_page_takes_the_weight(fmt, page, small, order, new):
     q = m.rng.uniform(3.5, 4.5, (new, 2, 64)).astype(np.float16)
     got = m.attend(q, [new])
     hold(m, got, largest_product(m, q, length, new, 64 ** -0.5, 0), length)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("dim,page", [(64, 32), (96, 64), (128, 64), (192, 128), (256, 64)])
+@pytest.mark.parametrize("new", [2, 16, 70])
+def test_opposite_values_cancel(fmt, dim, page, new):
+    """Two visible keys of nearly equal weight and opposite values: the output
+    is a small difference, in which a weight rounded to one fp16 number
+    (2^-11 of A) would show. As two, a weight is within 2^-20 of itself (both
+    parts toward zero); its exponent, at most 16, is rounded twice and the
+    scales' logarithm, exponential and reciprocal add 2^-22 each, together
+    below 2^-18: |err| <= (e + 2^-18) A + N 2^-34 top C + 2^-11 |o| + 2^-25."""
+    say("weights, opposite values", fmt, dim, page, new)
+    length = 130
+    m = Model([53, dim, new], 1, 1, dim, page, fmt, length)
+    v = (m.rng.uniform(50, 100, (length, 1, 1)) * np.where(np.arange(length) % 2, 1.0, -1.0)[:, None, None] *
+         np.ones((1, 1, dim))).astype(np.float16)
+    v[:, :, ::3] = v[:, :, ::3] / 2
+    v[1::2] = -v[0::2]
+    m.append([length], k=m.values(length), v=v)
+    q = (m.rng.standard_normal((new, 2, dim)) * 0.02).astype(np.float16)
+    o, _, (eo, _, spread, mass) = m.attend(q, [new], window=2)
+    c = largest_product(m, q, length, new, dim ** -0.5, 2)
+    e = 2 * ((dim + 4) * U * mass + 2.0 ** -21 + 4 * U)
+    tol = (e + 2.0 ** -18)[..., None] * spread + 2.0 ** -11 * np.abs(eo) + 2.0 ** -25 + \
+        (2 * 2.0 ** -34 * float(kv_oracle.TOP[m.fmt]) * c)[..., None]
+    err = np.abs(o.astype(np.float64) - eo)
+    assert (err <= tol).all(), f"worst {np.max(err / tol):.3f} of the bound"

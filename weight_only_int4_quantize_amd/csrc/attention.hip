@@ -7,13 +7,16 @@
 // earlier tiles are multiplied by 2^(m_old - m). The values' page scale
 // vs = f 2^e (1/2 <= f < 1) goes into the weights: the outputs have a maximum
 // of their own, M, a whole number that is at least every t + e seen by the
-// row, and f 2^(t + e - M) times a power of two (2^15 in decode, 2^11 in
-// prefill, where t + e may pass M by 4) is what enters the second product in
-// fp16. A row's largest weight times scale is thus at least 2^13 (2^9) there,
-// and what fp16's subnormals lose is below 2^-38 (2^-34) of it for each key,
-// however far the pages' scales lie apart and whatever scales the masked
-// pages have. (Both exponents stay whole where scales enter, so no bits go
-// with them.) Logits, maxima, sums and outputs are fp32.
+// row, and f 2^(t + e - M) times a power of two (2^15 in decode, 2^12 in
+// prefill, where t + e may pass M by 3) is what enters the second product, as
+// two fp16 numbers: its rounding, and what that left. (The rounding of one
+// alone would add as much error as the output's own: 2.9e-4 of a prefill's
+// outputs against 2.07e-4, of which 2.07e-4 is the output's.) A row's largest
+// weight times scale is at least 2^13 (2^10) in these units, and what fp16's
+// subnormals lose is at most 2^-38 (2^-34) of it for each key, however far
+// the pages' scales lie apart and whatever scales the masked pages have.
+// (Both exponents stay whole where scales enter, so no bits go with them.)
+// Logits, maxima, sums and outputs are fp32.
 //
 // Both kernels compute the transposed products: S^T = K . Q^T and
 // O^T = V^T . P^T. A lane then owns one query (a column), so the softmax's
@@ -34,8 +37,8 @@ namespace {
 
 constexpr float kNone = -1.0e38f;       // running maximum before any visible key
 constexpr float kWeightUnit = 15.0f;    // log2 of the unit of the rounded weights
-constexpr float kPrefillUnit = 11.0f;   // the same in prefill
-constexpr float kSlack = 4.0f;          // what t and t + e may pass their maxima by there
+constexpr float kPrefillUnit = 12.0f;   // the same in prefill
+constexpr float kSlack = 3.0f;          // what t and t + e may pass their maxima by there
 constexpr float kTinyScale = 1.0e-20f;  // scales at or below it count as it
 constexpr int kSc1 = 16;                // cache-policy bit sc1 (device scope)
 constexpr float kLn2 = 0.69314718056f;
@@ -79,6 +82,18 @@ __device__ inline float across_halves_max(float v) {
 __device__ inline float across_quarters_max(float v) {
     const uint32_t u = __builtin_bit_cast(uint32_t, across_halves_max(v));
     return larger_of(__builtin_amdgcn_permlane16_swap(u, u, false, false));
+}
+
+// Two numbers to fp16, toward zero (one instruction; the nearest takes three).
+__device__ inline half2_t toward_zero(float a, float b) {
+    return __builtin_bit_cast(half2_t, __builtin_amdgcn_cvt_pkrtz(a, b));
+}
+
+// r = w - hi, exact (one instruction for each; a conversion and a difference
+// otherwise).
+__device__ inline void less_half(const float (&w)[2], half2_t hi, float (&r)[2]) {
+    asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel:[0,0,0] op_sel_hi:[1,0,0]" : "=v"(r[0]) : "v"(hi), "v"(w[0]));
+    asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(r[1]) : "v"(hi), "v"(w[1]));
 }
 
 // The positions rows [row0, row0 + rows) of a kv head see.
@@ -445,10 +460,7 @@ __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 64 ? 4 : D <= 96 ? 3 : D 
             const float shrink = __builtin_amdgcn_exp2f(m - mn);
             const float carry = __builtin_amdgcn_exp2f(om - on);
             const float shift = ve + kWeightUnit - on;
-            // A weight goes into the second product as two fp16 numbers, its
-            // rounding and what that left: the product's matrix time is free
-            // here, and the rounding of one would add as much error as the
-            // output's own.
+            // (the second part's matrix time is free here)
             half8_t pf[2], pl[2];
             float part = 0.f;
 #pragma unroll
@@ -529,12 +541,14 @@ __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 64 ? 4 : D <= 96 ? 3 : D 
 // 8 (l / 32) .. + 7, and holds results 8 (i / 4) + 4 (l / 32) + i % 4 of
 // column l % 32. S^T row r is token 16 ((r / 4) % 2) + 4 (r / 8) + r % 4 of a
 // 32-token unit, so half h of the wave holds tokens 16 h + i.
-// Bound by the VALU and the matrix cores together: per wave and tile some 200
-// vector instructions (32 exponentials, 64 to unpack) against 32 MFMAs, the
-// counters reading 52% and 38% of the time, from two waves per SIMD (222
-// VGPRs). Measured (int8, 32 heads of 128 on 8, causal): 2 x 2048 tokens of
-// 4096 185-203 us, 744-816 TFLOP/s; 8192 of 8192 603 us, 913; e4m3, whose
-// unpack is half, 189 us; a large fp16 matrix product reaches 1158.
+// Bound by neither unit alone: per wave and tile some 390 vector instructions
+// (32 of them exponentials, 64 to unpack) and 48 MFMAs, the counters reading
+// 56% and 51% of the time, which two waves per SIMD (206 VGPRs) overlap in
+// part. 16 of the 48 are the weights' second parts. Measured (8 kv heads of
+// 128, 32 query heads, causal; us, in brackets with one part): 2 x 2048
+// tokens of 4096 247 (197), 609 TFLOP/s, e4m3 241 (184); 8192 of 8192 785
+// (607); 64 channels 146 (110); 4 kv heads of 192 213 (186), of 256 277
+// (240). A large fp16 matrix product reaches 1158 TFLOP/s.
 constexpr int kPrefillWaves = 4;
 constexpr int kPrefillRows = 32 * kPrefillWaves;
 
@@ -711,7 +725,7 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv_pre
         // ---- softmax: the logits stay unscaled, the page's scale (over 0, the
         // sign of `scale` is in the queries) goes into the exponent's fma, and
         // so do the values' scale and the weights' unit:
-        //   2^(x kscale + log2 f + (e + 11 - M)), the bracket exact
+        //   2^(x kscale + log2 f + (e + 12 - M)), the bracket exact
         float top[2], ksc[2], vm[2], ve[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -725,7 +739,7 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv_pre
         }
         const float mt = across_halves_max(fmaxf(top[0], top[1]));
         const float ot = NP == 2 ? across_halves_max(fmaxf(top[0] + ve[0], top[1] + ve[1])) : mt + ve[0];
-        // The maxima move only when one would be passed by 4 (weights stay
+        // The maxima move only when one would be passed by 3 (weights stay
         // below 2^15): rarely after the first tiles, and the outputs need no
         // rescaling until then.
         if (__any(mt > m + kSlack || ot > om + kSlack)) {
@@ -739,28 +753,41 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv_pre
             m = mn;
             om = on;
         }
-        half8_t pf[2][2];
+        // one unit's weights, then its products: the next unit's exponentials
+        // run beside them
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
+            half8_t pf[2], pl[2];
             const float shift = __builtin_amdgcn_logf(vm[u]) + (ve[u] + kPrefillUnit - om);
             float part = 0.f;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][e], ksc[u], shift));
-                part += w;
-                pf[u][e >> 3][e & 7] = static_cast<half_t>(w);
+            for (int e = 0; e < 16; e += 2) {
+                float w[2], r[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    w[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][e + j], ksc[u], shift));
+                    part += w[j];
+                }
+                const half2_t hi = toward_zero(w[0], w[1]);
+                less_half(w, hi, r);
+                const half2_t lo = toward_zero(r[0], r[1]);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    pf[e >> 3][(e & 7) + j] = hi[j];
+                    pl[e >> 3][(e & 7) + j] = lo[j];
+                }
             }
             const float back = __builtin_amdgcn_exp2f(om - m - (ve[u] + kPrefillUnit)) * __builtin_amdgcn_rcpf(vm[u]);
             sum = __builtin_fmaf(part, back, sum);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int t = 0; t < DT; ++t) {
+                    const half8_t v = vs[(4 * u + 2 * half + k) * D + 32 * t + col];
+                    acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, pf[k], acc[t], 0, 0, 0);
+                    acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, pl[k], acc[t], 0, 0, 0);
+                }
         }
-#pragma unroll
-        for (int t = 0; t < DT; ++t)
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vs[(4 * u + 2 * half + k) * D + 32 * t + col],
-                                                                    pf[u][k], acc[t], 0, 0, 0);
     };
 
     if (from < to) {
