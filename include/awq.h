@@ -611,7 +611,7 @@ typedef struct {
  *                count as that
  *   n_seqs       0 .. 32767
  *   max_tokens   at least every cu_tokens[b + 1] - cu_tokens[b]
- *   max_len      at least every kv_len[b]
+ *   max_len      at least every kv_len[b]; at most 2^31 - 1024
  * max_tokens and max_len only size the launch (the lengths themselves are
  * read on the device, so a captured graph can be replayed with new ones).
  * Whatever the arrays hold, no access leaves the tensors: a kv_len past

@@ -808,7 +808,7 @@ awq_status kv_pages(const awq_kv_cache* cache, const awq_kv_seqs* seqs, int64_t 
     if (cache->n_pages < 1 || cache->n_pages > INT32_MAX || cache->n_kv_heads < 1 || cache->n_kv_heads > 65535)
         return AWQ_ERR_SHAPE;
     if (seqs->n_seqs < 0 || seqs->n_seqs > 32767 || seqs->max_pages < 0 || seqs->table_stride < seqs->max_pages ||
-        seqs->max_tokens < 0 || seqs->max_tokens > INT32_MAX || seqs->max_len < 0 || seqs->max_len > INT32_MAX - 256 ||
+        seqs->max_tokens < 0 || seqs->max_tokens > INT32_MAX || seqs->max_len < 0 || seqs->max_len > kKvMaxLen ||
         n_tokens < 0 || n_tokens > INT32_MAX)
         return AWQ_ERR_SHAPE;
     *empty = seqs->n_seqs == 0 || seqs->max_tokens == 0 || n_tokens == 0;

@@ -878,7 +878,7 @@ Plan plan_for(int n_seqs, int kv_heads, int ratio, int64_t max_tokens, int64_t m
         splits = std::max<int64_t>(1, splits);
     }
     const int64_t units = std::max<int64_t>(1, ceil_div(max_len, unit));
-    p.tokens = static_cast<int>(std::min<int64_t>(ceil_div(units, splits) * unit, INT32_MAX / 1024 * 1024));
+    p.tokens = static_cast<int>(ceil_div(units, splits) * unit);      // at most kKvMaxLen
     p.splits = static_cast<int>(std::max<int64_t>(1, ceil_div(max_len, p.tokens)));
     return p;
 }

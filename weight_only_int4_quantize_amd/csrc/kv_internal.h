@@ -25,6 +25,10 @@ struct KvPages {
     int max_len;
 };
 
+// Longest sequence: whole splits of 1024 positions, and a tile past them, in
+// 32 bits, so that one split can hold every position.
+constexpr int64_t kKvMaxLen = (int64_t{1} << 31) - 1024;
+
 constexpr float kInt8Top = 127.0f;
 constexpr float kE4m3Top = 448.0f;
 constexpr float kHalfMax = 65504.0f;
