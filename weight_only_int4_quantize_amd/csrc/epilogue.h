@@ -48,7 +48,7 @@ __device__ inline void epilogue_act(float (&v)[N], int act) {
     switch (act) {
         case AWQ_ACT_RELU:
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = fmaxf(v[i], 0.f);
+            for (int i = 0; i < N; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];    // a NaN stays
             break;
         case AWQ_ACT_SILU:
 #pragma unroll
