@@ -258,10 +258,12 @@ __global__ __launch_bounds__(kWriteThreads) void kv_read_kernel(KvReadArgs a) {
     }
 }
 
-// pages that max_tokens consecutive tokens can touch, and those of a sequence
+// Blocks along x: the pages that max_tokens consecutive tokens can touch, at
+// most a sequence's. One also where a sequence has none: the read's first
+// block zeroes the rows at positions below 0.
 int64_t touched_pages(const KvPages& c, int64_t max_tokens) {
     const int64_t page = int64_t{1} << c.log2_page;
-    return std::min<int64_t>((max_tokens + page - 2) / page + 1, c.max_pages);
+    return std::max<int64_t>(1, std::min<int64_t>((max_tokens + page - 2) / page + 1, c.max_pages));
 }
 
 // a launch takes 2^32 threads along x
