@@ -33,19 +33,23 @@ constexpr float kInt8Top = 127.0f;
 constexpr float kE4m3Top = 448.0f;
 constexpr float kHalfMax = 65504.0f;
 
-// One sequence of the batch: its rows in the token tensors, its tokens, the
-// position of row row0. Whatever the arrays hold, rows stay in [0, n_tokens)
-// and positions below max_pages pages, so no access leaves a tensor.
+// One sequence of the batch: its rows in the token tensors (row0 and the
+// n - 1 behind it), its tokens, the position of row row0. Whatever the arrays
+// hold, rows stay in [0, n_tokens) and positions below max_pages pages, so no
+// access leaves a tensor. Positions count from the sequence's last new token,
+// whether the tensors have its row or not.
 struct KvSeq {
     int row0, n, len, start;
+    __device__ int end() const { return start + n; }    // position behind the last row's
 };
 __device__ inline KvSeq kv_seq(const KvPages& c, int b) {
     KvSeq s;
     s.row0 = min(max(c.cu[b], 0), c.n_tokens);
-    s.n = min(max(c.cu[b + 1], s.row0), c.n_tokens) - s.row0;
+    const int rows_end = max(c.cu[b + 1], s.row0);
+    s.n = min(rows_end, c.n_tokens) - s.row0;
     const int64_t held = static_cast<int64_t>(c.max_pages) << c.log2_page;
     s.len = min(max(c.len[b], 0), static_cast<int>(held < c.max_len ? held : c.max_len));
-    s.start = s.len - s.n;
+    s.start = s.len - (rows_end - s.row0);
     return s;
 }
 
@@ -72,10 +76,11 @@ __device__ inline int kv_page(const KvPages& c, int b, int p) {
 __device__ inline KvSeq kv_seq_shared(const KvPages& c, int b) {
     KvSeq s;
     s.row0 = min(max(kv_shared_load(c.cu + b), 0), c.n_tokens);
-    s.n = min(max(kv_shared_load(c.cu + b + 1), s.row0), c.n_tokens) - s.row0;
+    const int rows_end = max(kv_shared_load(c.cu + b + 1), s.row0);
+    s.n = min(rows_end, c.n_tokens) - s.row0;
     const int64_t held = static_cast<int64_t>(c.max_pages) << c.log2_page;
     s.len = min(max(kv_shared_load(c.len + b), 0), static_cast<int>(held < c.max_len ? held : c.max_len));
-    s.start = s.len - s.n;
+    s.start = s.len - (rows_end - s.row0);
     return s;
 }
 __device__ inline int kv_page_shared(const KvPages& c, int b, int p) {

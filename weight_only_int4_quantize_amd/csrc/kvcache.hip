@@ -52,14 +52,14 @@ __global__ __launch_bounds__(kWriteThreads) void kv_write_kernel(KvWriteArgs a) 
     const int b = blockIdx.z >> 1;
     const KvSeq sq = kv_seq(c, b);
     const int lo = max(sq.start, 0);
-    if (lo >= sq.len) return;
+    if (lo >= sq.end()) return;
     const int p = (lo >> c.log2_page) + static_cast<int>(blockIdx.x);
     const int page_tokens = 1 << c.log2_page;
-    if ((static_cast<int64_t>(p) << c.log2_page) >= sq.len) return;
+    if ((static_cast<int64_t>(p) << c.log2_page) >= sq.end()) return;
     const int first = p << c.log2_page;
     const int id = kv_page(c, b, p);
     if (id < 0) return;
-    const int t0 = max(lo - first, 0), t1 = min(sq.len - first, page_tokens);   // the page's new tokens
+    const int t0 = max(lo - first, 0), t1 = min(sq.end() - first, page_tokens);   // the page's new tokens
     const int D = a.head_dim;
     const int64_t token_stride = values ? a.v_token : a.k_token;
     // row of the page's token 0 (rows before t0 are not read)
@@ -201,15 +201,15 @@ __global__ __launch_bounds__(kWriteThreads) void kv_read_kernel(KvReadArgs a) {
     const int lo = max(sq.start, 0);
     const kv_u32x4 zero = {0u, 0u, 0u, 0u};
     if (blockIdx.x == 0 && sq.start < 0) {      // rows at positions below 0
-        for (int64_t i = tid; i < static_cast<int64_t>(-sq.start) * (D / 8); i += kWriteThreads)
+        for (int64_t i = tid; i < static_cast<int64_t>(min(-sq.start, sq.n)) * (D / 8); i += kWriteThreads)
             *reinterpret_cast<kv_u32x4*>(y + (sq.start + i / (D / 8)) * token_stride + i % (D / 8) * 8) = zero;
     }
-    if (lo >= sq.len) return;
+    if (lo >= sq.end()) return;
     const int p = (lo >> c.log2_page) + static_cast<int>(blockIdx.x);
-    if ((static_cast<int64_t>(p) << c.log2_page) >= sq.len) return;
+    if ((static_cast<int64_t>(p) << c.log2_page) >= sq.end()) return;
     const int page_tokens = 1 << c.log2_page;
     const int first = p << c.log2_page;
-    const int t0 = max(lo - first, 0), t1 = min(sq.len - first, page_tokens);
+    const int t0 = max(lo - first, 0), t1 = min(sq.end() - first, page_tokens);
     y += first * token_stride;
     const int id = kv_page(c, b, p);
     if (id < 0) {
