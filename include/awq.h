@@ -692,8 +692,10 @@ awq_status awq_kv_read(const awq_kv_cache* cache, const awq_kv_seqs* seqs,
  *   scale        finite
  *   causal       0 or 1; window 0 (none) or > 0 (causal only)
  *   out_f16      device, fp16 [n_tokens, n_heads, head_dim] (output, same
- *                rules as q, and strides of at least head_dim; must not alias
- *                the inputs). Rows of no sequence are left as they were.
+ *                rules as q; must not alias the inputs). No two rows may
+ *                share memory: each stride at least head_dim, and one of
+ *                them past all the other's rows. Rows of no sequence are
+ *                left as they were.
  *   lse          device, fp32 [n_tokens, n_heads] or NULL (output): the
  *                natural logarithm of the softmax denominator
  *   workspace    device memory of at least

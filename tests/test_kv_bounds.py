@@ -34,3 +34,17 @@ def test_longest_length_is_taken(L):
     need = L.awq_kv_attention_workspace_bytes(ctypes.byref(cache()), ctypes.byref(s), 4)
     assert need > 0
     assert attend(L, cache(), s, ws=0x10000, nbytes=need - 1) == 5      # past the shape checks
+
+
+def test_output_rows_that_interleave(L):
+    """Strides of head_dim and more whose tokens and heads still meet: token 1
+    of head 0 would be head 1 of token 0, written by two blocks."""
+    c, s = cache(), seqs()
+    for strides in ((128, 128), (256, 256), (256, 128), (384, 128), (128, 256), (128, 15 * 128 - 8), (504, 128)):
+        assert attend(L, c, s, os=strides) == SHAPE, strides
+    # taken (what fails is the workspace, checked behind the strides)
+    for strides in ((512, 128), (1024, 128), (128, 15 * 128), (136, 16 * 136), (1024, 256)):
+        assert attend(L, c, s, os=strides, ws=0x10000, nbytes=0) == 5, strides
+    assert attend(L, c, s, os=(128, 128), n=1, ws=0x10000, nbytes=0) == 5      # one token: no two meet
+    one = cache(n_kv_heads=1)
+    assert attend(L, one, s, os=(128, 0), heads=1, ws=0x10000, nbytes=0) == 5

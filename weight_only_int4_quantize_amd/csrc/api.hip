@@ -916,6 +916,9 @@ awq_status awq_kv_attention(const awq_kv_cache* cache, const awq_kv_seqs* seqs, 
     // rows of the output that share memory would be written by several blocks
     if ((n_tokens > 1 && out_token_stride < cache->head_dim) || (n_heads > 1 && out_head_stride < cache->head_dim))
         return AWQ_ERR_SHAPE;
+    if (n_tokens > 1 && n_heads > 1 && out_token_stride < (n_heads - 1) * out_head_stride + cache->head_dim &&
+        out_head_stride < (n_tokens - 1) * out_token_stride + cache->head_dim)
+        return AWQ_ERR_SHAPE;
     if (!std::isfinite(scale) || (causal != 0 && causal != 1) || window < 0 || (window > 0 && !causal))
         return AWQ_ERR_CONFIG;
     if (empty) return AWQ_OK;
