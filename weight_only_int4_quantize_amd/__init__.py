@@ -23,6 +23,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libawq_mi355x.so")
@@ -797,7 +798,8 @@ _fast = None           # (extension or None, addresses of the library's entry po
 
 def _fast_calls():
     """The call extension (csrc/calls.cpp) and the entry points it calls; the
-    wrappers below marshal in Python where it has not been built."""
+    wrappers below marshal in Python where it has not been built, or not for
+    this interpreter and this torch."""
     global _fast
     _torch()
     entries = {n: ctypes.cast(getattr(load(), "awq_" + n), ctypes.c_void_p).value
@@ -808,8 +810,13 @@ def _fast_calls():
         import importlib.machinery
         import importlib.util
         loader = importlib.machinery.ExtensionFileLoader("_calls", path)
-        ext = importlib.util.module_from_spec(importlib.util.spec_from_loader("_calls", loader))
-        loader.exec_module(ext)
+        try:
+            ext = importlib.util.module_from_spec(importlib.util.spec_from_loader("_calls", loader))
+            loader.exec_module(ext)
+        except ImportError as e:
+            warnings.warn(f"{path} is of another build and is left out, calls take some 4 us longer; run "
+                          f"`python -m weight_only_int4_quantize_amd.build` ({e})", RuntimeWarning, stacklevel=3)
+            ext = None
     _fast = (ext, *entries.values())
     return _fast
 
