@@ -78,6 +78,18 @@ bool tokens(PyObject* o, int64_t heads, int64_t dim, int64_t device, Tokens& r) 
     return true;
 }
 
+// The status of an entry point's call, as a Python integer. The interpreter is
+// other threads' meanwhile (a launch waits when its queue is full); the
+// arguments' tensors are the caller's, who waits for this.
+template <class F, class... A>
+PyObject* status_of(F entry, A... args) {
+    awq_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = entry(args...);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(st);
+}
+
 // gemm_fused(entry, stream, device, x, qweight, scales, zeros, group, bias, act, mul, residual, path, out, workspace)
 PyObject* gemm_fused(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (n != 15) Py_RETURN_NONE;
@@ -108,9 +120,9 @@ PyObject* gemm_fused(PyObject*, PyObject* const* a, Py_ssize_t n) {
     size_t bytes;
     if (!rows(a[10], M, N, dev, mul, ms) || !rows(a[11], M, N, dev, res, rs) || !workspace_of(a[14], dev, ws, bytes))
         Py_RETURN_NONE;
-    return PyLong_FromLong(entry(x->data_ptr(), static_cast<const uint32_t*>(q->data_ptr()), s->data_ptr(),
-                                 z->data_ptr(), M, N, K, static_cast<int>(group), bits, bias, static_cast<int>(act), mul,
-                                 ms, res, rs, y->data_ptr(), static_cast<int>(path), ws, bytes, stream));
+    return status_of(entry, x->data_ptr(), static_cast<const uint32_t*>(q->data_ptr()), s->data_ptr(), z->data_ptr(), M,
+                     N, K, static_cast<int>(group), bits, bias, static_cast<int>(act), mul, ms, res, rs, y->data_ptr(),
+                     static_cast<int>(path), ws, bytes, stream);
 }
 
 // kv_write(entry, stream, device, cache, seqs, heads, dim, k, v)
@@ -125,7 +137,7 @@ PyObject* kv_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t heads = integer(a[5], ok), dim = integer(a[6], ok);
     Tokens k, v;
     if (!ok || !tokens(a[7], heads, dim, dev, k) || !tokens(a[8], heads, dim, dev, v) || k.n != v.n) Py_RETURN_NONE;
-    return PyLong_FromLong(entry(cache, seqs, k.p, k.token, k.head, v.p, v.token, v.head, k.n, stream));
+    return status_of(entry, cache, seqs, k.p, k.token, k.head, v.p, v.token, v.head, k.n, stream);
 }
 
 // kv_read(entry, stream, device, cache, seqs, heads, dim, k, v): k or v may be None, not both
@@ -145,7 +157,7 @@ PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
             Py_RETURN_NONE;
     if (!ok || (a[7] == Py_None && a[8] == Py_None) || (a[7] != Py_None && a[8] != Py_None && t[0].n != t[1].n))
         Py_RETURN_NONE;
-    return PyLong_FromLong(entry(cache, seqs, t[0].p, t[1].p, a[7] != Py_None ? t[0].n : t[1].n, stream));
+    return status_of(entry, cache, seqs, t[0].p, t[1].p, a[7] != Py_None ? t[0].n : t[1].n, stream);
 }
 
 // kv_attention(entry, stream, device, cache, seqs, dim, q, scale, causal, window, out, lse, workspace)
@@ -171,9 +183,9 @@ PyObject* kv_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* ws;
     size_t bytes;
     if (q.heads > INT32_MAX || !workspace_of(a[12], dev, ws, bytes)) Py_RETURN_NONE;
-    return PyLong_FromLong(entry(cache, seqs, q.p, q.token, q.head, q.n, static_cast<int>(q.heads),
-                                 static_cast<float>(PyFloat_AS_DOUBLE(a[7])), a[8] == Py_True, window, o.p, o.token,
-                                 o.head, lse, ws, bytes, stream));
+    return status_of(entry, cache, seqs, q.p, q.token, q.head, q.n, static_cast<int>(q.heads),
+                     static_cast<float>(PyFloat_AS_DOUBLE(a[7])), static_cast<int>(a[8] == Py_True), window, o.p, o.token,
+                     o.head, lse, ws, bytes, stream);
 }
 
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
