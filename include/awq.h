@@ -557,6 +557,15 @@ awq_status awq_gemm_fused(const void* x_f16, const uint32_t* qweight,
                           void* stream);
 
 /*
+ * awq_gemm_fused_kernel - the kernel an awq_gemm_fused call of this shape
+ * runs when it has something to fuse: as awq_gemm_kernel, or 5 = the MFMA
+ * GEMM on its tiles for a few hundred rows; -1 when the requested path cannot
+ * take it or an argument is invalid. No GPU work.
+ */
+int awq_gemm_fused_kernel(int64_t M, int64_t N, int64_t K, int group_size, int bits, int path,
+                          int have_workspace);
+
+/*
  * A paged 8-bit key / value cache, the second tensor a decode step streams
  * beside the weights: quantized as it is written, with the symmetric map of
  * aissn.com 对称/非对称量化 (zero-point 0) and one fp32 scale per page (a

@@ -129,6 +129,8 @@ def load() -> ctypes.CDLL:
     L.awq_quantize_w8.argtypes = [c_vp, c_vp, c_i64, c_i64, c_int, c_int, c_vp, c_vp, c_vp, c_vp]
     L.awq_gemm_w8.restype = c_int
     L.awq_gemm_w8.argtypes = [c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_int, c_vp, c_int, c_vp, c_sz, c_vp]
+    L.awq_gemm_fused_kernel.restype = c_int
+    L.awq_gemm_fused_kernel.argtypes = [c_i64, c_i64, c_i64, c_int, c_int, c_int, c_int]
     L.awq_gemm_fused.restype = c_int
     L.awq_gemm_fused.argtypes = [c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_int, c_int, c_vp, c_int, c_vp, c_i64,
                                  c_vp, c_i64, c_vp, c_int, c_vp, c_sz, c_vp]
@@ -236,7 +238,7 @@ def awq_quantize(w, group_size: int = 128, channel_scale=None, out=None, symmetr
     return qweight, scales, zeros
 
 
-KERNEL_NAMES = {1: "gemv", 2: "gemm", 3: "skinny", 4: "coltile"}
+KERNEL_NAMES = {1: "gemv", 2: "gemm", 3: "skinny", 4: "coltile", 5: "gemm_small"}
 
 
 def gemm_kernel(M: int, N: int, K: int, group_size: int = 128, path: int = PATH_AUTO,
@@ -245,6 +247,16 @@ def gemm_kernel(M: int, N: int, K: int, group_size: int = 128, path: int = PATH_
     k = int(load().awq_gemm_kernel(M, N, K, group_size, path, int(workspace)))
     if k < 0:
         raise AwqError("awq_gemm_kernel", 4, "the path cannot take this shape")
+    return KERNEL_NAMES[k]
+
+
+def gemm_fused_kernel(M: int, N: int, K: int, group_size: int = 128, bits: int = 4, path: int = PATH_AUTO,
+                      workspace: bool = False) -> str:
+    """Name of the kernel awq_gemm_fused runs for this shape where it has
+    something to fuse (awq_gemm_fused_kernel)."""
+    k = int(load().awq_gemm_fused_kernel(M, N, K, group_size, bits, path, int(workspace)))
+    if k < 0:
+        raise AwqError("awq_gemm_fused_kernel", 4, "the path cannot take this shape")
     return KERNEL_NAMES[k]
 
 

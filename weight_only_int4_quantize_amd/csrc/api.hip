@@ -255,6 +255,23 @@ int choose_path(int64_t M, int64_t N, int64_t K, int group_size, int path, bool 
     return gemv_ok ? 1 : 2;
 }
 
+// The same behind an epilogue, whose GEMM has a tile for a few hundred rows
+// that also beats the skinny kernel above 32 of them.
+int choose_fused(int64_t M, int64_t N, int64_t K, int group_size, int path, bool have_workspace) {
+    const int chosen = choose_path(M, N, K, group_size, path, have_workspace);
+    if (path == 0 && chosen == 3 && M > kColTileMaxM && gemm_fused_mid(M, N, K, group_size, have_workspace)) return 2;
+    return chosen;
+}
+
+// The W8 layer's kernel (1 GEMV, 2 GEMM), or -1. The MFMA form needs 32-bit
+// byte offsets within a 256-row tile of x.
+int choose_w8(int64_t M, int64_t N, int64_t K, int path) {
+    const bool gemv_ok = gemv_supported(M, N, K, 8);
+    if (path == 1) return gemv_ok ? 1 : -1;
+    if (path == 0 && gemv_ok) return 1;
+    return K * 256 * 2 < (int64_t(1) << 31) ? 2 : -1;
+}
+
 // The linear layer behind awq_gemm_ex and awq_gemm_noalloc: checks, then
 // the kernel choice. workspace (may be NULL) feeds the skinny kernel's K
 // splits and, when split_gemm is set, the GEMM's stream-K partials. With
@@ -280,11 +297,9 @@ awq_status gemm_dispatch(const void* x_f16, const uint32_t* qweight, const void*
     const half_t* sc = static_cast<const half_t*>(scales_f16);
     const half_t* zr = static_cast<const half_t*>(zeros_f16);
     half_t* y = static_cast<half_t*>(y_f16);
-    int chosen = choose_path(M, N, K, group_size, path, workspace != nullptr || library_scratch);
+    const int chosen = epilogue ? choose_fused(M, N, K, group_size, path, workspace != nullptr)
+                                : choose_path(M, N, K, group_size, path, workspace != nullptr || library_scratch);
     if (chosen < 0) return AWQ_ERR_CONFIG;
-    if (epilogue && path == 0 && chosen == 3 && M > kColTileMaxM &&
-        gemm_fused_mid(M, N, K, group_size, workspace != nullptr))
-        chosen = 2;
     const bool use_skinny = chosen == 3;
     if (chosen == 4) return launch_coltile(x, qweight, sc, zr, M, N, K, group_size, y, stream, epilogue);
     if (chosen == 1) return launch_gemv(x, qweight, sc, zr, M, N, K, group_size, y, stream, 4, epilogue);
@@ -336,13 +351,9 @@ awq_status w8_dispatch(const void* x_f16, const uint32_t* qweight, const void* s
     const half_t* sc = static_cast<const half_t*>(scales_f16);
     const half_t* zr = static_cast<const half_t*>(zeros_f16);
     half_t* y = static_cast<half_t*>(y_f16);
-    const bool gemv_ok = gemv_supported(M, N, K, 8);
-    if (path == 1 && !gemv_ok) return AWQ_ERR_CONFIG;
-    // the MFMA form needs 32-bit byte offsets within a 256-row tile of x
-    if (path == 2 && K * 256 * 2 >= (int64_t(1) << 31)) return AWQ_ERR_CONFIG;
-    if (path == 1 || (path == 0 && gemv_ok))
-        return launch_gemv(x, qweight, sc, zr, M, N, K, group_size, y, stream, 8, epilogue);
-    if (K * 256 * 2 >= (int64_t(1) << 31)) return AWQ_ERR_SHAPE;
+    const int chosen = choose_w8(M, N, K, path);
+    if (chosen < 0) return path == 0 ? AWQ_ERR_SHAPE : AWQ_ERR_CONFIG;
+    if (chosen == 1) return launch_gemv(x, qweight, sc, zr, M, N, K, group_size, y, stream, 8, epilogue);
     if (workspace != nullptr) {
         if (reinterpret_cast<uintptr_t>(workspace) & 255) return AWQ_ERR_ALIGN;
         if (workspace_bytes < gemm_workspace_bytes(M, N)) return AWQ_ERR_WORKSPACE;
@@ -432,6 +443,16 @@ int awq_gemm_kernel(int64_t M, int64_t N, int64_t K, int group_size, int path, i
     if (check_dims(N, K, group_size) != AWQ_OK || path < 0 || path > 4) return -1;
     if (M < 1 || N < 1 || M > (int64_t(1) << 31) - 256 || N > (int64_t(1) << 31) - 256) return -1;
     return choose_path(M, N, K, group_size, path, have_workspace != 0);
+}
+
+int awq_gemm_fused_kernel(int64_t M, int64_t N, int64_t K, int group_size, int bits, int path, int have_workspace) {
+    if (check_dims(N, K, group_size) != AWQ_OK || (bits != 4 && bits != 8) || path < 0 || path > (bits == 4 ? 4 : 2))
+        return -1;
+    if (M < 1 || N < 1 || M > (int64_t(1) << 31) - 256 || N > (int64_t(1) << 31) - 256) return -1;
+    if (bits == 8 && group_size < 64) return -1;
+    const int chosen = bits == 4 ? choose_fused(M, N, K, group_size, path, have_workspace != 0)
+                                 : choose_w8(M, N, K, path);
+    return chosen == 2 && gemm_fused_mid(M, N, K, group_size, have_workspace != 0) ? 5 : chosen;
 }
 
 awq_status awq_gemm_grouped(const void* x_f16, int n_layers, const uint32_t* const* qweight,
