@@ -1081,7 +1081,10 @@ void launch_cfg(const ArgsOf<OMODE>& args, void* workspace, hipStream_t stream) 
                                static_cast<int>(tiles_n), sk);
         return;
     }
-    if constexpr (DIRECT && kHalfOut && !is_mid(GEO)) {
+    // (The narrow tile alone: r whole rounds of wide tiles and a short last one
+    // cost 20 (r + 1), the same area in narrow tiles at most 22 r + 12, so
+    // use_wide takes such a shape from r = 5 on, past the counters' 4 rounds.)
+    if constexpr (DIRECT && kHalfOut && GEO.bm == kNarrowTile.bm && GEO.bn == kNarrowTile.bn) {
         if (workspace != nullptr && use_hybrid(GEO, tiles, steps)) {
             sk.dp_tiles = static_cast<int>(tiles / resident_slots(GEO) * resident_slots(GEO));
             const int64_t tail = tiles - sk.dp_tiles;
