@@ -689,10 +689,10 @@ awq_status awq_kv_read(const awq_kv_cache* cache, const awq_kv_seqs* seqs,
  * with causal != 0 those with j <= p, and with window > 0 only the last
  * `window` of them (j > p - window). A query that sees no position gets
  * o = 0 and lse = -infinity. Logits, softmax statistics and sums are fp32;
- * the weights enter the second product as two fp16 numbers (a weight's
- * rounding and what that left). A
- * query with a NaN that sees a position gets NaN (o and lse); no other row
- * is touched by it, or by an infinity.
+ * the weights enter the second product as two fp16 numbers (a weight cut to
+ * fp16 and what that left), within 2^-20 of themselves. A query with a NaN
+ * that sees a position gets NaN (o and lse); no other row is touched by it,
+ * or by an infinity.
  *
  *   q_f16        device, fp16 [n_tokens, n_heads, head_dim], channels
  *                contiguous, 16-byte aligned, strides in halves, multiples

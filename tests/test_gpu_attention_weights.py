@@ -116,3 +116,23 @@ def test_opposite_values_cancel(fmt, dim, page, new):
         (2 * 2.0 ** -34 * float(kv_oracle.TOP[m.fmt]) * c)[..., None]
     err = np.abs(o.astype(np.float64) - eo)
     assert (err <= tol).all(), f"worst {np.max(err / tol):.3f} of the bound"
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("n_seqs,longest,new", [(1500, 40, 2), (1500, 40, 1), (6, 300, 200)])
+def test_every_weight_has_both_parts(fmt, n_seqs, longest, new):
+    """Some 2^17 weights of short sequences, where a single one that is off by
+    a step of fp16 shows in the outputs: the bound of the test above."""
+    say("weights, both parts", fmt, n_seqs, new)
+    m = Model([93], n_seqs, 1, 64, 32, fmt, longest)
+    lens = m.rng.integers(0, longest + 1, n_seqs)
+    m.append(lens)
+    count = np.minimum(lens, m.rng.integers(0, new + 1, n_seqs))
+    q = m.rng.standard_normal((int(count.sum()), 2, 64)).astype(np.float16)
+    for split in (True, False):
+        o, _, (eo, _, spread, mass) = m.attend(q, list(count), split=split)
+        e = 2 * ((m.dim + 4) * U * mass + 2.0 ** -21 + 2 * longest * U)
+        tol = (e + 2.0 ** -18)[..., None] * spread + 2.0 ** -11 * np.abs(eo) + 2.0 ** -25 + \
+            longest * 2.0 ** -34 * float(kv_oracle.TOP[fmt]) * float(m.vs.max())
+        err = np.abs(o.astype(np.float64) - eo)
+        assert (err <= tol).all(), f"worst {np.max(err / tol):.3f} of the bound"

@@ -9,11 +9,11 @@
 // of their own, M, a whole number that is at least every t + e seen by the
 // row, and f 2^(t + e - M) times a power of two (2^15 in decode, 2^12 in
 // prefill, where t + e may pass M by 3) is what enters the second product, as
-// two fp16 numbers: its rounding, and what that left. (The rounding of one
+// two fp16 numbers: it cut to fp16, and what that left. (The rounding of one
 // alone would add as much error as the output's own: 2.9e-4 of a prefill's
 // outputs against 2.07e-4, of which 2.07e-4 is the output's.) A row's largest
 // weight times scale is at least 2^13 (2^10) in these units, and what fp16's
-// subnormals lose is at most 2^-38 (2^-34) of it for each key, however far
+// subnormals lose is at most 2^-37 (2^-34) of it for each key, however far
 // the pages' scales lie apart and whatever scales the masked pages have.
 // (Both exponents stay whole where scales enter, so no bits go with them.)
 // Logits, maxima, sums and outputs are fp32.
@@ -84,16 +84,19 @@ __device__ inline float across_quarters_max(float v) {
     return larger_of(__builtin_amdgcn_permlane16_swap(u, u, false, false));
 }
 
-// Two numbers to fp16, toward zero (one instruction; the nearest takes three).
-__device__ inline half2_t toward_zero(float a, float b) {
-    return __builtin_bit_cast(half2_t, __builtin_amdgcn_cvt_pkrtz(a, b));
-}
-
-// r = w - hi, exact (one instruction for each; a conversion and a difference
-// otherwise).
-__device__ inline void less_half(const float (&w)[2], half2_t hi, float (&r)[2]) {
-    asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel:[0,0,0] op_sel_hi:[1,0,0]" : "=v"(r[0]) : "v"(hi), "v"(w[0]));
-    asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(r[1]) : "v"(hi), "v"(w[1]));
+// Two weights as two fp16 numbers each, both toward zero: hi + lo is within
+// 2^-20 of the weight. The rounding is one instruction for the pair (to the
+// nearest it takes three), the difference, exact, one each. Written out as
+// w - float(half(w)) with w a product, it went wrong: the compiler rounded
+// the exact product for the difference and the rounded one for the operand,
+// which differ by a step of fp16 at ties, so that one weight in some 2^14
+// was off by 2^-11 of itself.
+__device__ inline void two_parts(float w0, float w1, half2_t& hi, half2_t& lo) {
+    hi = __builtin_bit_cast(half2_t, __builtin_amdgcn_cvt_pkrtz(w0, w1));
+    float r0, r1;
+    asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel:[0,0,0] op_sel_hi:[1,0,0]" : "=v"(r0) : "v"(hi), "v"(w0));
+    asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(r1) : "v"(hi), "v"(w1));
+    lo = __builtin_bit_cast(half2_t, __builtin_amdgcn_cvt_pkrtz(r0, r1));
 }
 
 // The positions rows [row0, row0 + rows) of a kv head see.
@@ -277,10 +280,10 @@ __device__ inline void finish_rows(const KvAttentionArgs& a, const KvSeq& sq, co
 // 8, 680 MB, 126-134 us, 5.1-5.4 TB/s, the ragged lengths leaving few waves
 // at the end; 32 of 2048 down, 32 heads, 63 us, 5.4 TB/s; 2 of 131072 and
 // 81920 (e4m3, 8 heads) 84-88 us, 5.0-5.2 TB/s; a plain read reaches 6.1 to
-// 6.2. Two blocks per CU at 128 channels (190 VGPRs); holding them to 168 for
-// a third spilled and was slower (139 against 134 us), non-temporal loads
-// gained 7% on the 680 MB case and lost as much on caches that the 256 MB
-// last-level cache holds.
+// 6.2. The 163 VGPRs at 128 channels leave room for three blocks per CU, where
+// 190 left two: no difference was measured. Non-temporal loads gained 7% on
+// the 680 MB case and lost as much on caches that the 256 MB last-level cache
+// holds.
 constexpr int kDecodeRows = 16;
 constexpr int kDecodeWaves = 4;
 constexpr int kTile = 64;
@@ -464,11 +467,17 @@ __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 64 ? 4 : D <= 96 ? 3 : D 
             half8_t pf[2], pl[2];
             float part = 0.f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float p = __builtin_amdgcn_exp2f(s[i] + shift), w = p * vm;
-                part += p;
-                pf[i >> 3][i & 7] = static_cast<half_t>(w);
-                pl[i >> 3][i & 7] = static_cast<half_t>(w - static_cast<float>(pf[i >> 3][i & 7]));
+            for (int i = 0; i < 16; i += 2) {
+                const float p0 = __builtin_amdgcn_exp2f(s[i] + shift), p1 = __builtin_amdgcn_exp2f(s[i + 1] + shift);
+                part += p0;
+                part += p1;
+                half2_t hi, lo;
+                two_parts(p0 * vm, p1 * vm, hi, lo);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    pf[i >> 3][(i & 7) + j] = hi[j];
+                    pl[i >> 3][(i & 7) + j] = lo[j];
+                }
             }
             sum = __builtin_fmaf(part, __builtin_amdgcn_exp2f(on - mn - (ve + kWeightUnit)), sum * shrink);
             m = mn;
@@ -762,15 +771,14 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv_pre
             float part = 0.f;
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
-                float w[2], r[2];
+                float w[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     w[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][e + j], ksc[u], shift));
                     part += w[j];
                 }
-                const half2_t hi = toward_zero(w[0], w[1]);
-                less_half(w, hi, r);
-                const half2_t lo = toward_zero(r[0], r[1]);
+                half2_t hi, lo;
+                two_parts(w[0], w[1], hi, lo);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     pf[e >> 3][(e & 7) + j] = hi[j];
@@ -850,8 +858,7 @@ struct Plan {
 
 // Up to 32 query rows per kv head go to the decode kernel, longer runs to the
 // prefill kernel. The keys are split until the blocks fill the GPU: two
-// blocks per CU (what the decode kernel's registers allow at 128 channels) of
-// at least 1024 positions, which cover what a block costs apart from its
+// blocks per CU of at least 1024 positions, which cover what a block costs apart from its
 // tiles (some 8 us: its first loads, and the join); short launches of under a
 // block per CU split down to 256 positions, a tile per wave. Measured (us):
 // 16 x 4096 tokens, 4 heads of 256: 23 at 1024 positions, 33 at 512, 45 at
