@@ -623,6 +623,9 @@ typedef struct {
  *   max_len      at least every kv_len[b]; at most 2^31 - 1024
  * max_tokens and max_len only size the launch (the lengths themselves are
  * read on the device, so a captured graph can be replayed with new ones).
+ * awq_kv_attention splits max_len over the GPU, so with a bound far above the
+ * lengths few blocks have keys and the call is slower; a window does not
+ * narrow the split either.
  * Whatever the arrays hold, no access leaves the tensors: a kv_len past
  * max_len counts as max_len, and new tokens past max_tokens (from a
  * sequence's first new one on, rounded up to whole pages) are not processed.

@@ -646,7 +646,7 @@ def awq_gemm_fused(x, qweight, scales, zeros, group_size: int = 128, bias=None, 
     """awq_gemm_fused: y = act(x . dequant(Wq)^T + bias) * mul + residual in
     one launch, INT4 or W8 weights by qweight's width (K / 8 or K / 4 words).
 
-    bias fp16 [N]; mul and residual fp16 [M, N], rows any stride apart;
+    bias fp16 [N]; mul and residual fp16 [M, N], rows N halves or more apart;
     activation one of ACTIVATIONS. out may be residual or mul itself (when
     packed). workspace: gemm_workspace(M, N, K)."""
     act = ACTIVATIONS.get(activation)
