@@ -566,35 +566,56 @@ int awq_gemm_fused_kernel(int64_t M, int64_t N, int64_t K, int group_size, int b
                           int have_workspace);
 
 /*
- * A paged 8-bit key / value cache, the second tensor a decode step streams
- * beside the weights: quantized as it is written, with the symmetric map of
+ * A paged key / value cache, the second tensor a decode step streams beside
+ * the weights: quantized as it is written, to 8 bits with the symmetric map of
  * aissn.com 对称/非对称量化 (zero-point 0) and one fp32 scale per page (a
  * block of page_size consecutive tokens of one sequence) and head, for keys
  * and for values (the granularity of xxmr.cn §1.4, a block in place of a
- * weight group).
+ * weight group); or to 4 bits, asymmetric, in the finer groups that 16 levels
+ * need.
  *
  *   format       AWQ_KV_INT8: code = rint(v / s) in -127..127, stored as the
  *                byte code + 128; s = max|v| / 127
  *                AWQ_KV_E4M3: the OCP fp8 (1-4-3) value of v / s, rounded to
  *                nearest even; s = max|v| / 448
+ *                AWQ_KV_INT4: code = rint((v - lo) / s) in 0..15, lo the
+ *                smallest number of its group and s a fifteenth of the group's
+ *                range, both fp16; the group is 32 channels of a token for
+ *                keys (a few channels of a key are much larger than the
+ *                others), a token's head for values. The cached number is
+ *                fp16(lo + s * code), rounded once.
  *   n_pages      pages the tensors hold, 1 .. 2^31 - 1
  *   n_kv_heads   1 .. 65535
  *   page_size    32, 64, 128 or 256 tokens
  *   head_dim     64, 96, 128, 192 or 256 channels
+ * INT8 and E4M3:
  *   k_codes      device, uint8 [n_pages, n_kv_heads, head_dim / 16, page_size,
  *                16]: 16 consecutive channels of a token are adjacent
  *   v_codes      device, uint8 [n_pages, n_kv_heads, page_size / 16, head_dim,
  *                16]: 16 consecutive tokens of a channel are adjacent
- *   k_scales, v_scales   device, fp32 [n_pages, n_kv_heads], 0 .. 65504
- * Codes 16-byte aligned, scales 4-byte aligned. A page need not be
- * initialised before the first write to it.
+ *   k_scales, v_scales   device, fp32 [n_pages, n_kv_heads], 0 .. 65504,
+ *                4-byte aligned
+ * INT4:
+ *   k_codes      device, uint8 [n_pages, n_kv_heads, head_dim / 32, page_size,
+ *                16]: the codes of 32 consecutive channels of a token; of eight
+ *                consecutive ones, in 4 bytes, number 2 j is in bits 4 j .. and
+ *                number 2 j + 1 in bits 16 + 4 j ..
+ *   v_codes      device, uint8 [n_pages, n_kv_heads, page_size / 32, head_dim,
+ *                16]: the codes of 32 consecutive tokens of a channel, so too
+ *   k_scales     device, fp16 [n_pages, n_kv_heads, head_dim / 32, page_size,
+ *                2]: (s, lo)
+ *   v_scales     device, fp16 [n_pages, n_kv_heads, 2, page_size]: every
+ *                token's s, then every token's lo
+ *                both 16-byte aligned
+ * Codes 16-byte aligned. A page need not be initialised before the first write
+ * to it.
  */
-enum { AWQ_KV_INT8 = 0, AWQ_KV_E4M3 = 1 };
+enum { AWQ_KV_INT8 = 0, AWQ_KV_E4M3 = 1, AWQ_KV_INT4 = 4 };
 typedef struct {
     void* k_codes;
     void* v_codes;
-    float* k_scales;
-    float* v_scales;
+    void* k_scales;
+    void* v_scales;
     int64_t n_pages;
     int n_kv_heads;
     int page_size;
@@ -628,7 +649,8 @@ typedef struct {
  * narrow the split either.
  * Whatever the arrays hold, no access leaves the tensors: a kv_len past
  * max_len counts as max_len, and new tokens past max_tokens (from a
- * sequence's first new one on, rounded up to whole pages) are not processed.
+ * sequence's first new one on, rounded up to whole pages, or to 32 tokens with
+ * AWQ_KV_INT4) are not processed.
  */
 typedef struct {
     const int32_t* block_table;
@@ -654,6 +676,12 @@ typedef struct {
  * half a step of the page's final scale for its own rounding and for each
  * later growth of its page's scale (int8; relative 2^-4 each in e4m3); a
  * prompt written in one call is rounded once.
+ * AWQ_KV_INT4, for every new token and group (32 channels of a key; the head
+ * of a value), in float32:
+ *   lo = min x,  s = the largest fp16 number not above (max x - lo) / 15
+ *   codes = clamp(round((x - lo) / s), 0, 15), 0 where s is 0
+ * A number thus carries at most half a step (plus 15 times what s was cut by,
+ * under 2^-10 of it, at the top of the range); what was written before stays.
  * NaN is stored as 0, an infinity as +-65504.
  *
  *   k_f16, v_f16     device, fp16 [n_tokens, n_kv_heads, head_dim], the
@@ -672,7 +700,8 @@ awq_status awq_kv_write(const awq_kv_cache* cache, const awq_kv_seqs* seqs,
 
 /*
  * awq_kv_read - the sequences' newest tokens (all of a sequence when
- * cu_tokens counts kv_len tokens for it) back as fp16(code * scale).
+ * cu_tokens counts kv_len tokens for it) back as fp16(code * scale), or as the
+ * cached numbers fp16(lo + s * code) of AWQ_KV_INT4.
  *
  *   k_f16, v_f16     device, fp16 [n_tokens, n_kv_heads, head_dim], packed,
  *                    16-byte aligned (outputs). Either may be NULL. Rows of
@@ -727,6 +756,127 @@ awq_status awq_kv_attention(const awq_kv_cache* cache, const awq_kv_seqs* seqs,
                             int64_t n_tokens, int n_heads, float scale, int causal, int64_t window,
                             void* out_f16, int64_t out_token_stride, int64_t out_head_stride,
                             float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * awq_rmsnorm - root-mean-square norm of the residual stream, with the sum
+ * that makes it: per row, in float32,
+ *   h = x + residual,  residual_out = fp16(h)
+ *   y = h * (weight_offset + weight) / sqrt(mean(h^2) + eps)
+ * y is taken from h, not from the rounded sum, and rounded once: to fp16, or
+ * to 8 bits by a row's or a group's scale,
+ *   a = max(max |y|, 1e-5),  s = a / top,  code = round(y * (1 / s))
+ * with top = 127 (int8, round-half-to-even) or 448 (OCP fp8 1-4-3). A row or
+ * group with a NaN among its y has the scale NaN and codes 0; with fp16 the
+ * elements are what the formula gives.
+ *
+ *   x_f16          device, fp16 [rows, width], rows x_stride halves apart
+ *   residual_f16   device, fp16 [rows, width] or NULL (h = x)
+ *   residual_out   device, fp16 [rows, width] or NULL (output; may be x_f16 or
+ *                  residual_f16 itself, with the same stride)
+ *   weight_f16     device, fp16 [width] or NULL (y = h / sqrt(..))
+ *   weight_offset  finite; 0, or 1 where the stored weight is the difference
+ *                  from 1
+ *   eps            finite, >= 0
+ *   rows, width    rows >= 0, 1 <= width <= 2^24
+ *   format         AWQ_NORM_F16, _INT8 (signed bytes) or _E4M3
+ *   group_size     0 (one scale a row), or 32, 64, 128, 256 or 512 channels
+ *                  with width % group_size == 0; 0 with AWQ_NORM_F16
+ *   out            device, [rows, width] of the format (output), rows
+ *                  out_stride elements apart. fp16 may be x_f16 or residual_f16
+ *                  itself (same stride) if residual_out is not that tensor.
+ *   scales         device, fp32 [rows, width / group_size or 1], packed
+ *                  (output); ignored with AWQ_NORM_F16
+ * fp16 pointers 2-byte, scales 4-byte aligned: rows need no alignment (16-byte
+ * aligned ones are a little faster). Strides >= 0 for x and residual, >= width
+ * for the outputs, and below 2^40. Outputs must not overlap inputs otherwise.
+ * Asynchronous on `stream`; results are the same on every run.
+ */
+enum { AWQ_NORM_F16 = 0, AWQ_NORM_INT8 = 1, AWQ_NORM_E4M3 = 2 };
+awq_status awq_rmsnorm(const void* x_f16, int64_t x_stride,
+                       const void* residual_f16, int64_t residual_stride,
+                       void* residual_out_f16, int64_t residual_out_stride,
+                       const void* weight_f16, float weight_offset, float eps,
+                       int64_t rows, int64_t width, int format, int group_size,
+                       void* out, int64_t out_stride, float* scales, void* stream);
+
+/*
+ * awq_rope_frequencies - the frequencies of rotary positions, radians per
+ * position, for rotary_dim / 2 pairs of channels:
+ *   f_i = base^(-2 i / rotary_dim)
+ * stretched by `factor` for contexts past the trained length:
+ *   AWQ_ROPE_NONE        as they are (the other arguments are ignored)
+ *   AWQ_ROPE_LINEAR      f_i / factor (positions interpolated)
+ *   AWQ_ROPE_NTK         base * factor^(R / (R - 2)), R = rotary_dim > 2
+ *   AWQ_ROPE_YARN        f_i / factor for pairs that turn less than `low` times
+ *                        over the trained length, f_i for more than `high`
+ *                        times, a linear ramp over the pairs between; the
+ *                        rotated numbers times 0.1 ln(factor) + 1. The pair
+ *                        that turns n times is number
+ *                        R ln(L / (2 pi n)) / (2 ln base); the ramp's ends are
+ *                        rounded outwards to whole pairs.
+ *   AWQ_ROPE_WAVELENGTH  f_i / factor at L / wavelength <= low, f_i at >= high,
+ *                        linear in that quotient between
+ *
+ *   rotary_dim   even, 2 .. 4096
+ *   base         > 1
+ *   factor       >= 1
+ *   trained_len  L, > 0 (YARN, WAVELENGTH)
+ *   low, high    0 < low < high (YARN, WAVELENGTH; 1 and 32, 1 and 4 are usual)
+ *   freqs        host, double [rotary_dim / 2] (output)
+ *   amplitude    host, double (output): 1, or YARN's factor
+ * Host arithmetic only; no GPU work.
+ */
+enum { AWQ_ROPE_NONE = 0, AWQ_ROPE_LINEAR = 1, AWQ_ROPE_NTK = 2, AWQ_ROPE_YARN = 3, AWQ_ROPE_WAVELENGTH = 4 };
+awq_status awq_rope_frequencies(int rotary_dim, double base, int scaling, double factor,
+                                double trained_len, double low, double high,
+                                double* freqs, double* amplitude);
+
+/*
+ * awq_rope - rotates queries and keys by their positions, in one launch: with
+ * c = cos(p f_i), s = sin(p f_i) of a token at position p,
+ *   (a, b) -> amplitude * (a c - b s, b c + a s)
+ * for the pairs i of every head, (a, b) = channels (i, i + rotary_dim / 2) with
+ * AWQ_ROPE_HALF, (2 i, 2 i + 1) with AWQ_ROPE_INTERLEAVED. Channels from
+ * rotary_dim on pass unchanged. The angle is reduced to a part of a turn in
+ * float64, so far positions lose nothing; the rotation is float32, rounded to
+ * fp16 once. A negative position turns back.
+ *
+ *   rope         frequencies device, double [rotary_dim / 2]
+ *   positions    device, int32 [n_tokens]; or NULL, and
+ *   seqs         a batch whose rows cu_tokens[b] .. are the newest tokens of
+ *                sequences of kv_len[b] tokens, as for awq_kv_write (the block
+ *                table is not used; kv_len past max_len counts as it, new
+ *                tokens past max_tokens are not processed). Rows of no
+ *                sequence are left as they were. Exactly one of the two.
+ *   q, k         tensors [n_tokens, heads, head_dim] in fp16, channels
+ *                contiguous, strides in halves; heads 0 (or a NULL pointer to
+ *                the struct): none. out may be in itself, with the same
+ *                strides; otherwise it must not overlap an input, and all of a
+ *                row is written.
+ *   head_dim     rotary_dim <= head_dim <= 4096
+ *   n_tokens     0 .. 2^24 - 1
+ * Pointers 2-byte aligned (rows need no alignment; 16-byte aligned ones are
+ * faster). Strides >= 0 for in; for out no two rows may share memory: each
+ * stride at least head_dim, one of them past all the other's rows.
+ * Asynchronous on `stream`.
+ */
+enum { AWQ_ROPE_HALF = 0, AWQ_ROPE_INTERLEAVED = 1 };
+typedef struct {
+    const double* freqs;
+    int rotary_dim;
+    int layout;
+    float amplitude;
+} awq_rope_table;
+typedef struct {
+    const void* in;
+    void* out;
+    int64_t in_token_stride, in_head_stride;
+    int64_t out_token_stride, out_head_stride;
+    int heads;
+} awq_rope_heads;
+awq_status awq_rope(const awq_rope_table* rope, const int32_t* positions, const awq_kv_seqs* seqs,
+                    const awq_rope_heads* q, const awq_rope_heads* k, int head_dim, int64_t n_tokens,
+                    void* stream);
 
 #ifdef __cplusplus
 }

@@ -13,9 +13,12 @@ Entry points (same names as the C ABI in include/awq.h):
     awq_scale_search(w, x, group_size=128, alphas=None) -> losses, best_index, best_scales
     awq_gemm_fused(x, qweight, scales, zeros, group_size=128, bias=None, activation="none", mul=None,
         residual=None) -> y
+    awq_rmsnorm(x, weight=None, eps=1e-5, residual=None, residual_out=None, fmt=None, group_size=0)
+        -> y, or codes, scales
+    awq_rope(q, k, rope, positions=None, seqs=None) -> q, k   (frequencies: Rope)
     awq_kv_write(cache, seqs, k, v), awq_kv_read(cache, seqs) -> k, v
     awq_kv_attention(q, cache, seqs) -> out
-        (a paged 8-bit cache, KVCache, and a batch of sequences over it, KVSeqs)
+        (a paged 8-bit or 4-bit cache, KVCache, and a batch of sequences over it, KVSeqs)
 """
 
 from __future__ import annotations
@@ -38,9 +41,23 @@ PATH_AUTO, PATH_GEMV, PATH_GEMM, PATH_SKINNY, PATH_COLTILE = 0, 1, 2, 3, 4
 QUANT_ASYMMETRIC, QUANT_SYMMETRIC = 0, 1
 
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
-KV_FORMATS = {"int8": 0, "e4m3": 1}
+KV_FORMATS = {"int8": 0, "e4m3": 1, "int4": 4}
+NORM_FORMATS = {None: 0, "int8": 1, "e4m3": 2}
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "wavelength": 4}
 
 _lib = None
+
+
+class _RopeTableStruct(ctypes.Structure):
+    _fields_ = [("freqs", ctypes.c_void_p), ("rotary_dim", ctypes.c_int), ("layout", ctypes.c_int),
+                ("amplitude", ctypes.c_float)]
+
+
+class _RopeHeadsStruct(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("in_token_stride", ctypes.c_int64),
+                ("in_head_stride", ctypes.c_int64), ("out_token_stride", ctypes.c_int64),
+                ("out_head_stride", ctypes.c_int64), ("heads", ctypes.c_int)]
 
 
 class _KVCacheStruct(ctypes.Structure):
@@ -143,6 +160,14 @@ def load() -> ctypes.CDLL:
     L.awq_kv_attention.restype = c_int
     L.awq_kv_attention.argtypes = [c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_int, ctypes.c_float, c_int, c_i64,
                                    c_vp, c_i64, c_i64, c_vp, c_vp, c_sz, c_vp]
+    c_d, c_f = ctypes.c_double, ctypes.c_float
+    L.awq_rmsnorm.restype = c_int
+    L.awq_rmsnorm.argtypes = [c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_f, c_f, c_i64, c_i64, c_int, c_int, c_vp,
+                              c_i64, c_vp, c_vp]
+    L.awq_rope_frequencies.restype = c_int
+    L.awq_rope_frequencies.argtypes = [c_int, c_d, c_int, c_d, c_d, c_d, c_d, c_vp, c_vp]
+    L.awq_rope.restype = c_int
+    L.awq_rope.argtypes = [c_vp, c_vp, c_vp, c_vp, c_vp, c_int, c_i64, c_vp]
     _lib = L
     return L
 
@@ -621,7 +646,7 @@ def _rows(name: str, t, shape, dtype, index: int):
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     row, col = t.stride()
-    if shape[1] > 1 and col != 1:
+    if shape[0] > 0 and shape[1] > 1 and col != 1:
         raise ValueError(f"{name}'s rows must be contiguous")
     return t.data_ptr(), row if shape[0] > 1 else shape[1]
 
@@ -706,47 +731,62 @@ def awq_gemm_fused(x, qweight, scales, zeros, group_size: int = 128, bias=None, 
     return out
 
 
-# ---------------------------------------------------------------- the paged 8-bit key / value cache
+# ---------------------------------------------------------------- the paged key / value cache
+
+def _kv_shapes(fmt: str, pages: int, heads: int, dim: int, page: int):
+    """Shapes of a cache's k_codes, v_codes, k_scales and v_scales."""
+    if fmt == "int4":
+        return ((pages, heads, dim // 32, page, 16), (pages, heads, page // 32, dim, 16),
+                (pages, heads, dim // 32, page, 2), (pages, heads, 2, page))
+    return ((pages, heads, dim // 16, page, 16), (pages, heads, page // 16, dim, 16), (pages, heads), (pages, heads))
+
 
 class KVCache:
-    """A paged 8-bit key / value cache (awq_kv_cache): the caller's tensors
-    k_codes uint8 [pages, heads, D / 16, page, 16], v_codes uint8 [pages,
-    heads, page / 16, D, 16], k_scales and v_scales fp32 [pages, heads];
-    fmt "int8" or "e4m3". KVCache.empty allocates them."""
+    """A paged key / value cache (awq_kv_cache) over the caller's tensors.
+    fmt "int8" or "e4m3": k_codes uint8 [pages, heads, D / 16, page, 16],
+    v_codes uint8 [pages, heads, page / 16, D, 16], k_scales and v_scales fp32
+    [pages, heads]. fmt "int4": k_codes uint8 [pages, heads, D / 32, page, 16],
+    v_codes uint8 [pages, heads, page / 32, D, 16], k_scales fp16 [pages,
+    heads, D / 32, page, 2], v_scales fp16 [pages, heads, 2, page].
+    KVCache.empty allocates them."""
 
     def __init__(self, k_codes, v_codes, k_scales, v_scales, fmt: str = "int8"):
         torch = _torch()
         if fmt not in KV_FORMATS:
             raise ValueError(f"fmt must be one of {sorted(KV_FORMATS)}")
+        unit, scale = (32, torch.float16) if fmt == "int4" else (16, torch.float32)
         _need_gpu("k_codes", k_codes, torch.uint8)
         _need_gpu("v_codes", v_codes, torch.uint8)
-        _need_gpu("k_scales", k_scales, torch.float32)
-        _need_gpu("v_scales", v_scales, torch.float32)
+        _need_gpu("k_scales", k_scales, scale)
+        _need_gpu("v_scales", v_scales, scale)
         if k_codes.dim() != 5 or k_codes.shape[4] != 16:
-            raise ValueError("k_codes must be [pages, heads, D / 16, page, 16]")
+            raise ValueError(f"k_codes must be [pages, heads, D / {unit}, page, 16]")
         pages, heads, dc, page, _ = k_codes.shape
-        if tuple(v_codes.shape) != (pages, heads, page // 16, dc * 16, 16) or page % 16:
-            raise ValueError(f"v_codes must be [{pages}, {heads}, page / 16, {dc * 16}, 16]")
-        if tuple(k_scales.shape) != (pages, heads) or tuple(v_scales.shape) != (pages, heads):
-            raise ValueError(f"k_scales and v_scales must be [{pages}, {heads}]")
+        _, v_shape, ks_shape, vs_shape = _kv_shapes(fmt, pages, heads, dc * unit, page)
+        if tuple(v_codes.shape) != v_shape or page % unit:
+            raise ValueError(f"v_codes must be [{pages}, {heads}, page / {unit}, {dc * unit}, 16]")
+        if tuple(k_scales.shape) != ks_shape or tuple(v_scales.shape) != vs_shape:
+            raise ValueError(f"k_scales and v_scales must be {list(ks_shape)} and {list(vs_shape)}")
         if len({t.device for t in (k_codes, v_codes, k_scales, v_scales)}) != 1:
             raise ValueError("the cache's tensors must be on one device")
         self.k_codes, self.v_codes, self.k_scales, self.v_scales, self.fmt = k_codes, v_codes, k_scales, v_scales, fmt
-        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = pages, heads, page, dc * 16
+        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = pages, heads, page, dc * unit
         self.device, self.index, self.half = k_codes.device, k_codes.get_device(), torch.float16
         self._struct = _KVCacheStruct(_ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), pages, heads, page,
-                                      dc * 16, KV_FORMATS[fmt])
+                                      dc * unit, KV_FORMATS[fmt])
         self._ref = ctypes.addressof(self._struct)
 
     @classmethod
     def empty(cls, n_pages: int, n_kv_heads: int, head_dim: int, page_size: int = 64, fmt: str = "int8", device=None):
         """A cache of n_pages pages that hold nothing yet."""
         torch = _torch()
+        if fmt not in KV_FORMATS:
+            raise ValueError(f"fmt must be one of {sorted(KV_FORMATS)}")
         dev = device or "cuda"
-        return cls(torch.empty((n_pages, n_kv_heads, head_dim // 16, page_size, 16), dtype=torch.uint8, device=dev),
-                   torch.empty((n_pages, n_kv_heads, page_size // 16, head_dim, 16), dtype=torch.uint8, device=dev),
-                   torch.zeros((n_pages, n_kv_heads), dtype=torch.float32, device=dev),
-                   torch.zeros((n_pages, n_kv_heads), dtype=torch.float32, device=dev), fmt)
+        kc, vc, ks, vs = _kv_shapes(fmt, n_pages, n_kv_heads, head_dim, page_size)
+        scale = torch.float16 if fmt == "int4" else torch.float32
+        return cls(torch.empty(kc, dtype=torch.uint8, device=dev), torch.empty(vc, dtype=torch.uint8, device=dev),
+                   torch.zeros(ks, dtype=scale, device=dev), torch.zeros(vs, dtype=scale, device=dev), fmt)
 
 
 class KVSeqs:
@@ -1000,3 +1040,216 @@ def awq_kv_attention(q, cache: KVCache, seqs: KVSeqs, scale: float | None = None
     if st != AWQ_OK:
         _check("awq_kv_attention", st)
     return out
+
+
+# ---------------------------------------------------------------- the norm
+
+_more = None           # addresses of the entry points below, for the call extension
+
+
+def _more_calls():
+    global _more
+    _more = {n: ctypes.cast(getattr(load(), "awq_" + n), ctypes.c_void_p).value for n in ("rmsnorm", "rope")}
+    return _more
+
+
+def _norm_dtype(fmt):
+    torch = _torch()
+    return {None: torch.float16, "int8": torch.int8, "e4m3": torch.float8_e4m3fn}[fmt]
+
+
+def awq_rmsnorm(x, weight=None, eps: float = 1e-5, residual=None, residual_out=None, weight_offset: float = 0.0,
+                fmt: str | None = None, group_size: int = 0, out=None, scales=None):
+    """awq_rmsnorm: y = h * (weight_offset + weight) / sqrt(mean(h^2) + eps) of
+    the rows h = x + residual (fp16 [T, K], contiguous rows; x alone without a
+    residual), weight fp16 [K] or none.
+
+    residual_out fp16 [T, K], when given, receives h; it may be residual or x
+    itself. fmt None gives y in fp16; "int8" or "e4m3" give (codes, scales),
+    codes torch.int8 or torch.float8_e4m3fn [T, K], scales fp32 [T, 1], or
+    [T, K / group_size] with a group size of 32 .. 512 channels. out and scales:
+    tensors to fill; a fp16 out may be x or residual itself."""
+    code = NORM_FORMATS.get(fmt)
+    if code is None:
+        raise ValueError("fmt must be None, 'int8' or 'e4m3'")
+    torch = _torch()
+    index = -1
+    if out is None or (code and scales is None):
+        _need_rows("x", x, torch.float16)
+        if out is None:
+            out = torch.empty(x.shape, dtype=_norm_dtype(fmt), device=x.device)
+        if code and scales is None:
+            n = x.shape[1] // group_size if isinstance(group_size, int) and group_size > 0 else 1
+            scales = torch.empty((x.shape[0], n), dtype=torch.float32, device=x.device)
+    ext = (_fast or _fast_calls())[0]
+    if ext is not None:
+        try:
+            index = x.get_device()
+            stream = _stream_on(index)
+        except (AttributeError, TypeError, RuntimeError):
+            stream = None
+        if stream is not None and hasattr(ext, "rmsnorm"):
+            st = ext.rmsnorm((_more or _more_calls())["rmsnorm"], stream, index, x, weight, eps, residual, residual_out,
+                             weight_offset, code, group_size, out, scales)
+            if st == AWQ_OK:
+                return (out, scales) if code else out
+            if st is not None:
+                _check("awq_rmsnorm", st)
+    half = torch.float16
+    _need_rows("x", x, half)
+    index, (T, K) = x.get_device(), x.shape
+    if not isinstance(group_size, int):
+        raise TypeError("group_size must be an int")
+    if weight is not None:
+        _need_on("weight", weight, half, index)
+        if tuple(weight.shape) != (K,):
+            raise ValueError(f"weight must be [{K}]")
+    ptr = {}
+    for name, t, dtype in (("x", x, half), ("residual", residual, half), ("residual_out", residual_out, half),
+                           ("out", out, _norm_dtype(fmt))):
+        ptr[name] = _rows(name, t, x.shape, dtype, index)
+    if code:
+        n = K // group_size if group_size > 0 else 1
+        _need_on("scales", scales, torch.float32, index)
+        if tuple(scales.shape) != (T, n):
+            raise ValueError(f"scales must be [{T}, {n}]")
+    st = _on_device(index, (_lib or load()).awq_rmsnorm, *ptr["x"], *ptr["residual"], *ptr["residual_out"], _ptr(weight),
+                    float(weight_offset), float(eps), T, K, code, group_size, *ptr["out"], _ptr(scales) if code else None)
+    if st != AWQ_OK:
+        _check("awq_rmsnorm", st)
+    return (out, scales) if code else out
+
+
+def _need_rows(name: str, t, dtype) -> None:
+    """Raises what is wrong with t as a 2-D GPU tensor of dtype."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a GPU tensor (no CPU path exists)")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D [rows, width]")
+
+
+# ---------------------------------------------------------------- rotary positions
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     trained_len: float = 0.0, low: float | None = None, high: float | None = None):
+    """awq_rope_frequencies: (a list of rotary_dim / 2 frequencies in radians
+    per position, the amplitude). scaling one of ROPE_SCALINGS; low and high
+    default to 1 and 32 for "yarn", 1 and 4 for "wavelength"."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+    low = 1.0 if low is None else float(low)
+    high = (32.0 if scaling == "yarn" else 4.0) if high is None else float(high)
+    n = rotary_dim // 2 if isinstance(rotary_dim, int) and 2 <= rotary_dim <= 4096 else 1
+    freqs, amplitude = (ctypes.c_double * n)(), ctypes.c_double()
+    _check("awq_rope_frequencies", load().awq_rope_frequencies(rotary_dim, float(base), ROPE_SCALINGS[scaling],
+                                                               float(factor), float(trained_len), low, high, freqs,
+                                                               ctypes.byref(amplitude)))
+    return list(freqs), amplitude.value
+
+
+class Rope:
+    """The frequencies of rotary positions on a GPU (awq_rope_table): a head's
+    first rotary_dim channels turn, paired as layout says ("half": i and
+    i + rotary_dim / 2, "interleaved": 2 i and 2 i + 1). The other arguments are
+    rope_frequencies'. Rope.of takes frequencies of any other kind."""
+
+    def __init__(self, rotary_dim: int, base: float = 10000.0, layout: str = "half", scaling: str = "none",
+                 factor: float = 1.0, trained_len: float = 0.0, low: float | None = None, high: float | None = None,
+                 device=None):
+        torch = _torch()
+        freqs, amplitude = rope_frequencies(rotary_dim, base, scaling, factor, trained_len, low, high)
+        self._set(torch.tensor(freqs, dtype=torch.float64, device=device or "cuda"), layout, amplitude)
+
+    @classmethod
+    def of(cls, freqs, layout: str = "half", amplitude: float = 1.0):
+        """From a GPU tensor of frequencies, fp64 [rotary_dim / 2]."""
+        self = cls.__new__(cls)
+        self._set(freqs, layout, amplitude)
+        return self
+
+    def _set(self, freqs, layout, amplitude):
+        torch = _torch()
+        if layout not in ROPE_LAYOUTS:
+            raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}")
+        _need_gpu("freqs", freqs, torch.float64)
+        if freqs.dim() != 1 or freqs.numel() < 1:
+            raise ValueError("freqs must be [rotary_dim / 2]")
+        self.freqs, self.layout, self.amplitude, self.rotary_dim = freqs, layout, float(amplitude), 2 * freqs.numel()
+        self.device, self.index = freqs.device, freqs.get_device()
+        self._struct = _RopeTableStruct(_ptr(freqs), self.rotary_dim, ROPE_LAYOUTS[layout], self.amplitude)
+        self._ref = ctypes.addressof(self._struct)
+
+
+def _rope_tensor(name: str, t, rope, like=None):
+    """Checks t as fp16 [T, heads, D] with contiguous channels on the table's
+    device, of like's shape if given."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.float16:
+        raise TypeError(f"{name} must be torch.float16, got {t.dtype}")
+    if t.get_device() != rope.index:
+        raise ValueError(f"{name} must be on {rope.device}")
+    if t.dim() != 3 or (like is not None and t.shape != like.shape):
+        raise ValueError(f"{name} must be [tokens, heads, D]" if like is None else f"{name} must be {list(like.shape)}")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}'s channels must be contiguous")
+
+
+def awq_rope(q, k, rope: Rope, positions=None, seqs: KVSeqs | None = None, out=None):
+    """awq_rope: queries and keys (fp16 [T, heads, D], any token and head
+    strides; either may be None) rotated by their positions, int32 [T], or by
+    those of the newest tokens of a batch, seqs. Returns (q, k).
+
+    out: the two tensors to fill, (q, k) itself for in place. Without it new
+    ones, in which the rows of no sequence are 0."""
+    torch = _torch()
+    if out is None:
+        make = torch.zeros_like if seqs is not None else torch.empty_like
+        out = tuple(None if t is None else make(t, memory_format=torch.contiguous_format) for t in (q, k))
+    qo, ko = out
+    ext = (_fast or _fast_calls())[0]
+    stream = _stream_on(rope.index) if ext is not None else None
+    if stream is not None and hasattr(ext, "rope") and (seqs is None or seqs.index == rope.index):
+        st = ext.rope((_more or _more_calls())["rope"], stream, rope.index, rope._ref, positions,
+                      0 if seqs is None else seqs._ref, q, k, qo, ko)
+        if st == AWQ_OK:
+            return qo, ko
+        if st is not None:
+            _check("awq_rope", st)
+    if (positions is None) == (seqs is None):
+        raise ValueError("give either positions or seqs")
+    heads, first = [], None
+    for name, t, o in (("q", q, qo), ("k", k, ko)):
+        if t is None:
+            if o is not None:
+                raise ValueError(f"out has a tensor for {name}, which is None")
+            heads.append(_RopeHeadsStruct())
+            continue
+        _rope_tensor(name, t, rope)
+        _rope_tensor(f"out of {name}", o, rope, t)
+        if first is not None and (t.shape[0] != first.shape[0] or t.shape[2] != first.shape[2]):
+            raise ValueError("q and k must hold the same tokens and channels")
+        first = t
+        heads.append(_RopeHeadsStruct(t.data_ptr(), o.data_ptr(), *t.stride()[:2], *o.stride()[:2], t.shape[1]))
+    if first is None:
+        return qo, ko
+    T, _, D = first.shape
+    if rope.rotary_dim > D:
+        raise ValueError(f"the table rotates {rope.rotary_dim} channels, a head has {D}")
+    if positions is not None:
+        _need_on("positions", positions, torch.int32, rope.index)
+        if tuple(positions.shape) != (T,):
+            raise ValueError(f"positions must be [{T}]")
+    elif seqs.index != rope.index:
+        raise ValueError(f"seqs must be on {rope.device}")
+    st = _on_device(rope.index, (_lib or load()).awq_rope, rope._ref, _ptr(positions),
+                    None if seqs is None else seqs._ref, ctypes.addressof(heads[0]), ctypes.addressof(heads[1]), D, T)
+    if st != AWQ_OK:
+        _check("awq_rope", st)
+    return qo, ko

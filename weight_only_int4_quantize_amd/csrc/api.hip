@@ -813,7 +813,7 @@ awq_status awq_gemm_fused(const void* x_f16, const uint32_t* qweight, const void
 
 }  // extern "C"
 
-// ---- the paged 8-bit cache ----
+// ---- the paged cache ----
 namespace {
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -822,7 +822,8 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 // when there is nothing to do (no sequence, no token).
 awq_status kv_pages(const awq_kv_cache* cache, const awq_kv_seqs* seqs, int64_t n_tokens, KvPages* out, bool* empty) {
     if (!cache || !seqs) return AWQ_ERR_NULL;
-    if (cache->format != AWQ_KV_INT8 && cache->format != AWQ_KV_E4M3) return AWQ_ERR_CONFIG;
+    const bool int4 = cache->format == AWQ_KV_INT4;
+    if (cache->format != AWQ_KV_INT8 && cache->format != AWQ_KV_E4M3 && !int4) return AWQ_ERR_CONFIG;
     const int page = cache->page_size, dim = cache->head_dim;
     if (page != 32 && page != 64 && page != 128 && page != 256) return AWQ_ERR_CONFIG;
     if (dim != 64 && dim != 96 && dim != 128 && dim != 192 && dim != 256) return AWQ_ERR_CONFIG;
@@ -839,12 +840,12 @@ awq_status kv_pages(const awq_kv_cache* cache, const awq_kv_seqs* seqs, int64_t 
         return AWQ_ERR_NULL;
     if (!aligned16(cache->k_codes) || !aligned16(cache->v_codes) || !aligned4(cache->k_scales) ||
         !aligned4(cache->v_scales) || !aligned4(seqs->block_table) || !aligned4(seqs->cu_tokens) ||
-        !aligned4(seqs->kv_len))
+        !aligned4(seqs->kv_len) || (int4 && (!aligned16(cache->k_scales) || !aligned16(cache->v_scales))))
         return AWQ_ERR_ALIGN;
     out->k_codes = static_cast<uint8_t*>(cache->k_codes);
     out->v_codes = static_cast<uint8_t*>(cache->v_codes);
-    out->k_scales = cache->k_scales;
-    out->v_scales = cache->v_scales;
+    out->k_scales = static_cast<float*>(cache->k_scales);     // fp16 pairs behind them with AWQ_KV_INT4
+    out->v_scales = static_cast<float*>(cache->v_scales);
     out->table = seqs->block_table;
     out->cu = seqs->cu_tokens;
     out->len = seqs->kv_len;
@@ -967,6 +968,173 @@ awq_status awq_kv_attention(const awq_kv_cache* cache, const awq_kv_seqs* seqs, 
             return AWQ_ERR_WORKSPACE;
     }
     return launch_kv_attention(a, workspace, as_stream(stream));
+}
+
+}  // extern "C"
+
+// ---- the norm and the rotary positions ----
+namespace {
+
+bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
+
+constexpr int64_t kMaxStride = int64_t{1} << 40;
+bool stride_ok(int64_t stride, int64_t least) { return stride >= least && stride < kMaxStride; }
+
+// a tensor of rotary positions: AWQ_OK and *out filled
+awq_status rope_heads(const awq_rope_heads* t, int head_dim, int64_t n_tokens, RopeHeads* out) {
+    *out = RopeHeads{};
+    if (t == nullptr || t->heads == 0) return AWQ_OK;
+    if (t->heads < 0 || t->heads > 65535) return AWQ_ERR_SHAPE;
+    if (!stride_ok(t->in_token_stride, 0) || !stride_ok(t->in_head_stride, 0)) return AWQ_ERR_SHAPE;
+    const bool tokens = n_tokens > 1, heads = t->heads > 1;
+    if (!stride_ok(t->out_token_stride, tokens ? head_dim : 0) || !stride_ok(t->out_head_stride, heads ? head_dim : 0))
+        return AWQ_ERR_SHAPE;
+    if (tokens && heads && t->out_token_stride < (t->heads - 1) * t->out_head_stride + head_dim &&
+        t->out_head_stride < (n_tokens - 1) * t->out_token_stride + head_dim)
+        return AWQ_ERR_SHAPE;
+    if (t->in == t->out && ((tokens && t->in_token_stride != t->out_token_stride) ||
+                            (heads && t->in_head_stride != t->out_head_stride)))
+        return AWQ_ERR_SHAPE;
+    if (n_tokens > 0 && (!t->in || !t->out)) return AWQ_ERR_NULL;
+    if (!aligned2(t->in) || !aligned2(t->out)) return AWQ_ERR_ALIGN;
+    out->in = static_cast<const half_t*>(t->in);
+    out->out = static_cast<half_t*>(t->out);
+    out->in_token = t->in_token_stride;
+    out->in_head = t->in_head_stride;
+    out->out_token = t->out_token_stride;
+    out->out_head = t->out_head_stride;
+    out->heads = t->heads;
+    return AWQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+awq_status awq_rmsnorm(const void* x_f16, int64_t x_stride, const void* residual_f16, int64_t residual_stride,
+                       void* residual_out_f16, int64_t residual_out_stride, const void* weight_f16,
+                       float weight_offset, float eps, int64_t rows, int64_t width, int format, int group_size,
+                       void* out, int64_t out_stride, float* scales, void* stream) {
+    if (format != AWQ_NORM_F16 && format != AWQ_NORM_INT8 && format != AWQ_NORM_E4M3) return AWQ_ERR_CONFIG;
+    if (group_size != 0 && (format == AWQ_NORM_F16 || (group_size != 32 && group_size != 64 && group_size != 128 &&
+                                                       group_size != 256 && group_size != 512)))
+        return AWQ_ERR_CONFIG;
+    if (!std::isfinite(weight_offset) || !std::isfinite(eps) || eps < 0.f) return AWQ_ERR_CONFIG;
+    if (rows < 0 || rows >= int64_t{1} << 31 || width < 1 || width > int64_t{1} << 24 ||
+        (group_size != 0 && width % group_size != 0))
+        return AWQ_ERR_SHAPE;
+    const int64_t least = rows > 1 ? width : 0;
+    if (!stride_ok(x_stride, 0) || !stride_ok(out_stride, least) || (residual_f16 && !stride_ok(residual_stride, 0)) ||
+        (residual_out_f16 && !stride_ok(residual_out_stride, least)))
+        return AWQ_ERR_SHAPE;
+    const auto same = [&](const void* o, int64_t os, const void* i, int64_t is) {
+        return o && o == i && rows > 1 && os != is;
+    };
+    if (same(residual_out_f16, residual_out_stride, x_f16, x_stride) ||
+        same(residual_out_f16, residual_out_stride, residual_f16, residual_stride) ||
+        (format == AWQ_NORM_F16 &&
+         (same(out, out_stride, x_f16, x_stride) || same(out, out_stride, residual_f16, residual_stride))))
+        return AWQ_ERR_SHAPE;
+    if (rows == 0) return AWQ_OK;
+    if (!x_f16 || !out || (format != AWQ_NORM_F16 && !scales)) return AWQ_ERR_NULL;
+    if (out == residual_out_f16) return AWQ_ERR_SHAPE;
+    // 8-bit rows written over fp16 ones would overtake them
+    if (format != AWQ_NORM_F16 && (out == x_f16 || out == residual_f16)) return AWQ_ERR_SHAPE;
+    if (!aligned2(x_f16) || !aligned2(residual_f16) || !aligned2(residual_out_f16) || !aligned2(weight_f16) ||
+        (format == AWQ_NORM_F16 && !aligned2(out)) || (format != AWQ_NORM_F16 && !aligned4(scales)))
+        return AWQ_ERR_ALIGN;
+    NormArgs a{};
+    a.x = static_cast<const half_t*>(x_f16);
+    a.residual = static_cast<const half_t*>(residual_f16);
+    a.sum = static_cast<half_t*>(residual_out_f16);
+    a.weight = static_cast<const half_t*>(weight_f16);
+    a.out = out;
+    a.scales = scales;
+    a.x_stride = x_stride;
+    a.residual_stride = residual_stride;
+    a.sum_stride = residual_out_stride;
+    a.out_stride = out_stride;
+    a.rows = rows;
+    a.width = width;
+    a.offset = weight_offset;
+    a.eps = eps;
+    a.format = format;
+    a.group = group_size;
+    return launch_rmsnorm(a, as_stream(stream));
+}
+
+awq_status awq_rope_frequencies(int rotary_dim, double base, int scaling, double factor, double trained_len, double low,
+                                double high, double* freqs, double* amplitude) {
+    if (!freqs || !amplitude) return AWQ_ERR_NULL;
+    if (rotary_dim < 2 || rotary_dim > 4096 || rotary_dim % 2 != 0) return AWQ_ERR_SHAPE;
+    if (scaling < AWQ_ROPE_NONE || scaling > AWQ_ROPE_WAVELENGTH || !(base > 1.0) || !std::isfinite(base))
+        return AWQ_ERR_CONFIG;
+    const bool ramp = scaling == AWQ_ROPE_YARN || scaling == AWQ_ROPE_WAVELENGTH;
+    if (scaling != AWQ_ROPE_NONE && (!(factor >= 1.0) || !std::isfinite(factor))) return AWQ_ERR_CONFIG;
+    if (ramp && (!(trained_len > 0.0) || !std::isfinite(trained_len) || !(low > 0.0) || !(high > low) ||
+                 !std::isfinite(high)))
+        return AWQ_ERR_CONFIG;
+    if (scaling == AWQ_ROPE_NTK && rotary_dim == 2) return AWQ_ERR_CONFIG;
+    constexpr double kTurn = 6.283185307179586;
+    const double R = rotary_dim;
+    const double b = scaling == AWQ_ROPE_NTK ? base * std::pow(factor, R / (R - 2.0)) : base;
+    double first = 0.0, last = 0.0;
+    if (scaling == AWQ_ROPE_YARN) {
+        const auto pair = [&](double turns) { return R * std::log(trained_len / (kTurn * turns)) / (2.0 * std::log(base)); };
+        first = std::max(std::floor(pair(high)), 0.0);
+        last = std::min(std::ceil(pair(low)), R - 1.0);
+    }
+    for (int i = 0; i < rotary_dim / 2; ++i) {
+        const double f = std::pow(b, -2.0 * i / R);
+        double keep = 1.0;      // of the frequency that stays
+        if (scaling == AWQ_ROPE_LINEAR) keep = 0.0;
+        if (scaling == AWQ_ROPE_YARN)
+            keep = 1.0 - std::min(std::max((i - first) / std::max(last - first, 0.001), 0.0), 1.0);
+        if (scaling == AWQ_ROPE_WAVELENGTH)
+            keep = std::min(std::max((trained_len * f / kTurn - low) / (high - low), 0.0), 1.0);
+        freqs[i] = f * keep + f / factor * (1.0 - keep);
+        if (keep == 1.0) freqs[i] = f;
+    }
+    *amplitude = scaling == AWQ_ROPE_YARN ? 0.1 * std::log(factor) + 1.0 : 1.0;
+    return AWQ_OK;
+}
+
+awq_status awq_rope(const awq_rope_table* rope, const int32_t* positions, const awq_kv_seqs* seqs,
+                    const awq_rope_heads* q, const awq_rope_heads* k, int head_dim, int64_t n_tokens, void* stream) {
+    if (!rope) return AWQ_ERR_NULL;
+    if (rope->layout != AWQ_ROPE_HALF && rope->layout != AWQ_ROPE_INTERLEAVED) return AWQ_ERR_CONFIG;
+    if (!std::isfinite(rope->amplitude)) return AWQ_ERR_CONFIG;
+    if (head_dim < 2 || head_dim > 4096 || rope->rotary_dim < 2 || rope->rotary_dim > head_dim ||
+        rope->rotary_dim % 2 != 0 || n_tokens < 0 || n_tokens >= int64_t{1} << 24)
+        return AWQ_ERR_SHAPE;
+    if ((positions == nullptr) == (seqs == nullptr) && n_tokens > 0) return AWQ_ERR_NULL;
+    if (seqs && (seqs->n_seqs < 0 || seqs->n_seqs > 32767 || seqs->max_tokens < 0 || seqs->max_tokens > INT32_MAX ||
+                 seqs->max_len < 0 || seqs->max_len > kKvMaxLen))
+        return AWQ_ERR_SHAPE;
+    RopeArgs a{};
+    awq_status st = rope_heads(q, head_dim, n_tokens, &a.q);
+    if (st == AWQ_OK) st = rope_heads(k, head_dim, n_tokens, &a.k);
+    if (st != AWQ_OK) return st;
+    if (n_tokens == 0 || a.q.heads + a.k.heads == 0 || (seqs && (seqs->n_seqs == 0 || seqs->max_tokens == 0)))
+        return AWQ_OK;
+    if (!rope->freqs || (seqs && (!seqs->cu_tokens || !seqs->kv_len))) return AWQ_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(rope->freqs) & 7u) != 0 || !aligned4(positions) ||
+        (seqs && (!aligned4(seqs->cu_tokens) || !aligned4(seqs->kv_len))))
+        return AWQ_ERR_ALIGN;
+    a.freqs = rope->freqs;
+    a.positions = positions;
+    a.n_tokens = static_cast<int>(n_tokens);
+    a.dim = head_dim;
+    a.rotary = rope->rotary_dim;
+    a.amplitude = rope->amplitude;
+    a.interleaved = rope->layout == AWQ_ROPE_INTERLEAVED;
+    if (seqs) {
+        a.cu = seqs->cu_tokens;
+        a.len = seqs->kv_len;
+        a.max_len = static_cast<int>(seqs->max_len);
+    }
+    return launch_rope(a, seqs ? std::min(seqs->max_tokens, n_tokens) : n_tokens, seqs ? seqs->n_seqs : 1,
+                       as_stream(stream));
 }
 
 }  // extern "C"

@@ -229,6 +229,43 @@ awq_status launch_salient_apply(const half_t* x, const int* idx, const half_t* w
 awq_status launch_salient_subtract(const half_t* x, const int* idx, const half_t* w_sal, int64_t M, int64_t N,
                                    int64_t K, int n_sal, float* y32, hipStream_t stream);
 
+// Root-mean-square norm (strides in elements; nullptr where there is none).
+struct NormArgs {
+    const half_t* x;
+    const half_t* residual;
+    half_t* sum;            // x + residual as fp16, may be x or residual
+    const half_t* weight;
+    void* out;
+    float* scales;
+    int64_t x_stride, residual_stride, sum_stride, out_stride;
+    int64_t rows, width;
+    float offset, eps;
+    int format, group;      // AWQ_NORM_*; group 0: one scale a row
+};
+awq_status launch_rmsnorm(const NormArgs& a, hipStream_t stream);
+
+// Rotary positions: a token's heads of one tensor (strides in halves).
+struct RopeHeads {
+    const half_t* in;
+    half_t* out;
+    int64_t in_token, in_head, out_token, out_head;
+    int heads;
+};
+struct RopeArgs {
+    RopeHeads q, k;
+    const double* freqs;        // [rotary / 2], radians per position
+    const int32_t* positions;   // [n_tokens], or nullptr: the batch's
+    const int32_t* cu;
+    const int32_t* len;
+    int n_tokens, max_len;
+    int dim, rotary;
+    int rotated, passed;        // set by the launcher
+    float amplitude;
+    bool interleaved;
+};
+// tokens: of the call, or a bound of a sequence's (n_seqs of them)
+awq_status launch_rope(const RopeArgs& a, int64_t tokens, int n_seqs, hipStream_t stream);
+
 // Scale-search helpers.
 size_t absmean_workspace_bytes(int64_t T, int64_t K);
 awq_status launch_absmean(const half_t* x, int64_t T, int64_t K, double* m, double* partials,

@@ -1,5 +1,6 @@
-// The serving calls' argument marshalling (awq_gemm_fused, awq_kv_write,
-// awq_kv_read, awq_kv_attention) as a CPython extension over torch tensors.
+// The serving calls' argument marshalling (awq_gemm_fused, awq_rmsnorm, awq_rope,
+// awq_kv_write, awq_kv_read, awq_kv_attention) as a CPython extension over torch
+// tensors.
 //
 // A decode step makes such a call every 5 to 10 us. Checking eight tensors
 // attribute by attribute in Python and passing twenty numbers through ctypes
@@ -188,6 +189,92 @@ PyObject* kv_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
                      o.head, lse, ws, bytes, stream);
 }
 
+double number(PyObject* o, bool& ok) {
+    if (PyFloat_Check(o)) return PyFloat_AS_DOUBLE(o);
+    return static_cast<double>(integer(o, ok));
+}
+// [M, N] of a type with contiguous rows: its address and row stride
+bool rows_of(PyObject* o, int64_t M, int64_t N, at::ScalarType type, int64_t device, void*& p, int64_t& stride) {
+    const Tensor* t = tensor(o);
+    if (t == nullptr || !on(*t, type, device) || t->dim() != 2 || t->size(0) != M || t->size(1) != N ||
+        (N > 1 && t->stride(1) != 1))
+        return false;
+    p = t->data_ptr();
+    stride = M > 1 ? t->stride(0) : N;
+    return true;
+}
+
+// rmsnorm(entry, stream, device, x, weight, eps, residual, residual_out, offset, format, group, out, scales)
+PyObject* rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (n != 13) Py_RETURN_NONE;
+    bool ok = true;
+    auto entry = reinterpret_cast<decltype(&awq_rmsnorm)>(address(a[0], ok));
+    void* stream = address(a[1], ok);
+    const int64_t dev = integer(a[2], ok);
+    const Tensor* x = tensor(a[3]);
+    const double eps = number(a[5], ok), offset = number(a[8], ok);
+    const int64_t format = integer(a[9], ok), group = integer(a[10], ok);
+    if (!ok || !x || x->dim() != 2 || group < 0 || group > 1 << 20 || format < 0 || format > 2) Py_RETURN_NONE;
+    const int64_t M = x->size(0), N = x->size(1);
+    void *xp, *rp = nullptr, *sp = nullptr, *op, *wp = nullptr, *scales = nullptr;
+    int64_t xs, rs = 0, ss = 0, os;
+    const at::ScalarType types[3] = {at::kHalf, at::kChar, at::kFloat8_e4m3fn};
+    if (!rows_of(a[3], M, N, at::kHalf, dev, xp, xs) || !rows_of(a[11], M, N, types[format], dev, op, os) ||
+        (a[6] != Py_None && !rows_of(a[6], M, N, at::kHalf, dev, rp, rs)) ||
+        (a[7] != Py_None && !rows_of(a[7], M, N, at::kHalf, dev, sp, ss)))
+        Py_RETURN_NONE;
+    if (a[4] != Py_None) {
+        const Tensor* w = tensor(a[4]);
+        if (w == nullptr || !dense(*w, at::kHalf, dev) || w->dim() != 1 || w->size(0) != N) Py_RETURN_NONE;
+        wp = w->data_ptr();
+    }
+    if (format != 0) {
+        const Tensor* t = tensor(a[12]);
+        if (t == nullptr || !dense(*t, at::kFloat, dev) || t->dim() != 2 || t->size(0) != M ||
+            t->size(1) != (group > 0 ? N / group : 1))
+            Py_RETURN_NONE;
+        scales = t->data_ptr();
+    }
+    return status_of(entry, xp, xs, rp, rs, sp, ss, wp, static_cast<float>(offset), static_cast<float>(eps), M, N,
+                     static_cast<int>(format), static_cast<int>(group), op, os, static_cast<float*>(scales), stream);
+}
+
+// rope(entry, stream, device, table, positions or None, batch or 0, q, k, q_out, k_out); q with q_out, k with k_out
+// may be None
+PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (n != 10) Py_RETURN_NONE;
+    bool ok = true;
+    auto entry = reinterpret_cast<decltype(&awq_rope)>(address(a[0], ok));
+    void* stream = address(a[1], ok);
+    const int64_t dev = integer(a[2], ok);
+    auto* table = static_cast<const awq_rope_table*>(address(a[3], ok));
+    auto* seqs = static_cast<const awq_kv_seqs*>(address(a[5], ok));
+    if (!ok || (a[4] == Py_None) == (seqs == nullptr)) Py_RETURN_NONE;
+    awq_rope_heads heads[2] = {};
+    int64_t T = -1, D = -1;
+    for (int i = 0; i < 2; ++i) {
+        if (a[6 + i] == Py_None && a[8 + i] == Py_None) continue;
+        const Tensor *in = tensor(a[6 + i]), *out = tensor(a[8 + i]);
+        if (in == nullptr || out == nullptr || in->dim() != 3) Py_RETURN_NONE;
+        if (T < 0) T = in->size(0), D = in->size(2);
+        for (const Tensor* t : {in, out})
+            if (!on(*t, at::kHalf, dev) || t->dim() != 3 || t->size(0) != T || t->size(2) != D ||
+                t->size(1) != in->size(1) || (D > 1 && t->stride(2) != 1))
+                Py_RETURN_NONE;
+        if (in->size(1) > INT32_MAX) Py_RETURN_NONE;
+        heads[i] = {in->data_ptr(), out->data_ptr(), in->stride(0), in->stride(1), out->stride(0), out->stride(1),
+                    static_cast<int>(in->size(1))};
+    }
+    if (T < 0 || D > INT32_MAX || table->rotary_dim > D) Py_RETURN_NONE;
+    const int32_t* positions = nullptr;
+    if (a[4] != Py_None) {
+        const Tensor* p = tensor(a[4]);
+        if (p == nullptr || !dense(*p, at::kInt, dev) || p->dim() != 1 || p->size(0) != T) Py_RETURN_NONE;
+        positions = static_cast<const int32_t*>(p->data_ptr());
+    }
+    return status_of(entry, table, positions, seqs, &heads[0], &heads[1], static_cast<int>(D), T, stream);
+}
+
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyObject* guarded(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     try {
@@ -200,6 +287,7 @@ PyObject* guarded(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 #define AWQ_CALL(name) \
     {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(&guarded<name>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {AWQ_CALL(gemm_fused), AWQ_CALL(kv_write), AWQ_CALL(kv_read), AWQ_CALL(kv_attention),
+                         AWQ_CALL(rmsnorm), AWQ_CALL(rope),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

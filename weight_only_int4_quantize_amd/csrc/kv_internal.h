@@ -1,4 +1,4 @@
-// The paged 8-bit key / value cache: what its kernels share.
+// The paged key / value cache, 8-bit and 4-bit: what its kernels share.
 #pragma once
 
 #include "awq_internal.h"
@@ -28,6 +28,12 @@ struct KvPages {
 // Longest sequence: whole splits of 1024 positions, and a tile past them, in
 // 32 bits, so that one split can hold every position.
 constexpr int64_t kKvMaxLen = (int64_t{1} << 31) - 1024;
+
+// The 4-bit cache's scales are fp16, behind the same pointers: keys one pair
+// (s, lo) per page, head, 32 channels and token, values every token's s of a
+// page and head, then every lo.
+__device__ inline half2_t* kv4_k_scales(const KvPages& c) { return reinterpret_cast<half2_t*>(c.k_scales); }
+__device__ inline half_t* kv4_v_scales(const KvPages& c) { return reinterpret_cast<half_t*>(c.v_scales); }
 
 constexpr float kInt8Top = 127.0f;
 constexpr float kE4m3Top = 448.0f;
@@ -125,6 +131,53 @@ __device__ inline uint32_t kv_pack4(float a, float b, float c, float d) {
     }
 }
 
+// A word of eight 4-bit codes becomes four pairs of fp16 numbers in 13
+// instructions: the nibbles under an fp16 exponent are 1024 + c (nibbles 0 and
+// 4) and 1024 + 16 c (1 and 5), a shift by 8 brings the others, one packed
+// instruction takes the 1024 (and the 16) off, exactly, and one applies s and
+// lo: the cached numbers fp16(lo + s c). The pairs come out in order since code
+// 2 j is in nibble j and code 2 j + 1 in nibble j + 4.
+
+// Pairs (code 2 j, code 2 j + 1), j = 0 .. 3, of a word, as fp16 numbers 0 .. 15.
+__device__ inline void kv4_codes8(uint32_t w, half2_t (&c)[4]) {
+    const half2_t off = {static_cast<half_t>(1024.f), static_cast<half_t>(1024.f)};
+    const half2_t part = {static_cast<half_t>(0.0625f), static_cast<half_t>(0.0625f)};
+    const half2_t off16 = {static_cast<half_t>(-64.f), static_cast<half_t>(-64.f)};
+    auto bits = [](uint32_t v, uint32_t mask) { return __builtin_bit_cast(half2_t, (v & mask) | 0x64006400u); };
+    const uint32_t w8 = w >> 8;
+    c[0] = bits(w, 0x000F000Fu) - off;
+    c[1] = __builtin_elementwise_fma(bits(w, 0x00F000F0u), part, off16);
+    c[2] = bits(w8, 0x000F000Fu) - off;
+    c[3] = __builtin_elementwise_fma(bits(w8, 0x00F000F0u), part, off16);
+}
+// The eight numbers of a word whose group has one (s, lo): a key's.
+__device__ inline half8_t kv4_numbers8(uint32_t w, half2_t s_lo) {
+    half2_t c[4];
+    kv4_codes8(w, c);
+    const half2_t s = {s_lo[0], s_lo[0]}, lo = {s_lo[1], s_lo[1]};
+    half8_t r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const half2_t v = __builtin_elementwise_fma(c[j], s, lo);
+        r[2 * j] = v[0];
+        r[2 * j + 1] = v[1];
+    }
+    return r;
+}
+// The eight numbers of a word whose codes have an s and a lo each: a value's.
+__device__ inline half8_t kv4_numbers8(uint32_t w, half8_t s, half8_t lo) {
+    half2_t c[4];
+    kv4_codes8(w, c);
+    half8_t r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const half2_t v = __builtin_elementwise_fma(c[j], half2_t{s[2 * j], s[2 * j + 1]},
+                                                    half2_t{lo[2 * j], lo[2 * j + 1]});
+        r[2 * j] = v[0];
+        r[2 * j + 1] = v[1];
+    }
+    return r;
+}
 // ---- launchers ----
 struct KvWriteArgs {
     KvPages c;
@@ -143,6 +196,9 @@ struct KvReadArgs {
     int64_t max_tokens;
 };
 awq_status launch_kv_read(const KvReadArgs& a, hipStream_t stream);
+// the same over the 4-bit cache (format AWQ_KV_INT4)
+awq_status launch_kv4_write(const KvWriteArgs& a, hipStream_t stream);
+awq_status launch_kv4_read(const KvReadArgs& a, hipStream_t stream);
 
 struct KvAttentionArgs {
     KvPages c;
@@ -159,5 +215,6 @@ struct KvAttentionArgs {
 size_t kv_attention_workspace_bytes(int n_seqs, int kv_heads, int ratio, int head_dim, int64_t max_tokens,
                                     int64_t max_len);
 awq_status launch_kv_attention(const KvAttentionArgs& a, void* workspace, hipStream_t stream);
+awq_status launch_kv4_attention(const KvAttentionArgs& a, void* workspace, hipStream_t stream);
 
 }  // namespace awq

@@ -274,6 +274,7 @@ bool launchable(const KvPages& c, int64_t max_tokens) {
 }  // namespace
 
 awq_status launch_kv_write(const KvWriteArgs& a, hipStream_t stream) {
+    if (a.format == AWQ_KV_INT4) return launch_kv4_write(a, stream);
     if (!launchable(a.c, a.max_tokens)) return AWQ_ERR_SHAPE;
     const dim3 grid(static_cast<unsigned>(touched_pages(a.c, a.max_tokens)), static_cast<unsigned>(a.c.heads),
                     static_cast<unsigned>(2 * a.n_seqs));
@@ -285,6 +286,7 @@ awq_status launch_kv_write(const KvWriteArgs& a, hipStream_t stream) {
 }
 
 awq_status launch_kv_read(const KvReadArgs& a, hipStream_t stream) {
+    if (a.format == AWQ_KV_INT4) return launch_kv4_read(a, stream);
     if (!launchable(a.c, a.max_tokens)) return AWQ_ERR_SHAPE;
     const dim3 grid(static_cast<unsigned>(touched_pages(a.c, a.max_tokens)), static_cast<unsigned>(a.c.heads),
                     static_cast<unsigned>(2 * a.n_seqs));
