@@ -69,10 +69,16 @@ __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 64 ? 4 : D <= 96 ? 3 : D 
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 15, quarter = lane >> 4;
-    const int split = blockIdx.x;
-    const int b = blockIdx.z;
-    const int kv_head = blockIdx.y % c.heads;
-    const int row0 = blockIdx.y / c.heads * kDecodeRows;
+    // Blocks go to the 8 XCDs in turn: heads run fastest, so that each XCD gets
+    // splits of every sequence, and splits slowest, the last first, which only
+    // long sequences have. (With splits fastest, two of them put every
+    // sequence's first on the even XCDs and the seconds, often short or empty,
+    // on the odd: 64 sequences of 8192 down to 2048 tokens 100 us, now 87.)
+    const int kv_head = blockIdx.x % c.heads;
+    const int row_tile = blockIdx.x / c.heads;
+    const int row0 = row_tile * kDecodeRows;
+    const int b = blockIdx.y;
+    const int split = n_splits - 1 - blockIdx.z;
     const KvSeq sq = kv_seq_shared(c, b);
     const int all_rows = sq.n * a.ratio;
     if (row0 >= all_rows) return;
@@ -290,7 +296,7 @@ __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 64 ? 4 : D <= 96 ? 3 : D 
         sl[0][tid] = ll;
     }
     __syncthreads();
-    const int64_t tile_id = static_cast<int64_t>(b) * gridDim.y + blockIdx.y;
+    const int64_t tile_id = static_cast<int64_t>(b) * gridDim.x + blockIdx.x;
     const Rows rw{kv_head, row0, rows, last_split - first_split + 1, split - first_split,
                   sp.partials + tile_id * n_splits * kFloats, static_cast<int64_t>(n_splits) * kFloats * 4,
                   sp.counters + tile_id};
@@ -588,8 +594,8 @@ template <int D, int NP>
 void launch_np(const KvAttentionArgs& a, const Plan& p, const Split& sp, hipStream_t stream) {
     if (p.decode)
         hipLaunchKernelGGL((kv4_decode_kernel<D, NP>),
-                           dim3(static_cast<unsigned>(p.splits), static_cast<unsigned>(p.row_tiles * a.c.heads),
-                                static_cast<unsigned>(a.n_seqs)),
+                           dim3(static_cast<unsigned>(p.row_tiles * a.c.heads), static_cast<unsigned>(a.n_seqs),
+                                static_cast<unsigned>(p.splits)),
                            dim3(kDecodeWaves * kWave), 0, stream, a, sp, p.splits);
     else
         hipLaunchKernelGGL((kv4_prefill_kernel<D, NP>),
@@ -606,7 +612,7 @@ void launch_d(const KvAttentionArgs& a, const Plan& p, const Split& sp, hipStrea
 }  // namespace
 
 awq_status launch_kv4_attention(const KvAttentionArgs& a, void* workspace, hipStream_t stream) {
-    const Plan p = plan_for(a.n_seqs, a.c.heads, a.ratio, a.max_tokens, a.c.max_len, workspace != nullptr);
+    const Plan p = plan_for(a.n_seqs, a.c.heads, a.ratio, a.max_tokens, a.c.max_len, workspace != nullptr, AWQ_KV_INT4);
     if (!launchable(p, a.c.heads)) return AWQ_ERR_SHAPE;
     const Split sp = split_of(p, workspace);
     switch (a.head_dim) {

@@ -143,12 +143,18 @@ __device__ inline void kv4_codes8(uint32_t w, half2_t (&c)[4]) {
     const half2_t off = {static_cast<half_t>(1024.f), static_cast<half_t>(1024.f)};
     const half2_t part = {static_cast<half_t>(0.0625f), static_cast<half_t>(0.0625f)};
     const half2_t off16 = {static_cast<half_t>(-64.f), static_cast<half_t>(-64.f)};
-    auto bits = [](uint32_t v, uint32_t mask) { return __builtin_bit_cast(half2_t, (v & mask) | 0x64006400u); };
+    // (constants that the compiler cannot see, in registers: as literals they
+    // would take an and and an or)
+    uint32_t one = 0x64006400u, low = 0x000F000Fu, high = 0x00F000F0u;
+    asm("" : "+v"(one));
+    asm("" : "+s"(low));
+    asm("" : "+s"(high));
+    auto bits = [&](uint32_t v, uint32_t mask) { return __builtin_bit_cast(half2_t, (v & mask) | one); };
     const uint32_t w8 = w >> 8;
-    c[0] = bits(w, 0x000F000Fu) - off;
-    c[1] = __builtin_elementwise_fma(bits(w, 0x00F000F0u), part, off16);
-    c[2] = bits(w8, 0x000F000Fu) - off;
-    c[3] = __builtin_elementwise_fma(bits(w8, 0x00F000F0u), part, off16);
+    c[0] = bits(w, low) - off;
+    c[1] = __builtin_elementwise_fma(bits(w, high), part, off16);
+    c[2] = bits(w8, low) - off;
+    c[3] = __builtin_elementwise_fma(bits(w8, high), part, off16);
 }
 // The eight numbers of a word whose group has one (s, lo): a key's.
 __device__ inline half8_t kv4_numbers8(uint32_t w, half2_t s_lo) {
@@ -213,7 +219,7 @@ struct KvAttentionArgs {
     int window;                            // 0: none
 };
 size_t kv_attention_workspace_bytes(int n_seqs, int kv_heads, int ratio, int head_dim, int64_t max_tokens,
-                                    int64_t max_len);
+                                    int64_t max_len, int format);
 awq_status launch_kv_attention(const KvAttentionArgs& a, void* workspace, hipStream_t stream);
 awq_status launch_kv4_attention(const KvAttentionArgs& a, void* workspace, hipStream_t stream);
 
