@@ -77,8 +77,7 @@ __device__ inline int kv_page(const KvPages& c, int b, int p) {
     return id >= 0 && id < c.n_pages ? id : -1;
 }
 
-// kv_seq and kv_page for wave-uniform arguments (attention only: the write
-// changes what it would read)
+// kv_seq and kv_page for wave-uniform arguments (no kernel writes what they read)
 __device__ inline KvSeq kv_seq_shared(const KvPages& c, int b) {
     KvSeq s;
     s.row0 = min(max(kv_shared_load(c.cu + b), 0), c.n_tokens);
