@@ -1058,6 +1058,7 @@ awq_status awq_rmsnorm(const void* x_f16, int64_t x_stride, const void* residual
     a.width = width;
     a.offset = weight_offset;
     a.eps = eps;
+    a.per_width = static_cast<float>(1.0 / static_cast<double>(width));
     a.format = format;
     a.group = group_size;
     return launch_rmsnorm(a, as_stream(stream));

@@ -240,6 +240,7 @@ struct NormArgs {
     int64_t x_stride, residual_stride, sum_stride, out_stride;
     int64_t rows, width;
     float offset, eps;
+    float per_width;        // 1 / width
     int format, group;      // AWQ_NORM_*; group 0: one scale a row
 };
 awq_status launch_rmsnorm(const NormArgs& a, hipStream_t stream);

@@ -82,18 +82,38 @@ __device__ inline float scale_of(float top, float& inv) {
     return s;
 }
 
+// A value of the lane 1, 2, 4 .. 32 away in some order, by the wave's own moves
+// (over LDS the six steps took 0.2 us more of a 2.8 us call).
+template <int STEP>
+__device__ inline uint32_t moved(uint32_t v) {
+    typedef uint32_t swap_t __attribute__((ext_vector_type(2)));
+    if constexpr (STEP == 5) {
+        const swap_t r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        return threadIdx.x & 32 ? r[0] : r[1];
+    } else if constexpr (STEP == 4) {
+        const swap_t r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        return threadIdx.x & 16 ? r[0] : r[1];
+    } else {        // neighbours, pairs, halves of eight, halves of sixteen
+        constexpr int kControl = STEP == 0 ? 0xB1 : STEP == 1 ? 0x4E : STEP == 2 ? 0x141 : 0x140;
+        return static_cast<uint32_t>(
+            __builtin_amdgcn_update_dpp(static_cast<int>(v), static_cast<int>(v), kControl, 0xF, 0xF, true));
+    }
+}
+
 // (sum of squares, largest magnitude) of a row over its TPR threads
 struct Stats {
     float sum;
     uint32_t top;
 };
+template <int STEP = 0>
+__device__ inline void across_wave(Stats& v) {
+    v.sum += __builtin_bit_cast(float, moved<STEP>(__builtin_bit_cast(uint32_t, v.sum)));
+    v.top = max(v.top, moved<STEP>(v.top));
+    if constexpr (STEP < 5) across_wave<STEP + 1>(v);
+}
 template <int TPR>
 __device__ inline Stats across(Stats v) {
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) {
-        v.sum += __shfl_xor(v.sum, o);
-        v.top = max(v.top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v.top), o)));
-    }
+    across_wave(v);
     if constexpr (TPR > kWave) {
         constexpr int N = TPR / kWave;
         __shared__ float sums[N];
@@ -114,12 +134,15 @@ __device__ inline Stats across(Stats v) {
     return v;
 }
 
+// rows that need a wave each share a block
+constexpr int rows_per_block(int tpr) { return tpr == kWave ? 4 : 1; }
+
 // One row by TPR threads, thread l taking the pieces of eight elements l,
 // l + TPR, ..: P of them, in registers; P = 0: any number, and the row is read
 // a second time (from the caches, as far as they hold it).
 template <int FORMAT, int TPR, int P>
-__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_kernel(NormArgs a) {
-    constexpr int PER_BLOCK = TPR >= 256 ? 1 : 256 / TPR;
+__global__ __launch_bounds__(TPR * rows_per_block(TPR)) void rmsnorm_kernel(NormArgs a) {
+    constexpr int PER_BLOCK = rows_per_block(TPR);
     const int l = threadIdx.x % TPR;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * PER_BLOCK + threadIdx.x / TPR;
     if (PER_BLOCK > 1 && row >= a.rows) return;     // whole waves
@@ -183,7 +206,9 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_kernel(NormArgs
             store8(static_cast<uint8_t*>(a.out) + row * a.out_stride, 8 * p, K, w);
         }
     };
-    const auto inverse = [&](float squares) { return 1.0f / sqrtf(squares / static_cast<float>(K) + a.eps); };
+    const auto inverse = [&](float squares) {
+        return __builtin_amdgcn_rsqf(__builtin_fmaf(squares, a.per_width, a.eps));
+    };
     const auto row_scale = [&](uint32_t top, float inv) {
         float row_inv = 0.f;
         if constexpr (FORMAT != AWQ_NORM_F16) {
@@ -247,21 +272,25 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_kernel(NormArgs
 
 template <int FORMAT, int TPR, int P>
 awq_status launch_p(const NormArgs& a, hipStream_t stream) {
-    constexpr int PER_BLOCK = TPR >= 256 ? 1 : 256 / TPR;
-    constexpr int NT = TPR > 256 ? TPR : 256;
-    const int64_t blocks = ceil_div(a.rows, PER_BLOCK);
+    constexpr int NT = TPR * rows_per_block(TPR);
+    const int64_t blocks = ceil_div(a.rows, rows_per_block(TPR));
     if (blocks >= (int64_t{1} << 32) / NT) return AWQ_ERR_SHAPE;      // a launch takes 2^32 threads along x
     hipLaunchKernelGGL((rmsnorm_kernel<FORMAT, TPR, P>), dim3(static_cast<unsigned>(blocks)), dim3(NT), 0, stream, a);
     return last_launch_status();
 }
+// As many threads to a row as it has pieces of eight, up to 1024: measured with a
+// residual and its sum (us, in brackets with a quarter as many threads and four
+// pieces each): 1 x 4096 2.8 (4.4), 1 x 8192 3.3 (4.7), 64 x 8192 e4m3 4.4 (6.0),
+// 256 x 4096 3.7 (5.4), 4096 x 8192 50.7 (54.2). Between, 256 threads are some 8%
+// better (1024 x 4096 7.8 against 8.5): not worth instances of their own.
 template <int FORMAT>
 awq_status launch_format(const NormArgs& a, hipStream_t stream) {
     const int64_t pieces = ceil_div(a.width, 8);
     if (pieces <= 64) return launch_p<FORMAT, 64, 1>(a, stream);
-    if (pieces <= 128) return launch_p<FORMAT, 64, 2>(a, stream);
+    if (pieces <= 128) return launch_p<FORMAT, 128, 1>(a, stream);
     if (pieces <= 256) return launch_p<FORMAT, 256, 1>(a, stream);
-    if (pieces <= 512) return launch_p<FORMAT, 256, 2>(a, stream);
-    if (pieces <= 1024) return launch_p<FORMAT, 256, 4>(a, stream);
+    if (pieces <= 512) return launch_p<FORMAT, 512, 1>(a, stream);
+    if (pieces <= 1024) return launch_p<FORMAT, 1024, 1>(a, stream);
     if (pieces <= 2048) return launch_p<FORMAT, 1024, 2>(a, stream);
     if (pieces <= 4096) return launch_p<FORMAT, 1024, 4>(a, stream);
     return launch_p<FORMAT, 1024, 0>(a, stream);
