@@ -5,12 +5,15 @@
 // positions need more bits than fp32 has (2^17 positions times 1 radian leave
 // 2^-7): p f_i / 2 pi is taken in fp64 and its whole turns are dropped there;
 // what is left, at most half a turn, goes to fp32 (2^-25 turns) and to the
-// compiler's sincospi, within 4 units of the last place. The rotation is fp32,
-// rounded once.
+// hardware's sine and cosine, which take turns: within 2^-22.9 of the true
+// values over every multiple of 2^-25 turns (measured against fp64). The
+// rotation is fp32, rounded once.
 //
-// Bound by HBM: 2 bytes read and 2 written a number. A thread keeps the eight
-// pairs of one place in the head and goes over the token's heads with them, so
-// the angles are computed once for several heads.
+// Bound by HBM: 2 bytes read and 2 written a number; a call of few tokens by a
+// launch's length. A thread keeps one place in the head and goes over the
+// token's heads with it, so the angles are computed once for several heads.
+// Measured (us): 8192 tokens, 32 + 8 heads of 128, 168 MB, 37, 4.5 TB/s (a
+// copy reaches 5.1); one token of 32 + 32 heads 2.7.
 #include <algorithm>
 
 #include "awq_internal.h"
@@ -18,40 +21,40 @@
 namespace awq {
 namespace {
 
-constexpr int kThreads = 256;
-typedef half_t half16_t __attribute__((ext_vector_type(16)));
-typedef half8_t half8_any __attribute__((aligned(2)));
-typedef half16_t half16_any __attribute__((aligned(2)));
+// One wave: with 256 threads a token's heads left more of them idle (the 8192
+// tokens above 39.1 us against 37, with 5 heads 11.6 against 8.3).
+constexpr int kThreads = 64;
 
-// n (up to N) halves from p, the rest 0
-template <int N, typename V, typename Any>
-__device__ inline V load_n(const half_t* p, int n) {
-    if (n >= N) return *reinterpret_cast<const Any*>(p);
-    V v = {};
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-        if (j < n) v[j] = p[j];
-    return v;
+// N halves at any address that their type allows
+template <int N>
+struct Run {
+    half_t v[N];
+};
+template <int N>
+__device__ inline Run<N> load_run(const half_t* p) {
+    typedef half_t vec_t __attribute__((ext_vector_type(N)));
+    typedef vec_t any_t __attribute__((aligned(2)));
+    return __builtin_bit_cast(Run<N>, static_cast<vec_t>(*reinterpret_cast<const any_t*>(p)));
 }
-template <int N, typename V, typename Any>
-__device__ inline void store_n(half_t* p, int n, V v) {
-    if (n >= N) {
-        *reinterpret_cast<Any*>(p) = v;
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-        if (j < n) p[j] = v[j];
+template <>
+__device__ inline Run<1> load_run<1>(const half_t* p) {
+    return Run<1>{{*p}};
 }
-__device__ inline half8_t load8(const half_t* p, int n) { return load_n<8, half8_t, half8_any>(p, n); }
-__device__ inline void store8(half_t* p, int n, half8_t v) { store_n<8, half8_t, half8_any>(p, n, v); }
-__device__ inline half16_t load16(const half_t* p, int n) { return load_n<16, half16_t, half16_any>(p, n); }
-__device__ inline void store16(half_t* p, int n, half16_t v) { store_n<16, half16_t, half16_any>(p, n, v); }
+template <int N>
+__device__ inline void store_run(half_t* p, const Run<N>& r) {
+    typedef half_t vec_t __attribute__((ext_vector_type(N)));
+    typedef vec_t any_t __attribute__((aligned(2)));
+    *reinterpret_cast<any_t*>(p) = __builtin_bit_cast(vec_t, r);
+}
+template <>
+__device__ inline void store_run<1>(half_t* p, const Run<1>& r) {
+    *p = r.v[0];
+}
 
 // One token per blockIdx.x (of sequence blockIdx.z with BATCH), its heads
-// shared out over the blocks along y. A head's work is `rotated` units of
-// eight pairs and `passed` units of 16 channels behind them (none in place).
-template <bool INTERLEAVED, bool BATCH>
+// shared out over the blocks along y. A head is `rotated` units of U pairs and
+// `passed` units of 2 U channels behind them (none in place); U divides both.
+template <bool INTERLEAVED, bool BATCH, int U>
 __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a) {
     int64_t row = blockIdx.x;
     int position;
@@ -65,86 +68,98 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a) {
     } else {
         position = a.positions[row];
     }
-    const int half_r = a.rotary / 2;
     const int units = a.rotated + a.passed;
     const int heads = a.q.heads + a.k.heads;
-    const int step = kThreads * gridDim.y;
-    int at = -1;            // the unit whose angles c and s hold
-    float c[8], s[8];
-    for (int i = blockIdx.y * kThreads + threadIdx.x; i < heads * units; i += step) {
-        const int head = i / units, u = i % units;
-        const bool query = head < a.q.heads;
-        const RopeHeads& t = query ? a.q : a.k;
-        const int h = query ? head : head - a.q.heads;
-        const half_t* x = t.in + row * t.in_token + h * t.in_head;
-        half_t* y = t.out + row * t.out_token + h * t.out_head;
-        if (u >= a.rotated) {
-            const int d = a.rotary + 16 * (u - a.rotated);
-            store16(y + d, a.dim - d, load16(x + d, a.dim - d));
-            continue;
-        }
-        const int first = 8 * u, n = half_r - first;        // pairs of this unit: the first n of 8
-        if (at != u) {
-            at = u;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const double turns = position * (a.freqs[first + min(j, n - 1)] * 0.15915494309189535);
-                sincospif(2.0f * static_cast<float>(turns - __builtin_rint(turns)), &s[j], &c[j]);
-                s[j] *= a.amplitude;
-                c[j] *= a.amplitude;
-            }
-        }
-        const auto rotate = [&](half_t x0, half_t x1, int j, half_t& y0, half_t& y1) {
-            const float p = static_cast<float>(x0), q = static_cast<float>(x1);
-            y0 = static_cast<half_t>(p * c[j] - q * s[j]);
-            y1 = static_cast<half_t>(q * c[j] + p * s[j]);
+    // a thread keeps its unit, or its units one after the other, through the heads
+    const int lanes = min(units, kThreads);
+    const int at_once = kThreads / lanes;       // heads
+    const int tid = threadIdx.x;
+    if (tid >= at_once * lanes) return;
+    for (int u = tid % lanes; u < units; u += lanes) {
+        const bool turned = u < a.rotated;
+        const int first = U * u;
+        // a unit's two runs of U channels; the next head's are on their way while
+        // this one's turn
+        const int rest = a.rotary + 2 * U * (u - a.rotated);
+        const int at0 = !turned ? rest : INTERLEAVED ? 2 * first : first;
+        const int at1 = turned && !INTERLEAVED ? a.rotary / 2 + first : at0 + U;
+        const bool both = U > 1 || at1 < a.dim;         // false: an odd channel
+        const int step = at_once * gridDim.y;
+        int head = tid / lanes + blockIdx.y * at_once;
+        Run<U> v[2], next[2];
+        const auto fetch = [&](int head, Run<U> (&r)[2]) {
+            const bool query = head < a.q.heads;
+            const half_t* x = query ? a.q.in + row * a.q.in_token + head * a.q.in_head
+                                    : a.k.in + row * a.k.in_token + (head - a.q.heads) * a.k.in_head;
+            r[0] = load_run<U>(x + at0);
+            if (both) r[1] = load_run<U>(x + at1);
         };
-        if constexpr (INTERLEAVED) {
-            const half16_t v = load16(x + 2 * first, 2 * n);
-            half16_t w;
+        if (head < heads) fetch(head, v);
+        float c[U], s[U];
+        if (turned) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                half_t y0, y1;
-                rotate(v[2 * j], v[2 * j + 1], j, y0, y1);
-                w[2 * j] = y0;
-                w[2 * j + 1] = y1;
+            for (int j = 0; j < U; ++j) {
+                const double turns = position * (a.freqs[first + j] * 0.15915494309189535);
+                const float part = static_cast<float>(turns - __builtin_rint(turns));
+                c[j] = a.amplitude * __builtin_amdgcn_cosf(part);
+                s[j] = a.amplitude * __builtin_amdgcn_sinf(part);
             }
-            store16(y + 2 * first, 2 * n, w);
-        } else {
-            const half8_t v0 = load8(x + first, n), v1 = load8(x + half_r + first, n);
-            half8_t w0, w1;
+        }
+        for (; head < heads; head += step) {
+            if (head + step < heads) fetch(head + step, next);
+            if (turned) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                half_t y0, y1;
-                rotate(v0[j], v1[j], j, y0, y1);
-                w0[j] = y0;
-                w1[j] = y1;
+                for (int j = 0; j < U; ++j) {
+                    half_t& x0 = INTERLEAVED ? v[2 * j / U].v[2 * j % U] : v[0].v[j];
+                    half_t& x1 = INTERLEAVED ? v[(2 * j + 1) / U].v[(2 * j + 1) % U] : v[1].v[j];
+                    const float p = static_cast<float>(x0), q = static_cast<float>(x1);
+                    x0 = static_cast<half_t>(p * c[j] - q * s[j]);
+                    x1 = static_cast<half_t>(q * c[j] + p * s[j]);
+                }
             }
-            store8(y + first, n, w0);
-            store8(y + half_r + first, n, w1);
+            const bool query = head < a.q.heads;
+            half_t* y = query ? a.q.out + row * a.q.out_token + head * a.q.out_head
+                              : a.k.out + row * a.k.out_token + (head - a.q.heads) * a.k.out_head;
+            store_run<U>(y + at0, v[0]);
+            if (both) store_run<U>(y + at1, v[1]);
+            v[0] = next[0];
+            v[1] = next[1];
         }
     }
 }
 
-}  // namespace
-
-awq_status launch_rope(const RopeArgs& args, int64_t tokens, int n_seqs, hipStream_t stream) {
-    RopeArgs a = args;
-    a.rotated = static_cast<int>(ceil_div(a.rotary / 2, 8));
+template <int U>
+awq_status launch_units(RopeArgs a, int64_t tokens, int n_seqs, hipStream_t stream) {
+    a.rotated = a.rotary / 2 / U;
     const bool in_place = (a.q.heads == 0 || a.q.in == a.q.out) && (a.k.heads == 0 || a.k.in == a.k.out);
-    a.passed = in_place ? 0 : static_cast<int>(ceil_div(a.dim - a.rotary, 16));
-    const int64_t work = static_cast<int64_t>(a.q.heads + a.k.heads) * (a.rotated + a.passed);
-    const unsigned split = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(ceil_div(work, kThreads), 1024 / std::max<int64_t>(1, tokens * n_seqs))));
-    const dim3 grid(static_cast<unsigned>(tokens), split, static_cast<unsigned>(n_seqs));
+    a.passed = in_place ? 0 : static_cast<int>(ceil_div(a.dim - a.rotary, 2 * U));
+    // few tokens: their heads over several blocks, up to four a CU in all
+    const int at_once = std::max(1, kThreads / (a.rotated + a.passed));
+    const int64_t passes = ceil_div(static_cast<int64_t>(a.q.heads) + a.k.heads, at_once);
+    const int64_t split = std::max<int64_t>(1, std::min<int64_t>(passes, 4 * cu_count() / (tokens * n_seqs)));
+    const dim3 grid(static_cast<unsigned>(tokens), static_cast<unsigned>(split), static_cast<unsigned>(n_seqs));
     const bool batch = a.positions == nullptr;
     if (a.interleaved) {
-        if (batch) hipLaunchKernelGGL((rope_kernel<true, true>), grid, dim3(kThreads), 0, stream, a);
-        else hipLaunchKernelGGL((rope_kernel<true, false>), grid, dim3(kThreads), 0, stream, a);
+        if (batch) hipLaunchKernelGGL((rope_kernel<true, true, U>), grid, dim3(kThreads), 0, stream, a);
+        else hipLaunchKernelGGL((rope_kernel<true, false, U>), grid, dim3(kThreads), 0, stream, a);
     } else {
-        if (batch) hipLaunchKernelGGL((rope_kernel<false, true>), grid, dim3(kThreads), 0, stream, a);
-        else hipLaunchKernelGGL((rope_kernel<false, false>), grid, dim3(kThreads), 0, stream, a);
+        if (batch) hipLaunchKernelGGL((rope_kernel<false, true, U>), grid, dim3(kThreads), 0, stream, a);
+        else hipLaunchKernelGGL((rope_kernel<false, false, U>), grid, dim3(kThreads), 0, stream, a);
     }
     return last_launch_status();
+}
+
+}  // namespace
+
+// Units of 8, 4, 2 or 1 pairs, the most that divide a head (40 of 80 channels
+// rotated, 8192 tokens of 40 heads: 27 us in units of 4, 88 in units of 8 with a
+// rest by the element).
+awq_status launch_rope(const RopeArgs& a, int64_t tokens, int n_seqs, hipStream_t stream) {
+    const int sizes = a.rotary / 2 | (a.dim - a.rotary) / 2 | ((a.dim - a.rotary) % 2 ? 1 : 0);
+    if (sizes % 8 == 0) return launch_units<8>(a, tokens, n_seqs, stream);
+    if (sizes % 4 == 0) return launch_units<4>(a, tokens, n_seqs, stream);
+    if (sizes % 2 == 0) return launch_units<2>(a, tokens, n_seqs, stream);
+    return launch_units<1>(a, tokens, n_seqs, stream);
 }
 
 }  // namespace awq
