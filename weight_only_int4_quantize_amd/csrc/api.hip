@@ -918,7 +918,7 @@ size_t awq_kv_attention_workspace_bytes(const awq_kv_cache* cache, const awq_kv_
         return 0;
     if (empty) return 256;
     return kv_attention_workspace_bytes(seqs->n_seqs, cache->n_kv_heads, n_heads / cache->n_kv_heads, cache->head_dim,
-                                        seqs->max_tokens, seqs->max_len, cache->format);
+                                        seqs->max_tokens, seqs->max_len);
 }
 
 awq_status awq_kv_attention(const awq_kv_cache* cache, const awq_kv_seqs* seqs, const void* q_f16,
@@ -964,7 +964,7 @@ awq_status awq_kv_attention(const awq_kv_cache* cache, const awq_kv_seqs* seqs, 
     if (workspace) {
         if (reinterpret_cast<uintptr_t>(workspace) & 255) return AWQ_ERR_ALIGN;
         if (workspace_bytes < kv_attention_workspace_bytes(a.n_seqs, a.c.heads, a.ratio, a.head_dim, a.max_tokens,
-                                                           a.c.max_len, a.format))
+                                                           a.c.max_len))
             return AWQ_ERR_WORKSPACE;
     }
     return launch_kv_attention(a, workspace, as_stream(stream));

@@ -56,8 +56,7 @@ __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 64 ? 4 : D <= 96 ? 3 : D 
     constexpr int SO = D + 4;
     constexpr int kFloats = part_floats(kDecodeRows, D);
     typedef uint32_t words_t __attribute__((ext_vector_type(KW)));
-    __shared__ __attribute__((aligned(16))) float so_all[std::max(kDecodeWaves * kDecodeRows * SO,
-                                                                 join_floats(kDecodeRows, NT))];
+    __shared__ __attribute__((aligned(16))) float so_all[kDecodeWaves * kDecodeRows * SO];
     float(*so)[kDecodeRows][SO] = reinterpret_cast<float(*)[kDecodeRows][SO]>(so_all);
     __shared__ float sm[kDecodeWaves][kDecodeRows], sl[kDecodeWaves][kDecodeRows];
     __shared__ int s_flag;
@@ -300,7 +299,7 @@ __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 64 ? 4 : D <= 96 ? 3 : D 
     const Rows rw{kv_head, row0, rows, last_split - first_split + 1, split - first_split,
                   sp.partials + tile_id * n_splits * kFloats, static_cast<int64_t>(n_splits) * kFloats * 4,
                   sp.counters + tile_id};
-    finish_rows<D, kDecodeRows, NT>(a, sq, rw, [&](int p) { return (first_split + p) * kFloats; }, so_all, SO, &sm[0][0],
+    finish_rows<D, kDecodeRows, NT, true>(a, sq, rw, [&](int p) { return (first_split + p) * kFloats; }, so_all, SO, &sm[0][0],
                                     &sl[0][0], so_all, &s_flag);
 }
 
@@ -612,7 +611,7 @@ void launch_d(const KvAttentionArgs& a, const Plan& p, const Split& sp, hipStrea
 }  // namespace
 
 awq_status launch_kv4_attention(const KvAttentionArgs& a, void* workspace, hipStream_t stream) {
-    const Plan p = plan_for(a.n_seqs, a.c.heads, a.ratio, a.max_tokens, a.c.max_len, workspace != nullptr, AWQ_KV_INT4);
+    const Plan p = plan_for(a.n_seqs, a.c.heads, a.ratio, a.max_tokens, a.c.max_len, workspace != nullptr);
     if (!launchable(p, a.c.heads)) return AWQ_ERR_SHAPE;
     const Split sp = split_of(p, workspace);
     switch (a.head_dim) {

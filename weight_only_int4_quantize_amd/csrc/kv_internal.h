@@ -218,7 +218,7 @@ struct KvAttentionArgs {
     int window;                            // 0: none
 };
 size_t kv_attention_workspace_bytes(int n_seqs, int kv_heads, int ratio, int head_dim, int64_t max_tokens,
-                                    int64_t max_len, int format);
+                                    int64_t max_len);
 awq_status launch_kv_attention(const KvAttentionArgs& a, void* workspace, hipStream_t stream);
 awq_status launch_kv4_attention(const KvAttentionArgs& a, void* workspace, hipStream_t stream);
 
