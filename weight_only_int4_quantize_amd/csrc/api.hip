@@ -957,6 +957,7 @@ awq_status awq_kv_attention(const awq_kv_cache* cache, const awq_kv_seqs* seqs, 
     a.n_seqs = seqs->n_seqs;
     a.format = cache->format;
     a.ratio = n_heads / cache->n_kv_heads;
+    a.by_ratio = KvDivisor(static_cast<uint32_t>(a.ratio));
     a.max_tokens = seqs->max_tokens;        // as the workspace query counts
     a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     a.causal = causal != 0;

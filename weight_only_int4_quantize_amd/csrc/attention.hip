@@ -90,8 +90,8 @@ __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 64 ? 4 : D <= 96 ? 3 : D 
     const int rows = min(kDecodeRows, all_rows - row0);
     const Span span = row_span(a, sq, row0, rows);
     // the splits that hold a visible position; none at all: split 0 writes zeros
-    const int first_split = span.begin < span.end ? span.begin / sp.tokens : 0;
-    const int last_split = span.begin < span.end ? (span.end - 1) / sp.tokens : 0;
+    const int first_split = span.begin < span.end ? sp.by_tokens.of(span.begin) : 0;
+    const int last_split = span.begin < span.end ? sp.by_tokens.of(span.end - 1) : 0;
     if (split < first_split || split > last_split) return;
     const int page_mask = (1 << c.log2_page) - 1;
     const int64_t page_bytes = static_cast<int64_t>(D) << c.log2_page;
@@ -105,10 +105,10 @@ __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 64 ? 4 : D <= 96 ? 3 : D 
 #pragma unroll
     for (int i = 0; i < 2 * KC; ++i) qf[i] = half8_t{};
     if (col < rows) {
-        const int token = row / a.ratio;
+        const int token = a.by_ratio.of(row);
         visible(a, sq, token, lo, hi);
         const half_t* q = a.q + (static_cast<int64_t>(sq.row0) + token) * a.q_token +
-                          (kv_head * a.ratio + row % a.ratio) * a.q_head;
+                          ((kv_head - token) * a.ratio + row) * a.q_head;
 #pragma unroll
         for (int i = 0; i < KC; ++i)
             if (quarter + 4 * i < DC) {
@@ -372,8 +372,8 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv_pre
     if (row0 >= all_rows) return;
     const int rows = min(kPrefillRows, all_rows - row0);
     const Span span = row_span(a, sq, row0, rows);
-    const int first_split = span.begin < span.end ? span.begin / sp.tokens : 0;
-    const int last_split = span.begin < span.end ? (span.end - 1) / sp.tokens : 0;
+    const int first_split = span.begin < span.end ? sp.by_tokens.of(span.begin) : 0;
+    const int last_split = span.begin < span.end ? sp.by_tokens.of(span.end - 1) : 0;
     if (split < first_split || split > last_split) return;
 
     const int wrow = wave * 32 + col;
@@ -382,10 +382,10 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv_pre
 #pragma unroll
     for (int i = 0; i < DC; ++i) qf[i] = half8_t{};
     if (wrow < rows) {
-        const int token = (row0 + wrow) / a.ratio;
+        const int token = a.by_ratio.of(row0 + wrow);
         visible(a, sq, token, lo, hi);
         const half_t* q = a.q + (static_cast<int64_t>(sq.row0) + token) * a.q_token +
-                          (kv_head * a.ratio + (row0 + wrow) % a.ratio) * a.q_head;
+                          ((kv_head - token) * a.ratio + row0 + wrow) * a.q_head;
 #pragma unroll
         for (int i = 0; i < DC; ++i) {
             qf[i] = *reinterpret_cast<const half8_t*>(q + 16 * i + 8 * half);

@@ -46,7 +46,7 @@ __device__ inline half8_t first_n(half8_t v, int n) {
 // half a piece each), so a lane needs one (s, lo) per piece and token.
 template <int D, int NP>
 __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 64 ? 4 : D <= 96 ? 3 : D <= 192 ? 2 : 1) void kv4_decode_kernel(
-    KvAttentionArgs a, Split sp, int n_splits) {
+    KvAttentionArgs a, Split sp, int n_splits, int row_tiles) {
     constexpr int PC = D / 32;              // pieces of a key
     constexpr bool HALF = D == 64;          // half pieces
     constexpr int KC = HALF ? 1 : (PC + 3) / 4;
@@ -73,10 +73,9 @@ __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 64 ? 4 : D <= 96 ? 3 : D 
     // long sequences have. (With splits fastest, two of them put every
     // sequence's first on the even XCDs and the seconds, often short or empty,
     // on the odd: 64 sequences of 8192 down to 2048 tokens 100 us, now 87.)
-    const int kv_head = blockIdx.x % c.heads;
-    const int row_tile = blockIdx.x / c.heads;
-    const int row0 = row_tile * kDecodeRows;
-    const int b = blockIdx.y;
+    const int kv_head = blockIdx.x;
+    const int row0 = (blockIdx.y & (row_tiles - 1)) * kDecodeRows;     // one row tile or two
+    const int b = blockIdx.y >> (row_tiles - 1);
     const int split = n_splits - 1 - blockIdx.z;
     const KvSeq sq = kv_seq_shared(c, b);
     const int all_rows = sq.n * a.ratio;
@@ -84,8 +83,8 @@ __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 64 ? 4 : D <= 96 ? 3 : D 
     const int rows = min(kDecodeRows, all_rows - row0);
     const Span span = row_span(a, sq, row0, rows);
     // the splits that hold a visible position; none at all: split 0 writes zeros
-    const int first_split = span.begin < span.end ? span.begin / sp.tokens : 0;
-    const int last_split = span.begin < span.end ? (span.end - 1) / sp.tokens : 0;
+    const int first_split = span.begin < span.end ? sp.by_tokens.of(span.begin) : 0;
+    const int last_split = span.begin < span.end ? sp.by_tokens.of(span.end - 1) : 0;
     if (split < first_split || split > last_split) return;
     const int page = 1 << c.log2_page;
     const int from = max(span.begin, split * sp.tokens) / kTile;
@@ -98,10 +97,10 @@ __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 64 ? 4 : D <= 96 ? 3 : D 
 #pragma unroll
     for (int i = 0; i < KC * KW; ++i) qf[i] = half8_t{};
     if (col < rows) {
-        const int token = row / a.ratio;
+        const int token = a.by_ratio.of(row);
         visible(a, sq, token, lo, hi);
         const half_t* q = a.q + (static_cast<int64_t>(sq.row0) + token) * a.q_token +
-                          (kv_head * a.ratio + row % a.ratio) * a.q_head;
+                          ((kv_head - token) * a.ratio + row) * a.q_head;
 #pragma unroll
         for (int i = 0; i < KC; ++i) {
             const int first = HALF ? 16 * quarter : 32 * (quarter + 4 * i);
@@ -295,7 +294,7 @@ __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 64 ? 4 : D <= 96 ? 3 : D 
         sl[0][tid] = ll;
     }
     __syncthreads();
-    const int64_t tile_id = static_cast<int64_t>(b) * gridDim.x + blockIdx.x;
+    const int64_t tile_id = static_cast<int64_t>(blockIdx.y) * c.heads + kv_head;
     const Rows rw{kv_head, row0, rows, last_split - first_split + 1, split - first_split,
                   sp.partials + tile_id * n_splits * kFloats, static_cast<int64_t>(n_splits) * kFloats * 4,
                   sp.counters + tile_id};
@@ -362,8 +361,8 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv4_pr
     if (row0 >= all_rows) return;
     const int rows = min(kPrefillRows, all_rows - row0);
     const Span span = row_span(a, sq, row0, rows);
-    const int first_split = span.begin < span.end ? span.begin / sp.tokens : 0;
-    const int last_split = span.begin < span.end ? (span.end - 1) / sp.tokens : 0;
+    const int first_split = span.begin < span.end ? sp.by_tokens.of(span.begin) : 0;
+    const int last_split = span.begin < span.end ? sp.by_tokens.of(span.end - 1) : 0;
     if (split < first_split || split > last_split) return;
 
     const int wrow = wave * 32 + col;
@@ -372,10 +371,10 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv4_pr
 #pragma unroll
     for (int i = 0; i < DC; ++i) qf[i] = half8_t{};
     if (wrow < rows) {
-        const int token = (row0 + wrow) / a.ratio;
+        const int token = a.by_ratio.of(row0 + wrow);
         visible(a, sq, token, lo, hi);
         const half_t* q = a.q + (static_cast<int64_t>(sq.row0) + token) * a.q_token +
-                          (kv_head * a.ratio + (row0 + wrow) % a.ratio) * a.q_head;
+                          ((kv_head - token) * a.ratio + row0 + wrow) * a.q_head;
 #pragma unroll
         for (int i = 0; i < DC; ++i) {
             qf[i] = *reinterpret_cast<const half8_t*>(q + 16 * i + 8 * half);
@@ -593,9 +592,9 @@ template <int D, int NP>
 void launch_np(const KvAttentionArgs& a, const Plan& p, const Split& sp, hipStream_t stream) {
     if (p.decode)
         hipLaunchKernelGGL((kv4_decode_kernel<D, NP>),
-                           dim3(static_cast<unsigned>(p.row_tiles * a.c.heads), static_cast<unsigned>(a.n_seqs),
+                           dim3(static_cast<unsigned>(a.c.heads), static_cast<unsigned>(p.row_tiles * a.n_seqs),
                                 static_cast<unsigned>(p.splits)),
-                           dim3(kDecodeWaves * kWave), 0, stream, a, sp, p.splits);
+                           dim3(kDecodeWaves * kWave), 0, stream, a, sp, p.splits, static_cast<int>(p.row_tiles));
     else
         hipLaunchKernelGGL((kv4_prefill_kernel<D, NP>),
                            dim3(static_cast<unsigned>(p.row_tiles * p.splits * a.c.heads), 1,

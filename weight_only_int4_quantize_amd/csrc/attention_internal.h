@@ -18,6 +18,7 @@ constexpr float kLn2 = 0.69314718056f;
 // [s * tokens, (s + 1) * tokens).
 struct Split {
     int tokens;
+    KvDivisor by_tokens;
     float* partials;    // per (row tile, split): [rows][D] outputs, [rows] maxima, [rows] sums
     int* counters;      // per row tile, zero between launches
 };
@@ -81,8 +82,8 @@ __device__ inline void visible(const KvAttentionArgs& a, const KvSeq& sq, int to
     lo = a.window > 0 ? max(0, max(p, -1) - a.window + 1) : 0;
 }
 __device__ inline Span row_span(const KvAttentionArgs& a, const KvSeq& sq, int row0, int rows) {
-    const int first = row0 / a.ratio;
-    const int last = min(sq.n - 1, (row0 + rows - 1) / a.ratio);
+    const int first = a.by_ratio.of(row0);
+    const int last = min(sq.n - 1, a.by_ratio.of(row0 + rows - 1));
     Span s;
     visible(a, sq, first, s.begin, s.all_end);
     visible(a, sq, last, s.all_begin, s.end);
@@ -92,12 +93,12 @@ __device__ inline Span row_span(const KvAttentionArgs& a, const KvSeq& sq, int r
 // The output of one row: o (in true units) / sum, and its lse.
 __device__ inline void store_lse(const KvAttentionArgs& a, const KvSeq& sq, int kv_head, int row, float m, float sum) {
     if (a.lse == nullptr) return;
-    const int token = row / a.ratio, head = kv_head * a.ratio + row % a.ratio;
+    const int token = a.by_ratio.of(row), head = (kv_head - token) * a.ratio + row;
     a.lse[(static_cast<int64_t>(sq.row0) + token) * (static_cast<int64_t>(a.c.heads) * a.ratio) + head] =
         sum == 0.f ? -__builtin_huge_valf() : (m + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 __device__ inline half_t* out_row(const KvAttentionArgs& a, const KvSeq& sq, int kv_head, int row) {
-    const int token = row / a.ratio, head = kv_head * a.ratio + row % a.ratio;
+    const int token = a.by_ratio.of(row), head = (kv_head - token) * a.ratio + row;
     return a.out + (static_cast<int64_t>(sq.row0) + token) * a.out_token + head * a.out_head;
 }
 
@@ -345,6 +346,7 @@ inline size_t plan_bytes(const Plan& p, int n_seqs, int kv_heads, int head_dim) 
 inline Split split_of(const Plan& p, void* workspace) {
     Split sp;
     sp.tokens = p.tokens;
+    sp.by_tokens = KvDivisor(static_cast<uint32_t>(p.tokens));
     sp.counters = static_cast<int*>(workspace);
     sp.partials = workspace ? reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterBytes) : nullptr;
     return sp;
