@@ -183,6 +183,23 @@ __device__ inline half8_t kv4_numbers8(uint32_t w, half8_t s, half8_t lo) {
     }
     return r;
 }
+// n / d for 0 <= n < 2^31 in three instructions (a division takes some twenty, and
+// their code counts where a block runs it once): with 2^l the power of two from d
+// up and m = floor(2^32 (2^l - d) / d) + 1, it is (n m / 2^32 + n) / 2^l.
+struct KvDivisor {
+    uint32_t m = 1;
+    int l = 0;
+    KvDivisor() = default;
+    explicit KvDivisor(uint32_t d) {
+        while ((uint64_t{1} << l) < d) ++l;
+        m = static_cast<uint32_t>(((uint64_t{1} << 32) * ((uint64_t{1} << l) - d)) / d + 1);
+    }
+    __host__ __device__ int of(int n) const {
+        const uint32_t u = static_cast<uint32_t>(n);
+        return static_cast<int>((static_cast<uint32_t>((static_cast<uint64_t>(u) * m) >> 32) + u) >> l);
+    }
+};
+
 // ---- launchers ----
 struct KvWriteArgs {
     KvPages c;
@@ -204,23 +221,6 @@ awq_status launch_kv_read(const KvReadArgs& a, hipStream_t stream);
 // the same over the 4-bit cache (format AWQ_KV_INT4)
 awq_status launch_kv4_write(const KvWriteArgs& a, hipStream_t stream);
 awq_status launch_kv4_read(const KvReadArgs& a, hipStream_t stream);
-
-// n / d for 0 <= n < 2^31 in three instructions (a division takes some twenty, and
-// their code counts where a block runs it once): with 2^l the power of two from d
-// up and m = floor(2^32 (2^l - d) / d) + 1, it is (n m / 2^32 + n) / 2^l.
-struct KvDivisor {
-    uint32_t m = 1;
-    int l = 0;
-    KvDivisor() = default;
-    explicit KvDivisor(uint32_t d) {
-        while ((uint64_t{1} << l) < d) ++l;
-        m = static_cast<uint32_t>(((uint64_t{1} << 32) * ((uint64_t{1} << l) - d)) / d + 1);
-    }
-    __host__ __device__ int of(int n) const {
-        const uint32_t u = static_cast<uint32_t>(n);
-        return static_cast<int>((static_cast<uint32_t>((static_cast<uint64_t>(u) * m) >> 32) + u) >> l);
-    }
-};
 
 struct KvAttentionArgs {
     KvPages c;

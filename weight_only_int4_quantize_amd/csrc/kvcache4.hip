@@ -172,7 +172,7 @@ __device__ inline bool chunk_of(const KvPages& c, const KvSeq& sq, int b, int in
 // thread takes eight tokens of pairs of channels. Rows are D + 4 halves apart:
 // the four words' rows are then 16 banks apart.
 template <int D>
-__global__ __launch_bounds__(kThreads) void kv4_write_kernel(KvWriteArgs a) {
+__global__ __launch_bounds__(kThreads) void kv4_write_kernel(KvWriteArgs a, KvDivisor by_heads) {
     constexpr int PC = D / 32;
     constexpr int KL = D / 8;                                   // lanes to a token's keys
     constexpr int VL = D <= 64 ? 8 : D <= 128 ? 16 : 32;        // to its values, at least D / 8
@@ -183,11 +183,12 @@ __global__ __launch_bounds__(kThreads) void kv4_write_kernel(KvWriteArgs a) {
     __shared__ __attribute__((aligned(16))) float lo[kChunk], step[kChunk], inv[kChunk];
     const KvPages& c = a.c;
     const int tid = threadIdx.x;
-    const int head = blockIdx.x % c.heads;
+    const int index = by_heads.of(blockIdx.x);
+    const int head = blockIdx.x - index * c.heads;
     const int b = blockIdx.y;
     const KvSeq sq = kv_seq_shared(c, b);
     Chunk ch;
-    if (!chunk_of(c, sq, b, static_cast<int>(blockIdx.x / c.heads), head, ch)) return;
+    if (!chunk_of(c, sq, b, index, head, ch)) return;
     const half_t* xk = a.k + head * a.k_head + ch.row * a.k_token;
     const half_t* xv = a.v + head * a.v_head + ch.row * a.v_token;
     const int tokens = ch.t1 - ch.t0;
@@ -280,12 +281,12 @@ __global__ __launch_bounds__(kThreads) void kv4_write_kernel(KvWriteArgs a) {
 
 // Read: one block per (32 token slots, head, side) of the tokens asked for.
 template <int D>
-__global__ __launch_bounds__(kThreads) void kv4_read_kernel(KvReadArgs a) {
+__global__ __launch_bounds__(kThreads) void kv4_read_kernel(KvReadArgs a, KvDivisor by_heads) {
     constexpr int PC = D / 32;
     const KvPages& c = a.c;
     const int tid = threadIdx.x;
-    const int head = blockIdx.x % c.heads;
-    const int index = blockIdx.x / c.heads;
+    const int index = by_heads.of(blockIdx.x);
+    const int head = blockIdx.x - index * c.heads;
     const bool values = blockIdx.y & 1;
     const int b = blockIdx.y >> 1;
     half_t* y = values ? a.v : a.k;
@@ -376,13 +377,15 @@ awq_status by_dim(const Args& a, int sides, const Launch& launch) {
 
 awq_status launch_kv4_write(const KvWriteArgs& a, hipStream_t stream) {
     return by_dim(a, 1, [&](auto dim, dim3 grid) {
-        hipLaunchKernelGGL((kv4_write_kernel<decltype(dim)::value>), grid, dim3(kThreads), 0, stream, a);
+        hipLaunchKernelGGL((kv4_write_kernel<decltype(dim)::value>), grid, dim3(kThreads), 0, stream, a,
+                           KvDivisor(static_cast<uint32_t>(a.c.heads)));
     });
 }
 
 awq_status launch_kv4_read(const KvReadArgs& a, hipStream_t stream) {
     return by_dim(a, 2, [&](auto dim, dim3 grid) {
-        hipLaunchKernelGGL((kv4_read_kernel<decltype(dim)::value>), grid, dim3(kThreads), 0, stream, a);
+        hipLaunchKernelGGL((kv4_read_kernel<decltype(dim)::value>), grid, dim3(kThreads), 0, stream, a,
+                           KvDivisor(static_cast<uint32_t>(a.c.heads)));
     });
 }
 
