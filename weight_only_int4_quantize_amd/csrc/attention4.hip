@@ -45,7 +45,7 @@ __device__ inline half8_t first_n(half8_t v, int n) {
 // takes whole pieces of 32 channels of a key, piece q + 4 i (at 64 channels
 // half a piece each), so a lane needs one (s, lo) per piece and token.
 template <int D, int NP>
-__global__ __launch_bounds__(kDecodeWaves* kWave, D <= 64 ? 4 : D <= 96 ? 3 : D <= 192 ? 2 : 1) void kv4_decode_kernel(
+__global__ __launch_bounds__(kDecodeWaves* kWave, D <= 96 ? 4 : D <= 128 ? 3 : 2) void kv4_decode_kernel(
     KvAttentionArgs a, Split sp, int n_splits, int row_tiles) {
     constexpr int PC = D / 32;              // pieces of a key
     constexpr bool HALF = D == 64;          // half pieces
@@ -90,28 +90,27 @@ __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 64 ? 4 : D <= 96 ? 3 : D 
     const int from = max(span.begin, split * sp.tokens) / kTile;
     const int to = (min(static_cast<int64_t>(span.end), (static_cast<int64_t>(split) + 1) * sp.tokens) + kTile - 1) / kTile;
 
-    // ---- queries: word w of piece i holds the channels of that word ----
+    // ---- queries, in LDS in operand order: word w of piece i holds the channels of
+    // that word (in registers they are 16 to 32 a lane, and 256 channels leave room
+    // for one wave per SIMD in place of two)
+    __shared__ half8_t qs[KC * KW][kWave];
     const int row = row0 + col;
     int lo = 0, hi = 0;
-    half8_t qf[KC * KW];
-#pragma unroll
-    for (int i = 0; i < KC * KW; ++i) qf[i] = half8_t{};
     if (col < rows) {
         const int token = a.by_ratio.of(row);
         visible(a, sq, token, lo, hi);
         const half_t* q = a.q + (static_cast<int64_t>(sq.row0) + token) * a.q_token +
                           ((kv_head - token) * a.ratio + row) * a.q_head;
-#pragma unroll
-        for (int i = 0; i < KC; ++i) {
-            const int first = HALF ? 16 * quarter : 32 * (quarter + 4 * i);
-            if (first < D)
-#pragma unroll
-                for (int w = 0; w < KW; ++w) {
-                    half8_t v = *reinterpret_cast<const half8_t*>(q + first + 8 * w);
-                    qf[i * KW + w] = a.scale_log2 < 0.f ? -v : v;
-                }
+        for (int i = wave; i < KC * KW; i += kDecodeWaves) {
+            const int first = (HALF ? 16 * quarter : 32 * (quarter + 4 * (i / KW))) + 8 * (i % KW);
+            half8_t v = {};
+            if (first < D) v = *reinterpret_cast<const half8_t*>(q + first);
+            qs[i][lane] = a.scale_log2 < 0.f ? -v : v;
         }
+    } else {
+        for (int i = wave; i < KC * KW; i += kDecodeWaves) qs[i][lane] = half8_t{};
     }
+    __syncthreads();
     const float qscale = fmaxf(fabsf(a.scale_log2), kTinyScale);
 
     float m = kNone, sum = 0.f;
@@ -195,7 +194,7 @@ __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 64 ? 4 : D <= 96 ? 3 : D 
                 for (int i = 0; i < KC; ++i)
 #pragma unroll
                     for (int w = 0; w < KW; ++w)
-                        x = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv4_numbers8(kr[s4][i][w], ksc[s4][i]), qf[i * KW + w], x,
+                        x = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv4_numbers8(kr[s4][i][w], ksc[s4][i]), qs[i * KW + w][lane], x,
                                                                    0, 0, 0);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[4 * s4 + e] = x[e];
