@@ -209,6 +209,23 @@ def test_write_extreme_values():
     m.check_read(m.len)
 
 
+@pytest.mark.parametrize("dim,page", [(64, 32), (128, 64)])
+def test_write_among_later_tokens(dim, page):
+    """Tokens written again, at every place of a word of eight, leave the later
+    tokens of their pages."""
+    m = Model(24, 2, 2, dim, page, 100)
+    m.append([100, 70])
+    for first, n in ((35, 1), (64, 3), (8, 8), (30, 7), (95, 4)):
+        say("kv4 write among", dim, first, n)
+        s, cu, lens, table = m.seqs([n, 0], lens=[first + n, 70])
+        k, v = m.values(n), m.values(n, 0.3)
+        awq.awq_kv_write(m.cache, s, dev(k), dev(v))
+        lo.write(m.kc, m.ks, k, table, cu, lens, "k")
+        lo.write(m.vc, m.vs, v, table, cu, lens, "v")
+        m.check()
+    m.check_read([100, 70])
+
+
 def test_write_many_random_groups():
     """Half a million groups over 30 binary orders of magnitude."""
     m = Model([4], 1, 16, 256, 256, 4096)

@@ -273,7 +273,7 @@ __global__ __launch_bounds__(kThreads) void kv4_write_kernel(KvWriteArgs a, KvDi
         for (int e = 0; e < 2; ++e) {
             uint32_t* word = out + (d + e) * 4 + w;
             uint32_t bits = word_of(code[e]) & mine;
-            if (first > 0) bits |= *word & ~from_code(first);       // the old tokens' codes stay
+            if (mine != ~0u) bits |= *word & ~mine;     // the other tokens' codes stay
             *word = bits;
         }
     }
