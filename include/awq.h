@@ -681,7 +681,9 @@ typedef struct {
  *   lo = min x,  s = the largest fp16 number not above (max x - lo) / 15
  *   codes = clamp(round((x - lo) / s), 0, 15), 0 where s is 0
  * A number thus carries at most half a step (plus 15 times what s was cut by,
- * under 2^-10 of it, at the top of the range); what was written before stays.
+ * under 2^-10 of it, at the top of the range); what was written before stays,
+ * also at later places of the page. A call takes up to 2^24 pieces of 32
+ * consecutive tokens (that max_tokens from any place can touch) times heads.
  * NaN is stored as 0, an infinity as +-65504.
  *
  *   k_f16, v_f16     device, fp16 [n_tokens, n_kv_heads, head_dim], the
@@ -724,7 +726,9 @@ awq_status awq_kv_read(const awq_kv_cache* cache, const awq_kv_seqs* seqs,
  * the weights enter the second product as two fp16 numbers (a weight cut to
  * fp16 and what that left), within 2^-20 of themselves. A query with a NaN
  * that sees a position gets NaN (o and lse); no other row is touched by it,
- * or by an infinity.
+ * or by an infinity. With AWQ_KV_INT4 the products' numbers are the cached
+ * ones, those awq_kv_read gives. Every position below kv_len in a page that
+ * the cache holds has to have been written.
  *
  *   q_f16        device, fp16 [n_tokens, n_heads, head_dim], channels
  *                contiguous, 16-byte aligned, strides in halves, multiples
@@ -766,8 +770,9 @@ awq_status awq_kv_attention(const awq_kv_cache* cache, const awq_kv_seqs* seqs,
  * to 8 bits by a row's or a group's scale,
  *   a = max(max |y|, 1e-5),  s = a / top,  code = round(y * (1 / s))
  * with top = 127 (int8, round-half-to-even) or 448 (OCP fp8 1-4-3). A row or
- * group with a NaN among its y has the scale NaN and codes 0; with fp16 the
- * elements are what the formula gives.
+ * group with a NaN among its y has the scale NaN, one with an infinity (of a
+ * weight) the scale infinity, and both the codes 0; with fp16 the elements are
+ * what the formula gives.
  *
  *   x_f16          device, fp16 [rows, width], rows x_stride halves apart
  *   residual_f16   device, fp16 [rows, width] or NULL (h = x)
@@ -777,7 +782,7 @@ awq_status awq_kv_attention(const awq_kv_cache* cache, const awq_kv_seqs* seqs,
  *   weight_offset  finite; 0, or 1 where the stored weight is the difference
  *                  from 1
  *   eps            finite, >= 0
- *   rows, width    rows >= 0, 1 <= width <= 2^24
+ *   rows, width    0 <= rows < 2^31, 1 <= width <= 2^24
  *   format         AWQ_NORM_F16, _INT8 (signed bytes) or _E4M3
  *   group_size     0 (one scale a row), or 32, 64, 128, 256 or 512 channels
  *                  with width % group_size == 0; 0 with AWQ_NORM_F16
@@ -849,10 +854,10 @@ awq_status awq_rope_frequencies(int rotary_dim, double base, int scaling, double
  *                tokens past max_tokens are not processed). Rows of no
  *                sequence are left as they were. Exactly one of the two.
  *   q, k         tensors [n_tokens, heads, head_dim] in fp16, channels
- *                contiguous, strides in halves; heads 0 (or a NULL pointer to
- *                the struct): none. out may be in itself, with the same
- *                strides; otherwise it must not overlap an input, and all of a
- *                row is written.
+ *                contiguous, strides in halves; heads up to 65535, 0 (or a
+ *                NULL pointer to the struct): none. out may be in itself, with
+ *                the same strides; otherwise it must not overlap an input, and
+ *                all of a row is written.
  *   head_dim     rotary_dim <= head_dim <= 4096
  *   n_tokens     0 .. 2^24 - 1
  * Pointers 2-byte aligned (rows need no alignment; 16-byte aligned ones are
