@@ -171,6 +171,9 @@ __device__ inline bool chunk_of(const KvPages& c, const KvSeq& sq, int b, int in
 // Values: a token's range by LANES lanes, its row kept in LDS; then a
 // thread takes eight tokens of pairs of channels. Rows are D + 4 halves apart:
 // the four words' rows are then 16 banks apart.
+// Bound by HBM: 11776 tokens of 32 heads of 128, 193 MB read and 55 MB written,
+// 55 us alone, 4.5 TB/s (a copy reaches 5.2). 64 x 1 token of 8 heads 4.9 us,
+// latencies.
 template <int D>
 __global__ __launch_bounds__(kThreads) void kv4_write_kernel(KvWriteArgs a, KvDivisor by_heads) {
     constexpr int PC = D / 32;
@@ -280,6 +283,9 @@ __global__ __launch_bounds__(kThreads) void kv4_write_kernel(KvWriteArgs a, KvDi
 }
 
 // Read: one block per (32 token slots, head, side) of the tokens asked for.
+// Bound by the stores to HBM: the tokens above 55 us alone, 4.5 TB/s; the pair,
+// write and read, 107 us. Stored past the caches the read alone took 39 us, but
+// with what reads its result 125 against 108.
 template <int D>
 __global__ __launch_bounds__(kThreads) void kv4_read_kernel(KvReadArgs a, KvDivisor by_heads) {
     constexpr int PC = D / 32;

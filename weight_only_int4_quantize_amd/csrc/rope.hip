@@ -12,8 +12,8 @@
 // Bound by HBM: 2 bytes read and 2 written a number; a call of few tokens by a
 // launch's length. A thread keeps one place in the head and goes over the
 // token's heads with it, so the angles are computed once for several heads.
-// Measured (us): 8192 tokens, 32 + 8 heads of 128, 168 MB, 37, 4.5 TB/s (a
-// copy reaches 5.1); one token of 32 + 32 heads 2.7.
+// Measured (us): 8192 tokens, 32 + 8 heads of 128, 168 MB, 36, 4.6 TB/s (a
+// copy reaches 5.2); one token of 32 + 32 heads 2.8.
 #include <algorithm>
 
 #include "awq_internal.h"
