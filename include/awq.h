@@ -782,7 +782,10 @@ awq_status awq_kv_attention(const awq_kv_cache* cache, const awq_kv_seqs* seqs,
  *   weight_offset  finite; 0, or 1 where the stored weight is the difference
  *                  from 1
  *   eps            finite, >= 0
- *   rows, width    0 <= rows < 2^31, 1 <= width <= 2^24
+ *   rows, width    rows >= 0, 1 <= width <= 2^24; rows + 3 below 2^32
+ *                  over the threads of a row, width / 8 rounded up to a power
+ *                  of two from 64 to 1024 (some 2^26 rows up to 512 wide, 2^22
+ *                  past 4096 wide)
  *   format         AWQ_NORM_F16, _INT8 (signed bytes) or _E4M3
  *   group_size     0 (one scale a row), or 32, 64, 128, 256 or 512 channels
  *                  with width % group_size == 0; 0 with AWQ_NORM_F16

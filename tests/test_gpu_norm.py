@@ -193,19 +193,6 @@ def test_many_rows_and_none():
             check_f16(host(got), lo.rmsnorm(x, w, 1e-5, r)[1], 96)
 
 
-def test_more_rows_than_a_launch_takes():
-    """2^26 + 5 rows of 8 elements: past 2^32 threads."""
-    T, K = 2 ** 26 + 5, 8
-    say("rmsnorm", T, K)
-    g = torch.Generator(device="cuda").manual_seed(5)
-    x = torch.randn((T, K), device="cuda", dtype=torch.float16, generator=g)
-    codes, scales = awq.awq_rmsnorm(x, fmt="int8")
-    for a, b in ((0, 64), (2 ** 25, 2 ** 25 + 64), (2 ** 26 - 64, T)):
-        few, fs = awq.awq_rmsnorm(x[a:b], fmt="int8")
-        assert torch.equal(codes[a:b], few) and torch.equal(scales[a:b], fs)
-        check_8bit(host(few), host(fs), lo.rmsnorm(host(x[a:b]), None, 1e-5, None)[1], "int8", 0)
-
-
 def test_graph_replay_and_streams():
     x, r, w = inputs([8], 17, 4096)
     xd, rd, wd = dev(x), dev(r), dev(w)

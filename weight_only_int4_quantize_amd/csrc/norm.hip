@@ -11,8 +11,6 @@
 //
 // Bound by HBM: 2 bytes an element of x, r, the sum and y (4096 x 8192, 268 MB:
 // 51 us, 5.3 TB/s, a copy's rate), few rows by a launch's length.
-#include <algorithm>
-
 #include "awq_internal.h"
 
 namespace awq {
@@ -274,24 +272,12 @@ __global__ __launch_bounds__(TPR * rows_per_block(TPR)) void rmsnorm_kernel(Norm
 }
 
 template <int FORMAT, int TPR, int P>
-awq_status launch_p(NormArgs a, hipStream_t stream) {
-    constexpr int PER_BLOCK = rows_per_block(TPR);
-    constexpr int NT = TPR * PER_BLOCK;
-    constexpr int64_t kMost = ((int64_t{1} << 32) / NT - 1) * PER_BLOCK;     // a launch takes 2^32 threads along x
-    awq_status st = AWQ_OK;
-    for (int64_t left = a.rows; left > 0 && st == AWQ_OK; left -= kMost) {
-        a.rows = std::min(left, kMost);
-        hipLaunchKernelGGL((rmsnorm_kernel<FORMAT, TPR, P>), dim3(static_cast<unsigned>(ceil_div(a.rows, PER_BLOCK))),
-                           dim3(NT), 0, stream, a);
-        st = last_launch_status();
-        if (left <= kMost) break;
-        a.x += kMost * a.x_stride;
-        if (a.residual) a.residual += kMost * a.residual_stride;
-        if (a.sum) a.sum += kMost * a.sum_stride;
-        a.out = static_cast<char*>(a.out) + kMost * a.out_stride * (FORMAT == AWQ_NORM_F16 ? 2 : 1);
-        if (a.scales) a.scales += kMost * (a.group ? a.width / a.group : 1);
-    }
-    return st;
+awq_status launch_p(const NormArgs& a, hipStream_t stream) {
+    constexpr int NT = TPR * rows_per_block(TPR);
+    const int64_t blocks = ceil_div(a.rows, rows_per_block(TPR));
+    if (blocks >= (int64_t{1} << 32) / NT) return AWQ_ERR_SHAPE;      // a launch takes 2^32 threads along x
+    hipLaunchKernelGGL((rmsnorm_kernel<FORMAT, TPR, P>), dim3(static_cast<unsigned>(blocks)), dim3(NT), 0, stream, a);
+    return last_launch_status();
 }
 // As many threads to a row as it has pieces of eight, up to 1024: measured with a
 // residual and its sum (us, in brackets with a quarter as many threads and four
