@@ -727,8 +727,8 @@ awq_status awq_kv_read(const awq_kv_cache* cache, const awq_kv_seqs* seqs,
  * fp16 and what that left), within 2^-20 of themselves. A query with a NaN
  * that sees a position gets NaN (o and lse); no other row is touched by it,
  * or by an infinity. With AWQ_KV_INT4 the products' numbers are the cached
- * ones, those awq_kv_read gives. Every position below kv_len in a page that
- * the cache holds has to have been written.
+ * ones, those awq_kv_read gives, and a position that no query of its sequence
+ * sees may hold anything.
  *
  *   q_f16        device, fp16 [n_tokens, n_heads, head_dim], channels
  *                contiguous, 16-byte aligned, strides in halves, multiples

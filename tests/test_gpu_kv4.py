@@ -365,6 +365,26 @@ def test_attention_missing_pages(new, page):
     assert (got[0][new:] == 0).all()
 
 
+@pytest.mark.parametrize("page", [32, 64, 256])
+@pytest.mark.parametrize("new", [1, 9, 90])
+def test_attention_nothing_before_the_window(new, page):
+    """Positions before every query's window and behind the end hold NaN scales."""
+    m = Model(25, 2, 2, 64, page, 420)
+    m.append([400, 243])
+    q = m.rng.standard_normal((2 * new, 4, 64)).astype(np.float16)
+    plain = m.attend(q, [new, new], causal=True, window=21)
+    m.assert_attention(plain, 21)
+    for b in range(2):
+        first = int(m.len[b]) - new - 20        # the first query's window
+        for p in range(first // page + 1):
+            pid, n = int(m.table[b, p]), min(page, first - p * page)
+            m.cache.k_scales[pid, :, :, :n] = float("nan")
+            m.cache.v_scales[pid, :, :, :n] = float("nan")
+    got = m.attend(q, [new, new], causal=True, window=21)
+    np.testing.assert_array_equal(got[0], plain[0])
+    np.testing.assert_array_equal(got[1], plain[1])
+
+
 @pytest.mark.parametrize("new", [2, 70])
 def test_attention_values_far_apart(new):
     """Values whose sizes differ by 2^26 from token to token."""

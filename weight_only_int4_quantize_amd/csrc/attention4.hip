@@ -26,11 +26,17 @@ constexpr float kUnit = 12.0f;      // log2 of the weights' unit
 constexpr float kSlack = 3.0f;      // what a logit may pass the maximum by
 constexpr float kTinyScale = 1.0e-30f;  // |scale log2 e| below it counts as it (a masked logit times 0 would be NaN)
 
-// s and lo of the first n tokens as they are, of the others 0 (what lies behind
-// a sequence's end may be anything, NaN among it)
+// s and lo of the first n tokens, or of those from n on, as they are, of the
+// others 0 (what lies behind a sequence's end or before its window may be
+// anything, NaN among it)
 __device__ inline half8_t first_n(half8_t v, int n) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = j < n ? v[j] : static_cast<half_t>(0.f);
+    return v;
+}
+__device__ inline half8_t from_n(half8_t v, int n) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < n ? static_cast<half_t>(0.f) : v[j];
     return v;
 }
 
@@ -220,6 +226,13 @@ __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 96 ? 4 : D <= 128 ? 3 : 2
                 for (int j = 0; j < 2; ++j) {
                     vs[j] = first_n(vs[j], n - 8 * j);
                     vlo[j] = first_n(vlo[j], n - 8 * j);
+                }
+                if (span.begin > tb) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        vs[j] = from_n(vs[j], span.begin - j0 - 8 * j);
+                        vlo[j] = from_n(vlo[j], span.begin - j0 - 8 * j);
+                    }
                 }
             }
 
@@ -462,6 +475,13 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv4_pr
             for (int j = 0; j < 2; ++j) {
                 vs[j] = first_n(vs[j], n - 8 * j);
                 vlo[j] = first_n(vlo[j], n - 8 * j);
+            }
+        }
+        if (span.begin > tb) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                vs[j] = from_n(vs[j], span.begin - tb - 16 * wave - 8 * j);
+                vlo[j] = from_n(vlo[j], span.begin - tb - 16 * wave - 8 * j);
             }
         }
 #pragma unroll
