@@ -64,6 +64,42 @@ def test_the_most_sequences(new):
     assert torch.equal(by_batch, given)
 
 
+@pytest.mark.parametrize("dim,page,heads,ratio,new,causal,window", [
+    (64, 32, 4, 8, 4, True, 0),
+    (64, 64, 4, 1, 17, True, 30),
+    (96, 64, 4, 3, 9, True, 0),
+    (96, 32, 4, 1, 32, False, 0),
+    (128, 64, 4, 8, 3, True, 0),
+    (128, 32, 4, 5, 6, True, 33),
+    (128, 256, 4, 2, 16, False, 0),
+])
+@pytest.mark.parametrize("split", [True, False])
+def test_thirty_two_rows(dim, page, heads, ratio, new, causal, window, split):
+    """17 to 32 rows a kv head in a batch of bounds long enough for blocks of 32
+    rows: ragged lengths, missing pages, empty and short sequences, NaN queries,
+    rows before a sequence's start."""
+    say("kv4 rows", dim, page, ratio, new, window)
+    lens = [700, 0, 1, new, 2300, 64, 333, new - 1]
+    m = Model([45, dim, page, new], 8, heads, dim, page, max(lens))
+    m.append(lens)
+    news = [new, new, 1, new, new, 0, new, new]
+    q = m.rng.standard_normal((sum(news), heads * ratio, dim)).astype(np.float16)
+    table = m.table.copy()
+    table[4, 3] = -1
+    bound = 2 ** 16                 # 32 kv heads and more of 2^16 positions
+    got = m.attend(q, news, table=table, causal=causal, window=window, split=split, max_len=bound)
+    m.assert_attention(got, max(lens))
+    # as two blocks of 16 rows
+    two = m.attend(q, news, table=table, causal=causal, window=window, split=split)
+    m.assert_attention(two, max(lens))
+    q[news[0], 0] = np.nan          # a query of sequence 1, which is empty, and one of sequence 3
+    q[2 * new + 2, 1 % (heads * ratio)] = np.nan
+    o, lse, _ = m.attend(q, news, table=table, causal=causal, window=window, split=split, max_len=bound)
+    hit = np.isnan(q).any(-1) & np.isfinite(got[1])
+    assert np.isnan(o[hit]).all() and np.isnan(lse[hit]).all()
+    np.testing.assert_array_equal(o[~hit], got[0][~hit])
+
+
 def test_two_graphs_take_turns_on_a_workspace():
     m = Model(41, 3, 2, 128, 64, 1400)
     m.append([1300, 1, 700])

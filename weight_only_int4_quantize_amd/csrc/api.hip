@@ -917,8 +917,8 @@ size_t awq_kv_attention_workspace_bytes(const awq_kv_cache* cache, const awq_kv_
         seqs->max_tokens * (n_heads / cache->n_kv_heads) > INT32_MAX - 256)
         return 0;
     if (empty) return 256;
-    return kv_attention_workspace_bytes(seqs->n_seqs, cache->n_kv_heads, n_heads / cache->n_kv_heads, cache->head_dim,
-                                        seqs->max_tokens, seqs->max_len);
+    return kv_attention_workspace_bytes(cache->format, seqs->n_seqs, cache->n_kv_heads, n_heads / cache->n_kv_heads,
+                                        cache->head_dim, seqs->max_tokens, seqs->max_len);
 }
 
 awq_status awq_kv_attention(const awq_kv_cache* cache, const awq_kv_seqs* seqs, const void* q_f16,
@@ -964,8 +964,8 @@ awq_status awq_kv_attention(const awq_kv_cache* cache, const awq_kv_seqs* seqs, 
     a.window = static_cast<int>(std::min<int64_t>(window, INT32_MAX));
     if (workspace) {
         if (reinterpret_cast<uintptr_t>(workspace) & 255) return AWQ_ERR_ALIGN;
-        if (workspace_bytes < kv_attention_workspace_bytes(a.n_seqs, a.c.heads, a.ratio, a.head_dim, a.max_tokens,
-                                                           a.c.max_len))
+        if (workspace_bytes < kv_attention_workspace_bytes(a.format, a.n_seqs, a.c.heads, a.ratio, a.head_dim,
+                                                           a.max_tokens, a.c.max_len))
             return AWQ_ERR_WORKSPACE;
     }
     return launch_kv_attention(a, workspace, as_stream(stream));

@@ -639,15 +639,15 @@ void launch_d(const KvAttentionArgs& a, const Plan& p, const Split& sp, hipStrea
 
 }  // namespace
 
-size_t kv_attention_workspace_bytes(int n_seqs, int kv_heads, int ratio, int head_dim, int64_t max_tokens,
+size_t kv_attention_workspace_bytes(int format, int n_seqs, int kv_heads, int ratio, int head_dim, int64_t max_tokens,
                                     int64_t max_len) {
-    const Plan p = plan_for(n_seqs, kv_heads, ratio, max_tokens, max_len, true);
+    const Plan p = plan_for(format, head_dim, n_seqs, kv_heads, ratio, max_tokens, max_len, true);
     return launchable(p, kv_heads) ? plan_bytes(p, n_seqs, kv_heads, head_dim) : 0;
 }
 
 awq_status launch_kv_attention(const KvAttentionArgs& a, void* workspace, hipStream_t stream) {
     if (a.format == AWQ_KV_INT4) return launch_kv4_attention(a, workspace, stream);
-    const Plan p = plan_for(a.n_seqs, a.c.heads, a.ratio, a.max_tokens, a.c.max_len, workspace != nullptr);
+    const Plan p = plan_for(a.format, a.head_dim, a.n_seqs, a.c.heads, a.ratio, a.max_tokens, a.c.max_len, workspace != nullptr);
     if (!launchable(p, a.c.heads)) return AWQ_ERR_SHAPE;
     const Split sp = split_of(p, workspace);
     switch (a.head_dim) {

@@ -42,7 +42,8 @@ __device__ inline half8_t from_n(half8_t v, int n) {
 
 // ---------------------------------------------------------------- few rows
 
-// Decode: up to 16 query rows per block, the four waves walking the split's
+// Decode: 16 query rows per block, or 32 in two sets whose products share the
+// unpacked keys and values, the four waves walking the split's
 // 64-token tiles in turn, each on its own, as over the 8-bit cache.
 // v_mfma_f32_16x16x32_f16: lane l supplies row / column l % 16 and k-slots
 // 8 (l / 16) .. + 7, and holds results 4 (l / 16) + e of column l % 16.
@@ -55,21 +56,22 @@ __device__ inline half8_t from_n(half8_t v, int n) {
 // the time, the matrix cores 20%); 131072 and 131072 tokens 60 us, 5.2 TB/s.
 // 1 x 1000 tokens of 32 heads 7.8 us, a row of latencies. Not faster: six,
 // eight or sixteen waves a block, two tiles in flight, splits of 512 positions.
-template <int D, int NP>
-__global__ __launch_bounds__(kDecodeWaves* kWave, D <= 96 ? 4 : D <= 128 ? 3 : 2) void kv4_decode_kernel(
-    KvAttentionArgs a, Split sp, int n_splits, int row_tiles) {
+template <int D, int NP, int SETS>
+__global__ __launch_bounds__(kDecodeWaves* kWave, SETS == 2 ? 2 : D <= 96 ? 4 : D <= 128 ? 3 : 2) void
+kv4_decode_kernel(KvAttentionArgs a, Split sp, int n_splits, int row_tiles) {
     constexpr int PC = D / 32;              // pieces of a key
     constexpr bool HALF = D == 64;          // half pieces
     constexpr int KC = HALF ? 1 : (PC + 3) / 4;
     constexpr int KW = HALF ? 2 : 4;        // words of a lane's piece
     constexpr int DT = D / 16;              // 16-channel tiles of the output
     constexpr int NT = kDecodeWaves * kWave;
+    constexpr int ROWS = 16 * SETS;
     constexpr int SO = D + 4;
-    constexpr int kFloats = part_floats(kDecodeRows, D);
+    constexpr int kFloats = part_floats(ROWS, D);
     typedef uint32_t words_t __attribute__((ext_vector_type(KW)));
-    __shared__ __attribute__((aligned(16))) float so_all[kDecodeWaves * kDecodeRows * SO];
-    float(*so)[kDecodeRows][SO] = reinterpret_cast<float(*)[kDecodeRows][SO]>(so_all);
-    __shared__ float sm[kDecodeWaves][kDecodeRows], sl[kDecodeWaves][kDecodeRows];
+    __shared__ __attribute__((aligned(16))) float so_all[kDecodeWaves * ROWS * SO];
+    float(*so)[ROWS][SO] = reinterpret_cast<float(*)[ROWS][SO]>(so_all);
+    __shared__ float sm[kDecodeWaves][ROWS], sl[kDecodeWaves][ROWS];
     __shared__ int s_flag;
 
     const KvPages& c = a.c;
@@ -85,13 +87,13 @@ __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 96 ? 4 : D <= 128 ? 3 : 2
     // sequence's first on the even XCDs and the seconds, often short or empty,
     // on the odd: 64 sequences of 8192 down to 2048 tokens 100 us, now 87.)
     const int kv_head = blockIdx.x;
-    const int row0 = (blockIdx.y & (row_tiles - 1)) * kDecodeRows;     // one row tile or two
+    const int row0 = (blockIdx.y & (row_tiles - 1)) * ROWS;     // one row tile or two
     const int b = blockIdx.y >> (row_tiles - 1);
     const int split = n_splits - 1 - blockIdx.z;
     const KvSeq sq = kv_seq_shared(c, b);
     const int all_rows = sq.n * a.ratio;
     if (row0 >= all_rows) return;
-    const int rows = min(kDecodeRows, all_rows - row0);
+    const int rows = min(ROWS, all_rows - row0);
     const Span span = row_span(a, sq, row0, rows);
     // the splits that hold a visible position; none at all: split 0 writes zeros
     const int first_split = span.begin < span.end ? sp.by_tokens.of(span.begin) : 0;
@@ -104,30 +106,39 @@ __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 96 ? 4 : D <= 128 ? 3 : 2
     // ---- queries, in LDS in operand order: word w of piece i holds the channels of
     // that word (in registers they are 16 to 32 a lane, and 256 channels leave room
     // for one wave per SIMD in place of two)
-    __shared__ half8_t qs[KC * KW][kWave];
-    const int row = row0 + col;
-    int lo = 0, hi = 0;
-    if (col < rows) {
-        const int token = a.by_ratio.of(row);
-        visible(a, sq, token, lo, hi);
-        const half_t* q = a.q + (static_cast<int64_t>(sq.row0) + token) * a.q_token +
-                          ((kv_head - token) * a.ratio + row) * a.q_head;
-        for (int i = wave; i < KC * KW; i += kDecodeWaves) {
-            const int first = (HALF ? 16 * quarter : 32 * (quarter + 4 * (i / KW))) + 8 * (i % KW);
-            half8_t v = {};
-            if (first < D) v = *reinterpret_cast<const half8_t*>(q + first);
-            qs[i][lane] = a.scale_log2 < 0.f ? -v : v;
+    __shared__ half8_t qs[SETS][KC * KW][kWave];
+    int lo[SETS], hi[SETS];
+#pragma unroll
+    for (int r = 0; r < SETS; ++r) {
+        const int row = row0 + 16 * r + col;
+        lo[r] = hi[r] = 0;
+        if (16 * r + col < rows) {
+            const int token = a.by_ratio.of(row);
+            visible(a, sq, token, lo[r], hi[r]);
+            const half_t* q = a.q + (static_cast<int64_t>(sq.row0) + token) * a.q_token +
+                              ((kv_head - token) * a.ratio + row) * a.q_head;
+            for (int i = wave; i < KC * KW; i += kDecodeWaves) {
+                const int first = (HALF ? 16 * quarter : 32 * (quarter + 4 * (i / KW))) + 8 * (i % KW);
+                half8_t v = {};
+                if (first < D) v = *reinterpret_cast<const half8_t*>(q + first);
+                qs[r][i][lane] = a.scale_log2 < 0.f ? -v : v;
+            }
+        } else {
+            for (int i = wave; i < KC * KW; i += kDecodeWaves) qs[r][i][lane] = half8_t{};
         }
-    } else {
-        for (int i = wave; i < KC * KW; i += kDecodeWaves) qs[i][lane] = half8_t{};
     }
     __syncthreads();
     const float qscale = fmaxf(fabsf(a.scale_log2), kTinyScale);
 
-    float m = kNone, sum = 0.f;
-    float4_t acc[DT];
+    float m[SETS], sum[SETS];
+    float4_t acc[SETS][DT];
 #pragma unroll
-    for (int t = 0; t < DT; ++t) acc[t] = float4_t{0.f, 0.f, 0.f, 0.f};
+    for (int r = 0; r < SETS; ++r) {
+        m[r] = kNone;
+        sum[r] = 0.f;
+#pragma unroll
+        for (int t = 0; t < DT; ++t) acc[r][t] = float4_t{0.f, 0.f, 0.f, 0.f};
+    }
 
     // The pages of a tile: one or two, by scalar loads. A page past the
     // sequence's end counts as not held, whatever its entry.
@@ -197,18 +208,23 @@ __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 96 ? 4 : D <= 128 ? 3 : 2
             const Pages then = pages_of(next);
 
             // ---- logits (unscaled) ----
-            float s[16];
+            float s[SETS][16];
 #pragma unroll
             for (int s4 = 0; s4 < 4; ++s4) {
-                float4_t x = {0.f, 0.f, 0.f, 0.f};
+                float4_t x[SETS] = {};
 #pragma unroll
                 for (int i = 0; i < KC; ++i)
 #pragma unroll
-                    for (int w = 0; w < KW; ++w)
-                        x = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv4_numbers8(kr[s4][i][w], ksc[s4][i]), qs[i * KW + w][lane], x,
-                                                                   0, 0, 0);
+                    for (int w = 0; w < KW; ++w) {
+                        const half8_t k = kv4_numbers8(kr[s4][i][w], ksc[s4][i]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[4 * s4 + e] = x[e];
+                        for (int r = 0; r < SETS; ++r)
+                            x[r] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, qs[r][i * KW + w][lane], x[r], 0, 0, 0);
+                    }
+#pragma unroll
+                for (int r = 0; r < SETS; ++r)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[r][4 * s4 + e] = x[r][e];
             }
             load_k(next, then);
             __builtin_amdgcn_sched_barrier(0);
@@ -219,8 +235,10 @@ __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 96 ? 4 : D <= 128 ? 3 : 2
                 const bool ok = NP == 2 && quarter >= 2 ? now.held[NP - 1] : now.held[0];
                 const int j0 = tb + 16 * quarter;
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    s[i] = ok && j0 + i >= lo && j0 + i < hi ? s[i] : -__builtin_huge_valf();
+                for (int r = 0; r < SETS; ++r)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        s[r][i] = ok && j0 + i >= lo[r] && j0 + i < hi[r] ? s[r][i] : -__builtin_huge_valf();
                 const int n = ok ? sq.len - j0 : 0;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -237,41 +255,47 @@ __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 96 ? 4 : D <= 128 ? 3 : 2
             }
 
             // ---- softmax ----
-            float top = s[0];
+            half8_t pf[SETS][2], pl[SETS][2];
 #pragma unroll
-            for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
-            top = across_quarters_max(top) * qscale;
-            if (__any(top > m + kSlack)) {
-                const float mn = fmaxf(m, top);
-                const float carry = __builtin_amdgcn_exp2f(m - mn);
-                sum *= carry;
+            for (int r = 0; r < SETS; ++r) {
+                float top = s[r][0];
 #pragma unroll
-                for (int t = 0; t < DT; ++t) acc[t] *= carry;
-                m = mn;
-            }
-            const float shift = kUnit - m;
-            half8_t pf[2], pl[2];
+                for (int i = 1; i < 16; ++i) top = fmaxf(top, s[r][i]);
+                top = across_quarters_max(top) * qscale;
+                if (__any(top > m[r] + kSlack)) {
+                    const float mn = fmaxf(m[r], top);
+                    const float carry = __builtin_amdgcn_exp2f(m[r] - mn);
+                    sum[r] *= carry;
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-                const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], qscale, shift));
-                const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i + 1], qscale, shift));
-                sum += p0;
-                sum += p1;
-                half2_t ph, pr;
-                two_parts(p0, p1, ph, pr);
+                    for (int t = 0; t < DT; ++t) acc[r][t] *= carry;
+                    m[r] = mn;
+                }
+                const float shift = kUnit - m[r];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    pf[i >> 3][(i & 7) + j] = ph[j];
-                    pl[i >> 3][(i & 7) + j] = pr[j];
+                for (int i = 0; i < 16; i += 2) {
+                    const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][i], qscale, shift));
+                    const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][i + 1], qscale, shift));
+                    sum[r] += p0;
+                    sum[r] += p1;
+                    half2_t ph, pr;
+                    two_parts(p0, p1, ph, pr);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        pf[r][i >> 3][(i & 7) + j] = ph[j];
+                        pl[r][i >> 3][(i & 7) + j] = pr[j];
+                    }
                 }
             }
 #pragma unroll
             for (int t = 0; t < DT; ++t) {
                 const half8_t v0 = kv4_numbers8(vr[t][0], vs[0], vlo[0]), v1 = kv4_numbers8(vr[t][1], vs[1], vlo[1]);
-                acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pf[0], acc[t], 0, 0, 0);
-                acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pf[1], acc[t], 0, 0, 0);
-                acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pl[0], acc[t], 0, 0, 0);
-                acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pl[1], acc[t], 0, 0, 0);
+#pragma unroll
+                for (int r = 0; r < SETS; ++r) {
+                    acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pf[r][0], acc[r][t], 0, 0, 0);
+                    acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pf[r][1], acc[r][t], 0, 0, 0);
+                    acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pl[r][0], acc[r][t], 0, 0, 0);
+                    acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pl[r][1], acc[r][t], 0, 0, 0);
+                }
             }
             load_v(next, then);
             __builtin_amdgcn_sched_barrier(0);
@@ -280,33 +304,37 @@ __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 96 ? 4 : D <= 128 ? 3 : 2
     }
 
     // ---- the waves' results; sums and outputs carry 2^kUnit ----
-    sum += __shfl_xor(sum, 16);
-    sum += __shfl_xor(sum, 32);
 #pragma unroll
-    for (int t = 0; t < DT; ++t) *reinterpret_cast<float4_t*>(&so[wave][col][16 * t + 4 * quarter]) = acc[t];
-    if (quarter == 0) {
-        sm[wave][col] = m - kUnit;
-        sl[wave][col] = sum;
+    for (int r = 0; r < SETS; ++r) {
+        sum[r] += __shfl_xor(sum[r], 16);
+        sum[r] += __shfl_xor(sum[r], 32);
+#pragma unroll
+        for (int t = 0; t < DT; ++t)
+            *reinterpret_cast<float4_t*>(&so[wave][16 * r + col][16 * t + 4 * quarter]) = acc[r][t];
+        if (quarter == 0) {
+            sm[wave][16 * r + col] = m[r] - kUnit;
+            sl[wave][16 * r + col] = sum[r];
+        }
     }
     __syncthreads();
     float mm = kNone, ll = 0.f;
-    const int r16 = tid % kDecodeRows;
+    const int mine = tid % ROWS;
     float w[kDecodeWaves];
 #pragma unroll
-    for (int v = 0; v < kDecodeWaves; ++v) mm = fmaxf(mm, sm[v][r16]);
+    for (int v = 0; v < kDecodeWaves; ++v) mm = fmaxf(mm, sm[v][mine]);
 #pragma unroll
     for (int v = 0; v < kDecodeWaves; ++v) {
-        w[v] = __builtin_amdgcn_exp2f(sm[v][r16] - mm);
-        ll += w[v] * sl[v][r16];
+        w[v] = __builtin_amdgcn_exp2f(sm[v][mine] - mm);
+        ll += w[v] * sl[v][mine];
     }
-    for (int d = tid / kDecodeRows * 4; d < D; d += NT / kDecodeRows * 4) {
+    for (int d = tid / ROWS * 4; d < D; d += NT / ROWS * 4) {
         float4_t o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int v = 0; v < kDecodeWaves; ++v) o += *reinterpret_cast<const float4_t*>(&so[v][r16][d]) * w[v];
-        *reinterpret_cast<float4_t*>(&so[0][r16][d]) = o;
+        for (int v = 0; v < kDecodeWaves; ++v) o += *reinterpret_cast<const float4_t*>(&so[v][mine][d]) * w[v];
+        *reinterpret_cast<float4_t*>(&so[0][mine][d]) = o;
     }
     __syncthreads();
-    if (tid < kDecodeRows) {
+    if (tid < ROWS) {
         sm[0][tid] = mm;
         sl[0][tid] = ll;
     }
@@ -315,8 +343,8 @@ __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 96 ? 4 : D <= 128 ? 3 : 2
     const Rows rw{kv_head, row0, rows, last_split - first_split + 1, split - first_split,
                   sp.partials + tile_id * n_splits * kFloats, static_cast<int64_t>(n_splits) * kFloats * 4,
                   sp.counters + tile_id};
-    finish_rows<D, kDecodeRows, NT, true>(a, sq, rw, [&](int p) { return (first_split + p) * kFloats; }, so_all, SO, &sm[0][0],
-                                    &sl[0][0], so_all, &s_flag);
+    finish_rows<D, ROWS, NT, true>(a, sq, rw, [&](int p) { return (first_split + p) * kFloats; }, so_all, SO, &sm[0][0],
+                                   &sl[0][0], so_all, &s_flag);
 }
 
 // ---------------------------------------------------------------- many rows
@@ -620,12 +648,16 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv4_pr
 
 template <int D, int NP>
 void launch_np(const KvAttentionArgs& a, const Plan& p, const Split& sp, hipStream_t stream) {
-    if (p.decode)
-        hipLaunchKernelGGL((kv4_decode_kernel<D, NP>),
+    const auto decode = [&](auto sets) {
+        hipLaunchKernelGGL((kv4_decode_kernel<D, NP, decltype(sets)::value>),
                            dim3(static_cast<unsigned>(a.c.heads), static_cast<unsigned>(p.row_tiles * a.n_seqs),
                                 static_cast<unsigned>(p.splits)),
                            dim3(kDecodeWaves * kWave), 0, stream, a, sp, p.splits, static_cast<int>(p.row_tiles));
-    else
+    };
+    if (p.rows == kDecodeRows) decode(std::integral_constant<int, 1>{});
+    else if (p.decode) {
+        if constexpr (D <= kWideDim) decode(std::integral_constant<int, 2>{});
+    } else
         hipLaunchKernelGGL((kv4_prefill_kernel<D, NP>),
                            dim3(static_cast<unsigned>(p.row_tiles * p.splits * a.c.heads), 1,
                                 static_cast<unsigned>(a.n_seqs)),
@@ -640,7 +672,7 @@ void launch_d(const KvAttentionArgs& a, const Plan& p, const Split& sp, hipStrea
 }  // namespace
 
 awq_status launch_kv4_attention(const KvAttentionArgs& a, void* workspace, hipStream_t stream) {
-    const Plan p = plan_for(a.n_seqs, a.c.heads, a.ratio, a.max_tokens, a.c.max_len, workspace != nullptr);
+    const Plan p = plan_for(a.format, a.head_dim, a.n_seqs, a.c.heads, a.ratio, a.max_tokens, a.c.max_len, workspace != nullptr);
     if (!launchable(p, a.c.heads)) return AWQ_ERR_SHAPE;
     const Split sp = split_of(p, workspace);
     switch (a.head_dim) {

@@ -290,6 +290,7 @@ constexpr int kDecodeWaves = 4;
 constexpr int kTile = 64;
 constexpr int kPrefillWaves = 4;
 constexpr int kPrefillRows = 32 * kPrefillWaves;
+constexpr int kWideDim = 128;               // over the 4-bit cache: see plan_for
 
 // Counters at the workspace's start, whatever the call: a split launch has at
 // most this many row tiles.
@@ -298,6 +299,7 @@ constexpr size_t kCounterBytes = kCounters * sizeof(int);
 
 struct Plan {
     bool decode;
+    int rows;               // of a block
     int64_t row_tiles;      // per sequence and kv head
     int splits;
     int tokens;             // positions per split
@@ -314,14 +316,28 @@ struct Plan {
 // evenly to 512 blocks instead, which a ragged batch would ask for, was
 // slower on every shape (64 x 8192 to 2048: 145 against 134), as a block then
 // pays for two or more pieces.
-inline Plan plan_for(int n_seqs, int kv_heads, int ratio, int64_t max_tokens, int64_t max_len, bool have_workspace) {
+// Over the 4-bit cache, 17 to 32 rows are one block's, which unpacks the keys and
+// values once for both sixteens, where the sequences' kv heads are two to a CU, or
+// enough for few parts to join and long. Measured, 8 query heads a kv head, 8 kv
+// heads of 128, 4 tokens (us, in brackets as two blocks of 16 rows): 64 x 4096 87
+// (109), 64 x 64 9.0 (11.0), 8 x 32768 92 (120), 8 x 8192 29.5 (33.5), 2 x 131072
+// 93 (115); but 2 x 32768 37.7 (35.5), 1 x 131072 63 (64), one kv head 1 x 262144 59
+// (41), 16 x 2000 21.7 (21.1), 1 x 1000 11.2 (8.8). With 192 channels and more it
+// leaves one wave per SIMD: 64 x 4096 152 (171), but 16 x 4096 54 (48).
+inline Plan plan_for(int format, int head_dim, int n_seqs, int kv_heads, int ratio, int64_t max_tokens, int64_t max_len,
+                     bool have_workspace) {
     Plan p;
     const int64_t rows = max_tokens * ratio;
     p.decode = rows <= 2 * kDecodeRows;
-    const int per_block = p.decode ? kDecodeRows : kPrefillRows;
+    const int64_t cu = cu_count();
+    const int64_t pairs = static_cast<int64_t>(n_seqs) * kv_heads;
+    const bool wide = format == AWQ_KV_INT4 && rows > kDecodeRows && head_dim <= kWideDim &&
+                      (pairs >= 2 * cu || (pairs >= 32 && pairs * max_len >= int64_t{1} << 19) ||
+                       (pairs >= 16 && pairs * max_len >= int64_t{1} << 20));
+    const int per_block = p.rows = !p.decode ? kPrefillRows : wide ? 2 * kDecodeRows : kDecodeRows;
     p.row_tiles = ceil_div(rows, per_block);
     const int64_t tiles = p.row_tiles * n_seqs * kv_heads;
-    const int64_t most = max_splits(per_block), cu = cu_count();
+    const int64_t most = max_splits(per_block);
     int64_t splits = 1, unit = p.decode ? 1024 : kTile * 8;
     if (have_workspace && tiles <= kCounters) {
         splits = std::min({ceil_div(max_len, unit), 2 * cu / tiles, most});
@@ -339,7 +355,7 @@ inline Plan plan_for(int n_seqs, int kv_heads, int ratio, int64_t max_tokens, in
 
 inline size_t plan_bytes(const Plan& p, int n_seqs, int kv_heads, int head_dim) {
     const size_t tiles = static_cast<size_t>(p.row_tiles) * n_seqs * kv_heads;
-    const size_t floats = part_floats(p.decode ? kDecodeRows : kPrefillRows, head_dim);
+    const size_t floats = part_floats(p.rows, head_dim);
     return kCounterBytes + (p.splits > 1 ? tiles * p.splits * floats * sizeof(float) : 0);
 }
 

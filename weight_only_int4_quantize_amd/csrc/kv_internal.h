@@ -235,7 +235,7 @@ struct KvAttentionArgs {
     int window;                            // 0: none
     KvDivisor by_ratio;
 };
-size_t kv_attention_workspace_bytes(int n_seqs, int kv_heads, int ratio, int head_dim, int64_t max_tokens,
+size_t kv_attention_workspace_bytes(int format, int n_seqs, int kv_heads, int ratio, int head_dim, int64_t max_tokens,
                                     int64_t max_len);
 awq_status launch_kv_attention(const KvAttentionArgs& a, void* workspace, hipStream_t stream);
 awq_status launch_kv4_attention(const KvAttentionArgs& a, void* workspace, hipStream_t stream);
