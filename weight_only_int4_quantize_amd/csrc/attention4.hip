@@ -27,8 +27,8 @@ constexpr float kSlack = 3.0f;      // what a logit may pass the maximum by
 constexpr float kTinyScale = 1.0e-30f;  // |scale log2 e| below it counts as it (a masked logit times 0 would be NaN)
 
 // s and lo of the first n tokens, or of those from n on, as they are, of the
-// others 0 (what lies behind a sequence's end or before its window may be
-// anything, NaN among it)
+// others 0 (what none of the rows sees may be anything, NaN among it, and 0 times
+// that is NaN)
 __device__ inline half8_t first_n(half8_t v, int n) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = j < n ? v[j] : static_cast<half_t>(0.f);
@@ -140,8 +140,8 @@ kv4_decode_kernel(KvAttentionArgs a, Split sp, int n_splits, int row_tiles) {
         for (int t = 0; t < DT; ++t) acc[r][t] = float4_t{0.f, 0.f, 0.f, 0.f};
     }
 
-    // The pages of a tile: one or two, by scalar loads. A page past the
-    // sequence's end counts as not held, whatever its entry.
+    // The pages of a tile: one or two, by scalar loads. A page past what the rows
+    // see counts as not held, whatever its entry.
     struct Pages {
         int64_t block[NP];
         bool held[NP];
@@ -151,7 +151,7 @@ kv4_decode_kernel(KvAttentionArgs a, Split sp, int n_splits, int row_tiles) {
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const int p = (tile * kTile >> c.log2_page) + i;
-            const int id = (p << c.log2_page) < sq.len ? kv_page_shared(c, b, p) : -1;
+            const int id = (p << c.log2_page) < span.end ? kv_page_shared(c, b, p) : -1;
             g.held[i] = id >= 0;
             g.block[i] = static_cast<int64_t>(max(id, 0)) * c.heads + kv_head;
         }
@@ -239,7 +239,7 @@ kv4_decode_kernel(KvAttentionArgs a, Split sp, int n_splits, int row_tiles) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         s[r][i] = ok && j0 + i >= lo[r] && j0 + i < hi[r] ? s[r][i] : -__builtin_huge_valf();
-                const int n = ok ? sq.len - j0 : 0;
+                const int n = ok ? span.end - j0 : 0;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     vs[j] = first_n(vs[j], n - 8 * j);
@@ -456,8 +456,8 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv4_pr
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const int p = (tb >> c.log2_page) + i;
-            // a page past the sequence's end counts as not held, whatever its entry
-            const int id = (p << c.log2_page) < sq.len ? kv_page_shared(c, b, p) : -1;
+            // a page past what the rows see counts as not held, whatever its entry
+            const int id = (p << c.log2_page) < span.end ? kv_page_shared(c, b, p) : -1;
             pg.held[i] = id >= 0;
             block[i] = static_cast<int64_t>(max(id, 0)) * c.heads + kv_head;
         }
@@ -497,7 +497,7 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv4_pr
 #pragma unroll
             for (int w = 0; w < 4; ++w) ks[(4 * ch + w) * kTile + t] = kv4_numbers8(kr[i][w], ksc[i]);
         }
-        const int n = (pg.held[NP == 2 ? wave >> 1 : 0] ? sq.len : 0) - (tb + 16 * wave);
+        const int n = (pg.held[NP == 2 ? wave >> 1 : 0] ? span.end : 0) - (tb + 16 * wave);
         if (n < 16) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
