@@ -726,9 +726,10 @@ awq_status awq_kv_read(const awq_kv_cache* cache, const awq_kv_seqs* seqs,
  * the weights enter the second product as two fp16 numbers (a weight cut to
  * fp16 and what that left), within 2^-20 of themselves. A query with a NaN
  * that sees a position gets NaN (o and lse); no other row is touched by it,
- * or by an infinity. With AWQ_KV_INT4 the products' numbers are the cached
- * ones, those awq_kv_read gives, and a position that no query of its sequence
- * sees may hold anything.
+ * or by an infinity. A position that no query of its sequence sees may hold
+ * anything, and so may the scales of a page of such positions. With
+ * AWQ_KV_INT4 the products' numbers are the cached ones, those awq_kv_read
+ * gives.
  *
  *   q_f16        device, fp16 [n_tokens, n_heads, head_dim], channels
  *                contiguous, 16-byte aligned, strides in halves, multiples

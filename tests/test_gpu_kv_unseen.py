@@ -1,7 +1,7 @@
 """Attention over positions that no query of the call sees and that nobody has
-written: behind the rows that a token tensor holds where cu_tokens names more.
-What such a place holds (NaN codes, steps and scales that are NaN or infinite)
-changes no row.
+written: behind the rows that a token tensor holds where cu_tokens names more,
+and before every query's window. What such a place holds (NaN codes, steps and
+scales that are NaN or infinite) changes no row.
 
 Attention's bounds are test_gpu_kv's and test_gpu_kv4's.
 """
@@ -20,7 +20,7 @@ import test_gpu_kv as kv8  # noqa: E402
 import test_gpu_kv4 as kv4  # noqa: E402
 from test_gpu_parity import dev, host, say  # noqa: E402
 
-FORMATS = ["int4"]
+FORMATS = ["int4", "e4m3", "int8"]
 GARBAGE = [float("nan"), float("inf")]
 
 
@@ -102,3 +102,29 @@ def test_blocks_of_thirty_two_rows(page, garbage):
     here = np.minimum(new, [6, 6, 1, 6, 2, 0, 0, 0])
     m.append(np.array(held) + here)
     check(m, "int4", new, here, 6, int(here.sum()), 4, max_len=bound)
+
+
+@pytest.mark.parametrize("garbage", GARBAGE)
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("page", [32, 64, 256])
+@pytest.mark.parametrize("new", [1, 9, 90])
+def test_nothing_before_the_window(new, page, fmt, garbage):
+    """A sequence whose first tokens were never written, its first written one
+    the first that any window reaches."""
+    W = 21
+    say("unseen before the window", fmt, garbage, page, new)
+    for first in (0, 32, 45, 63):
+        n = W + new - 1
+        m = model(fmt, [85, page, new], 1, 2, 64, page, first + n, garbage)
+        if fmt != "int4":
+            # a page written from its middle keeps what its scale was
+            m.cache.k_scales.fill_(0.0)
+            m.cache.v_scales.fill_(0.0)
+            for p in range(first // page):
+                m.cache.k_scales[m.table[0, p]] = garbage
+                m.cache.v_scales[m.table[0, p]] = garbage
+        m.len[:] = first
+        m.append([n])
+        q = m.rng.standard_normal((new, 4, 64)).astype(np.float16)
+        for split in (True, False):
+            m.assert_attention(m.attend(q, [new], window=W, split=split), n)

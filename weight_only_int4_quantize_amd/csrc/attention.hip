@@ -38,6 +38,24 @@ constexpr float kPrefillUnit = 12.0f;   // the same in prefill
 constexpr float kSlack = 3.0f;          // what t and t + e may pass their maxima by there
 constexpr float kTinyScale = 1.0e-20f;  // scales at or below it count as it
 
+// ones in bytes from .. to - 1 of 16
+__device__ inline kv_u32x4 bytes_between(int from, int to) {
+    kv_u32x4 r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const auto below = [&](int n) {     // bytes 0 .. n - 1 of the word
+            const int k = min(max(n - 4 * j, 0), 4);
+            return k == 4 ? 0xFFFFFFFFu : (1u << (8 * k)) - 1u;
+        };
+        r[j] = below(to) & ~below(from);
+    }
+    return r;
+}
+// whether any of the rows sees a position of page p
+__device__ inline bool seen(const Span& s, int p, int log2_page) {
+    return (p << log2_page) < s.end && (static_cast<int64_t>(p) + 1) << log2_page > s.begin;
+}
+
 // ---------------------------------------------------------------- few rows
 
 // Decode: up to 16 query rows per block. The four waves walk the split's
@@ -122,8 +140,8 @@ __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 64 ? 4 : D <= 96 ? 3 : D 
 #pragma unroll
     for (int t = 0; t < DT; ++t) acc[t] = float4_t{0.f, 0.f, 0.f, 0.f};
 
-    // The pages of a tile: one or two, by scalar loads. A page past the
-    // sequence's end counts as not held, whatever its entry.
+    // The pages of a tile: one or two, by scalar loads. A page that none of the
+    // rows sees counts as not held, whatever its entry: its scales may be anything.
     struct Pages {
         int64_t block[NP];
         bool held[NP];
@@ -133,7 +151,7 @@ __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 64 ? 4 : D <= 96 ? 3 : D 
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const int p = (tile * kTile >> c.log2_page) + i;
-            const int id = (p << c.log2_page) < sq.len ? kv_page_shared(c, b, p) : -1;
+            const int id = seen(span, p, c.log2_page) ? kv_page_shared(c, b, p) : -1;
             g.held[i] = id >= 0;
             g.block[i] = static_cast<int64_t>(max(id, 0)) * c.heads + kv_head;
         }
@@ -208,14 +226,8 @@ __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 64 ? 4 : D <= 96 ? 3 : D 
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     s[i] = ok && j0 + i >= lo && j0 + i < hi ? s[i] : -__builtin_huge_valf();
-                // bytes past the sequence's end may be anything, fp8 NaN among them
-                const int n = ok ? min(max(sq.len - j0, 0), 16) : 0;
-                kv_u32x4 keep;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int k = min(max(n - 4 * j, 0), 4);
-                    keep[j] = k == 4 ? 0xFFFFFFFFu : (1u << (8 * k)) - 1u;
-                }
+                // bytes that none of the rows sees may be anything, fp8 NaN among them
+                const kv_u32x4 keep = ok ? bytes_between(span.begin - j0, span.end - j0) : kv_u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
                 for (int t = 0; t < DT; ++t) vr[t] &= keep;
             }
@@ -415,8 +427,8 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv_pre
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const int p = (tb >> c.log2_page) + i;
-            // a page past the sequence's end counts as not held, whatever its entry
-            const int id = (p << c.log2_page) < sq.len ? kv_page_shared(c, b, p) : -1;
+            // a page that none of the rows sees counts as not held, whatever its entry
+            const int id = seen(span, p, c.log2_page) ? kv_page_shared(c, b, p) : -1;
             pg.held[i] = id >= 0;
             block[i] = static_cast<int64_t>(max(id, 0)) * c.heads + kv_head;
             pg.ks[i] = pg.held[i] ? kv_shared_load(c.k_scales + block[i]) : 0.f;
@@ -441,7 +453,7 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv_pre
     };
     auto stage = [&](int tile, const Pages& pg, half8_t* ks, half8_t* vs) {
         const int tb = tile * kTile;
-        bool whole = tb + kTile <= sq.len;
+        bool whole = tb >= span.begin && tb + kTile <= span.end;
 #pragma unroll
         for (int i = 0; i < NP; ++i) whole = whole && pg.held[i];
 #pragma unroll
@@ -453,14 +465,10 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv_pre
             ks[(2 * ch + 1) * kTile + t] = kv_unpack8<FORMAT>(kr[i][2], kr[i][3]);
             const int d = e % D, tc = e / D;
             if (!whole) {
-                // bytes past the sequence's end may be anything, fp8 NaN among them
-                const bool ok = NP == 2 && tc >= 2 ? pg.held[NP - 1] : pg.held[0];
-                const int n = ok ? min(max(sq.len - (tb + 16 * tc), 0), 16) : 0;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int k = min(max(n - 4 * j, 0), 4);
-                    vr[i][j] &= k == 4 ? 0xFFFFFFFFu : (1u << (8 * k)) - 1u;
-                }
+                // bytes that none of the rows sees may be anything, fp8 NaN among them
+                const int j0 = tb + 16 * tc;
+                vr[i] &= (NP == 2 && tc >= 2 ? pg.held[NP - 1] : pg.held[0])
+                             ? bytes_between(span.begin - j0, span.end - j0) : kv_u32x4{0u, 0u, 0u, 0u};
             }
             vs[(2 * tc) * D + d] = kv_unpack8<FORMAT>(vr[i][0], vr[i][1]);
             vs[(2 * tc + 1) * D + d] = kv_unpack8<FORMAT>(vr[i][2], vr[i][3]);
