@@ -649,8 +649,8 @@ typedef struct {
  * narrow the split either.
  * Whatever the arrays hold, no access leaves the tensors: a kv_len past
  * max_len counts as max_len, and new tokens past max_tokens (from a
- * sequence's first new one on, rounded up to whole pages, or to 32 tokens with
- * AWQ_KV_INT4) are not processed.
+ * sequence's first new one on; in awq_kv_write and awq_kv_read rounded up to
+ * whole pages, or to 32 tokens with AWQ_KV_INT4) are not processed.
  */
 typedef struct {
     const int32_t* block_table;

@@ -1,7 +1,8 @@
 """Attention over positions that no query of the call sees and that nobody has
 written: behind the rows that a token tensor holds where cu_tokens names more,
-and before every query's window. What such a place holds (NaN codes, steps and
-scales that are NaN or infinite) changes no row.
+behind those that max_tokens leaves over, and before every query's window. What
+such a place holds (NaN codes, steps and scales that are NaN or infinite) changes
+no row.
 
 Attention's bounds are test_gpu_kv's and test_gpu_kv4's.
 """
@@ -91,6 +92,20 @@ def test_rows_that_are_not_there(dim, page, heads, ratio, held, new, fmt, garbag
 
 
 @pytest.mark.parametrize("garbage", GARBAGE)
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim,page,heads,ratio,held,new", SHAPES)
+def test_a_bound_below_the_tokens(dim, page, heads, ratio, held, new, fmt, garbage):
+    """New tokens past max_tokens: not written, not processed, in the way of nobody."""
+    for bound in {1, max(1, max(new) // 3), max(1, max(new) - 1)}:
+        say("unseen tokens", fmt, garbage, dim, page, new, bound)
+        m = model(fmt, [82, dim, bound], 3, heads, dim, page, max(h + n for h, n in zip(held, new)), garbage)
+        here = np.minimum(new, bound)
+        m.append(np.array(held) + here)
+        check(m, fmt, new, here, bound, sum(new), ratio)
+        check(m, fmt, new, here, bound, sum(new), ratio, window=9, split=False)
+
+
+@pytest.mark.parametrize("garbage", GARBAGE)
 @pytest.mark.parametrize("page", [32, 64])
 def test_blocks_of_thirty_two_rows(page, garbage):
     """The same over the 4-bit cache where 17 to 32 rows are one block's."""
@@ -102,6 +117,10 @@ def test_blocks_of_thirty_two_rows(page, garbage):
     here = np.minimum(new, [6, 6, 1, 6, 2, 0, 0, 0])
     m.append(np.array(held) + here)
     check(m, "int4", new, here, 6, int(here.sum()), 4, max_len=bound)
+    m = model("int4", [84, page], 8, 4, 128, page, max(lens), garbage)
+    here = np.minimum(new, 5)
+    m.append(np.array(held) + here)
+    check(m, "int4", new, here, 5, sum(new), 4, max_len=bound)
 
 
 @pytest.mark.parametrize("garbage", GARBAGE)

@@ -103,7 +103,7 @@ __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 64 ? 4 : D <= 96 ? 3 : D 
     const int kv_head = blockIdx.y % c.heads;
     const int row0 = blockIdx.y / c.heads * kDecodeRows;
     const KvSeq sq = kv_seq_shared(c, b);
-    const int all_rows = sq.n * a.ratio;
+    const int all_rows = rows_of(a, sq);
     if (row0 >= all_rows) return;
     const int rows = min(kDecodeRows, all_rows - row0);
     const Span span = row_span(a, sq, row0, rows);
@@ -380,7 +380,7 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv_pre
     const int row_tile = row_tiles - 1 - rest / n_splits;
     const int row0 = row_tile * kPrefillRows;
     const KvSeq sq = kv_seq_shared(c, b);
-    const int all_rows = sq.n * a.ratio;
+    const int all_rows = rows_of(a, sq);
     if (row0 >= all_rows) return;
     const int rows = min(kPrefillRows, all_rows - row0);
     const Span span = row_span(a, sq, row0, rows);

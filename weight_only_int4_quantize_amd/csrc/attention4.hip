@@ -91,7 +91,7 @@ kv4_decode_kernel(KvAttentionArgs a, Split sp, int n_splits, int row_tiles) {
     const int b = blockIdx.y >> (row_tiles - 1);
     const int split = n_splits - 1 - blockIdx.z;
     const KvSeq sq = kv_seq_shared(c, b);
-    const int all_rows = sq.n * a.ratio;
+    const int all_rows = rows_of(a, sq);
     if (row0 >= all_rows) return;
     const int rows = min(ROWS, all_rows - row0);
     const Span span = row_span(a, sq, row0, rows);
@@ -408,7 +408,7 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv4_pr
     const int row_tile = row_tiles - 1 - rest / n_splits;
     const int row0 = row_tile * kPrefillRows;
     const KvSeq sq = kv_seq_shared(c, b);
-    const int all_rows = sq.n * a.ratio;
+    const int all_rows = rows_of(a, sq);
     if (row0 >= all_rows) return;
     const int rows = min(kPrefillRows, all_rows - row0);
     const Span span = row_span(a, sq, row0, rows);

@@ -71,6 +71,12 @@ __device__ inline void two_parts(float w0, float w1, half2_t& hi, half2_t& lo) {
     lo = __builtin_bit_cast(half2_t, __builtin_amdgcn_cvt_pkrtz(r0, r1));
 }
 
+// Query rows of a kv head that the call works on. New tokens past max_tokens are
+// left out, also where a block has room for them: they would widen what the
+// block's rows see to positions that may hold anything.
+__device__ inline int rows_of(const KvAttentionArgs& a, const KvSeq& sq) {
+    return static_cast<int>(min(static_cast<int64_t>(sq.n), a.max_tokens)) * a.ratio;
+}
 // The positions rows [row0, row0 + rows) of a kv head see.
 struct Span {
     int begin, end;             // any of them
