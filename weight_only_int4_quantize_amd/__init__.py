@@ -24,6 +24,7 @@ Entry points (same names as the C ABI in include/awq.h):
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import re
 import warnings
@@ -184,6 +185,18 @@ def _check(fn: str, status: int) -> None:
     if status != AWQ_OK:
         msg = load().awq_status_string(status).decode()
         raise AwqError(fn, status, msg)
+
+
+def _int32(name: str, v) -> int:
+    """v, an integer of any kind, as one that a C int holds: ctypes would cut it
+    off, and the call would fill more than the buffer made for v."""
+    try:
+        v = operator.index(v)
+    except TypeError:
+        raise TypeError(f"{name} must be an int") from None
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError(f"{name} must fit 32 bits, got {v}")
+    return v
 
 
 def _torch():
@@ -1144,7 +1157,8 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "non
         raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
     low = 1.0 if low is None else float(low)
     high = (32.0 if scaling == "yarn" else 4.0) if high is None else float(high)
-    n = rotary_dim // 2 if isinstance(rotary_dim, int) and 2 <= rotary_dim <= 4096 else 1
+    rotary_dim = _int32("rotary_dim", rotary_dim)
+    n = rotary_dim // 2 if 2 <= rotary_dim <= 4096 else 1
     freqs, amplitude = (ctypes.c_double * n)(), ctypes.c_double()
     _check("awq_rope_frequencies", load().awq_rope_frequencies(rotary_dim, float(base), ROPE_SCALINGS[scaling],
                                                                float(factor), float(trained_len), low, high, freqs,
