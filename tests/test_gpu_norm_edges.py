@@ -1,0 +1,36 @@
+"""The norm (awq_rmsnorm) at the edges of its arguments.
+
+The bounds are test_gpu_norm's.
+"""
+
+import numpy as np
+import pytest
+
+from oracle import layer_oracle as lo
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import weight_only_int4_quantize_amd as awq  # noqa: E402
+
+from test_gpu_norm import check_8bit, inputs  # noqa: E402
+from test_gpu_parity import dev, host, say  # noqa: E402
+
+
+def test_group_sizes_of_any_integer_kind():
+    """Numpy's integers as Python's own; past a C int, where ctypes would cut
+    them to an ordinary group and the call fill more scales than there are, no
+    call."""
+    x, _, w = inputs([21], 2, 64, False)
+    xd, wd = dev(x), dev(w)
+    _, y = lo.rmsnorm(x, w)
+    for kind in (int, np.int32, np.int64):
+        codes, scales = awq.awq_rmsnorm(xd, wd, fmt="int8", group_size=kind(32))
+        check_8bit(host(codes), host(scales), y, "int8", 32)
+    for bad in (-2 ** 32 + 32, 2 ** 32 + 32, 2 ** 31):
+        say("rmsnorm group", bad)
+        with pytest.raises(ValueError, match="group_size"):
+            awq.awq_rmsnorm(xd, wd, fmt="int8", group_size=bad)
+    for bad in (32.0, "32", None):
+        with pytest.raises(TypeError, match="group_size"):
+            awq.awq_rmsnorm(xd, wd, fmt="int8", group_size=bad)

@@ -1087,12 +1087,14 @@ def awq_rmsnorm(x, weight=None, eps: float = 1e-5, residual=None, residual_out=N
         raise ValueError("fmt must be None, 'int8' or 'e4m3'")
     torch = _torch()
     index = -1
+    if type(group_size) is not int:
+        group_size = _int32("group_size", group_size)
     if out is None or (code and scales is None):
         _need_rows("x", x, torch.float16)
         if out is None:
             out = torch.empty(x.shape, dtype=_norm_dtype(fmt), device=x.device)
         if code and scales is None:
-            n = x.shape[1] // group_size if isinstance(group_size, int) and group_size > 0 else 1
+            n = x.shape[1] // group_size if group_size > 0 else 1
             scales = torch.empty((x.shape[0], n), dtype=torch.float32, device=x.device)
     ext = (_fast or _fast_calls())[0]
     if ext is not None:
@@ -1111,8 +1113,7 @@ def awq_rmsnorm(x, weight=None, eps: float = 1e-5, residual=None, residual_out=N
     half = torch.float16
     _need_rows("x", x, half)
     index, (T, K) = x.get_device(), x.shape
-    if not isinstance(group_size, int):
-        raise TypeError("group_size must be an int")
+    group_size = _int32("group_size", group_size)
     if weight is not None:
         _need_on("weight", weight, half, index)
         if tuple(weight.shape) != (K,):
