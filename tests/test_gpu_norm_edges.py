@@ -13,7 +13,7 @@ pytestmark = pytest.mark.gpu
 
 import weight_only_int4_quantize_amd as awq  # noqa: E402
 
-from test_gpu_norm import check_8bit, inputs  # noqa: E402
+from test_gpu_norm import check_8bit, check_f16, inputs, values  # noqa: E402
 from test_gpu_parity import dev, host, say  # noqa: E402
 
 
@@ -34,3 +34,22 @@ def test_group_sizes_of_any_integer_kind():
     for bad in (32.0, "32", None):
         with pytest.raises(TypeError, match="group_size"):
             awq.awq_rmsnorm(xd, wd, fmt="int8", group_size=bad)
+
+
+@pytest.mark.parametrize("fmt", [None, "int8", "e4m3"])
+@pytest.mark.parametrize("eps", [1e-45, 1e-40, 1.1e-38, 1.2e-38, 1e-30])
+def test_the_smallest_eps(eps, fmt):
+    """Rows of zeros are zeros with any eps > 0, subnormal numbers among them; the
+    smallest fp16 numbers are not the eps' business."""
+    x, _, w = inputs([22], 4, 96, False)
+    x[0] = 0
+    x[1] = np.float16(6e-8)
+    x[2] = 0
+    x[2, 5] = np.float16(6e-8)
+    _, y = lo.rmsnorm(x, w, eps)
+    assert np.isfinite(y).all() and not y[0].any()
+    got = awq.awq_rmsnorm(dev(x), dev(w), eps, fmt=fmt)
+    if fmt is None:
+        check_f16(host(got), y, 96)
+    else:
+        check_8bit(values(got[0]), host(got[1]), y, fmt, 0)

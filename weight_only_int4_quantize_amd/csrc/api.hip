@@ -2,6 +2,7 @@
 // host, then kernels enqueued on the caller's stream.
 #include <algorithm>
 #include <cmath>
+#include <limits>
 #include <mutex>
 #include <vector>
 
@@ -1058,7 +1059,10 @@ awq_status awq_rmsnorm(const void* x_f16, int64_t x_stride, const void* residual
     a.rows = rows;
     a.width = width;
     a.offset = weight_offset;
-    a.eps = eps;
+    // The kernel's reciprocal root takes a subnormal number as 0, and a row of zeros
+    // would be 0 / 0. The mean square of any other row is 2^-72 or more, beside
+    // which no such eps shows.
+    a.eps = eps > 0.f ? std::max(eps, std::numeric_limits<float>::min()) : eps;
     a.per_width = static_cast<float>(1.0 / static_cast<double>(width));
     a.format = format;
     a.group = group_size;
