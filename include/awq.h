@@ -780,8 +780,8 @@ awq_status awq_kv_attention(const awq_kv_cache* cache, const awq_kv_seqs* seqs,
  *   residual_out   device, fp16 [rows, width] or NULL (output; may be x_f16 or
  *                  residual_f16 itself, with the same stride)
  *   weight_f16     device, fp16 [width] or NULL (y = h / sqrt(..))
- *   weight_offset  finite; 0, or 1 where the stored weight is the difference
- *                  from 1
+ *   weight_offset  -65504 .. 65504; 0, or 1 where the stored weight is the
+ *                  difference from 1
  *   eps            finite, >= 0
  *   rows, width    rows >= 0, 1 <= width <= 2^24; rows + 3 below 2^32
  *                  over the threads of a row, width / 8 rounded up to a power

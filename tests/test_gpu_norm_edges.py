@@ -53,3 +53,23 @@ def test_the_smallest_eps(eps, fmt):
         check_f16(host(got), y, 96)
     else:
         check_8bit(values(got[0]), host(got[1]), y, fmt, 0)
+
+
+@pytest.mark.parametrize("offset", [1e36, -65505.0, 65504.0, -65504.0])
+def test_the_largest_offsets(offset):
+    """An offset as large as the largest weight: the 8-bit scales hold y, as far
+    from fp16 as it is. One past that is refused: the unscaled products pass
+    fp32, and finite rows had infinite scales."""
+    x, r, w = inputs([23], 3, 256)
+    x[1] = 65504
+    x[2] = np.float16(6e-8)
+    r[2] = 0
+    _, y = lo.rmsnorm(x, w, 1e-5, r, offset)
+    for fmt in ("int8", "e4m3"):
+        call = lambda: awq.awq_rmsnorm(dev(x), dev(w), residual=dev(r), weight_offset=offset, fmt=fmt, group_size=64)  # noqa: E731
+        if abs(offset) > 65504:
+            with pytest.raises(awq.AwqError):
+                call()
+        else:
+            codes, scales = call()
+            check_8bit(values(codes), host(scales), y, fmt, 64)

@@ -1,5 +1,6 @@
-"""Integers that size what a call fills: of other kinds than Python's own, and
-past what a C int holds."""
+"""Arguments of the operators between a decoder layer's linear layers at the ends
+of their ranges (host only): integers that size what a call fills, of other kinds
+than Python's own and past what a C int holds; the norm's offset."""
 
 import ctypes
 
@@ -46,3 +47,11 @@ def test_rotary_dim_past_a_c_int(entry):
     for bad in (0, 1, 7, -64, 4098, True):
         with pytest.raises(awq.AwqError):
             awq.rope_frequencies(bad)
+
+
+def test_norm_offsets():
+    L = awq.load()
+    for bad in (1e36, 65505.0, -65536.0, float("nan"), float("inf")):
+        assert L.awq_rmsnorm(0x10000, 64, None, 0, None, 0, None, bad, 1e-5, 4, 64, 0, 0, 0x20000, 64, None, None) == 4
+    for good in (65504.0, -65504.0, 1.0):       # (no rows: nothing to do)
+        assert L.awq_rmsnorm(0x10000, 64, None, 0, None, 0, None, good, 1e-5, 0, 64, 0, 0, 0x20000, 64, None, None) == 0

@@ -1021,7 +1021,8 @@ awq_status awq_rmsnorm(const void* x_f16, int64_t x_stride, const void* residual
     if (group_size != 0 && (format == AWQ_NORM_F16 || (group_size != 32 && group_size != 64 && group_size != 128 &&
                                                        group_size != 256 && group_size != 512)))
         return AWQ_ERR_CONFIG;
-    if (!std::isfinite(weight_offset) || !std::isfinite(eps) || eps < 0.f) return AWQ_ERR_CONFIG;
+    // (an offset as large as the largest weight keeps the unscaled products in fp32)
+    if (!(std::fabs(weight_offset) <= kHalfMax) || !std::isfinite(eps) || eps < 0.f) return AWQ_ERR_CONFIG;
     if (rows < 0 || rows >= int64_t{1} << 31 || width < 1 || width > int64_t{1} << 24 ||
         (group_size != 0 && width % group_size != 0))
         return AWQ_ERR_SHAPE;
