@@ -1,6 +1,6 @@
 """Arguments of the operators between a decoder layer's linear layers at the ends
 of their ranges (host only): integers that size what a call fills, of other kinds
-than Python's own and past what a C int holds; the norm's offset."""
+than Python's own and past what a C int holds; the norm's offset; strides."""
 
 import ctypes
 
@@ -55,3 +55,14 @@ def test_norm_offsets():
         assert L.awq_rmsnorm(0x10000, 64, None, 0, None, 0, None, bad, 1e-5, 4, 64, 0, 0, 0x20000, 64, None, None) == 4
     for good in (65504.0, -65504.0, 1.0):       # (no rows: nothing to do)
         assert L.awq_rmsnorm(0x10000, 64, None, 0, None, 0, None, good, 1e-5, 0, 64, 0, 0, 0x20000, 64, None, None) == 0
+
+
+@pytest.mark.parametrize("stride", [2 ** 39, 2 ** 40 - 1])
+def test_interleaved_rows_of_the_largest_strides(stride):
+    """Rows of the rotation's output that share memory, their tokens' reach past
+    64 bits."""
+    L = awq.load()
+    table = awq._RopeTableStruct(0x10000, 128, 0, 1.0)
+    q = awq._RopeHeadsStruct(0x10000, 0x20000, 256, 128, stride, 2 ** 39, 65535)
+    for n in (2 ** 24 - 1, 2 ** 23 + 1, 2 ** 23 + 5, 1000):
+        assert L.awq_rope(ctypes.byref(table), 0x10000, None, ctypes.byref(q), None, 128, n, None) == 2

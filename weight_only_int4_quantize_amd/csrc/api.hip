@@ -991,8 +991,9 @@ awq_status rope_heads(const awq_rope_heads* t, int head_dim, int64_t n_tokens, R
     const bool tokens = n_tokens > 1, heads = t->heads > 1;
     if (!stride_ok(t->out_token_stride, tokens ? head_dim : 0) || !stride_ok(t->out_head_stride, heads ? head_dim : 0))
         return AWQ_ERR_SHAPE;
+    // (2^24 tokens times a stride of 2^40 pass 64 bits)
     if (tokens && heads && t->out_token_stride < (t->heads - 1) * t->out_head_stride + head_dim &&
-        t->out_head_stride < (n_tokens - 1) * t->out_token_stride + head_dim)
+        t->out_head_stride < static_cast<__int128>(n_tokens - 1) * t->out_token_stride + head_dim)
         return AWQ_ERR_SHAPE;
     if (t->in == t->out && ((tokens && t->in_token_stride != t->out_token_stride) ||
                             (heads && t->in_head_stride != t->out_head_stride)))
