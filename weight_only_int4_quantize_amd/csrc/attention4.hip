@@ -647,26 +647,30 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv4_pr
 // ---------------------------------------------------------------- launch
 
 template <int D, int NP>
-void launch_np(const KvAttentionArgs& a, const Plan& p, const Split& sp, hipStream_t stream) {
+awq_status launch_np(const KvAttentionArgs& a, const Plan& p, const Split& sp, hipStream_t stream) {
     const auto decode = [&](auto sets) {
         hipLaunchKernelGGL((kv4_decode_kernel<D, NP, decltype(sets)::value>),
                            dim3(static_cast<unsigned>(a.c.heads), static_cast<unsigned>(p.row_tiles * a.n_seqs),
                                 static_cast<unsigned>(p.splits)),
                            dim3(kDecodeWaves * kWave), 0, stream, a, sp, p.splits, static_cast<int>(p.row_tiles));
     };
-    if (p.rows == kDecodeRows) decode(std::integral_constant<int, 1>{});
-    else if (p.decode) {
-        if constexpr (D <= kWideDim) decode(std::integral_constant<int, 2>{});
-    } else
+    if (!p.decode) {
         hipLaunchKernelGGL((kv4_prefill_kernel<D, NP>),
                            dim3(static_cast<unsigned>(p.row_tiles * p.splits * a.c.heads), 1,
                                 static_cast<unsigned>(a.n_seqs)),
                            dim3(kPrefillWaves * kWave), 0, stream, a, sp, p.splits);
+    } else if (p.rows == kDecodeRows) {
+        decode(std::integral_constant<int, 1>{});
+    } else if constexpr (D <= kWideDim) {
+        decode(std::integral_constant<int, 2>{});
+    } else {
+        return AWQ_ERR_CONFIG;      // no plan asks for it
+    }
+    return last_launch_status();
 }
 template <int D>
-void launch_d(const KvAttentionArgs& a, const Plan& p, const Split& sp, hipStream_t stream) {
-    if (a.c.log2_page == 5) launch_np<D, 2>(a, p, sp, stream);
-    else launch_np<D, 1>(a, p, sp, stream);
+awq_status launch_d(const KvAttentionArgs& a, const Plan& p, const Split& sp, hipStream_t stream) {
+    return a.c.log2_page == 5 ? launch_np<D, 2>(a, p, sp, stream) : launch_np<D, 1>(a, p, sp, stream);
 }
 
 }  // namespace
@@ -676,14 +680,13 @@ awq_status launch_kv4_attention(const KvAttentionArgs& a, void* workspace, hipSt
     if (!launchable(p, a.c.heads)) return AWQ_ERR_SHAPE;
     const Split sp = split_of(p, workspace);
     switch (a.head_dim) {
-        case 64: launch_d<64>(a, p, sp, stream); break;
-        case 96: launch_d<96>(a, p, sp, stream); break;
-        case 128: launch_d<128>(a, p, sp, stream); break;
-        case 192: launch_d<192>(a, p, sp, stream); break;
-        case 256: launch_d<256>(a, p, sp, stream); break;
+        case 64: return launch_d<64>(a, p, sp, stream);
+        case 96: return launch_d<96>(a, p, sp, stream);
+        case 128: return launch_d<128>(a, p, sp, stream);
+        case 192: return launch_d<192>(a, p, sp, stream);
+        case 256: return launch_d<256>(a, p, sp, stream);
         default: return AWQ_ERR_CONFIG;
     }
-    return last_launch_status();
 }
 
 }  // namespace awq
