@@ -38,22 +38,19 @@ constexpr float kPrefillUnit = 12.0f;   // the same in prefill
 constexpr float kSlack = 3.0f;          // what t and t + e may pass their maxima by there
 constexpr float kTinyScale = 1.0e-20f;  // scales at or below it count as it
 
-// ones in bytes from .. to - 1 of 16
-__device__ inline kv_u32x4 bytes_between(int from, int to) {
+// Ones in the first n bytes of 16.
+__device__ inline kv_u32x4 first_bytes(int n) {
     kv_u32x4 r;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const auto below = [&](int n) {     // bytes 0 .. n - 1 of the word
-            const int k = min(max(n - 4 * j, 0), 4);
-            return k == 4 ? 0xFFFFFFFFu : (1u << (8 * k)) - 1u;
-        };
-        r[j] = below(to) & ~below(from);
+        const int k = min(max(n - 4 * j, 0), 4);
+        r[j] = k == 4 ? 0xFFFFFFFFu : (1u << (8 * k)) - 1u;
     }
     return r;
 }
 // whether any of the rows sees a position of page p
 __device__ inline bool seen(const Span& s, int p, int log2_page) {
-    return (p << log2_page) < s.end && (static_cast<int64_t>(p) + 1) << log2_page > s.begin;
+    return (p << log2_page) < s.end && (p + 1) << log2_page > s.begin;
 }
 
 // ---------------------------------------------------------------- few rows
@@ -227,7 +224,8 @@ __global__ __launch_bounds__(kDecodeWaves* kWave, D <= 64 ? 4 : D <= 96 ? 3 : D 
                 for (int i = 0; i < 16; ++i)
                     s[i] = ok && j0 + i >= lo && j0 + i < hi ? s[i] : -__builtin_huge_valf();
                 // bytes that none of the rows sees may be anything, fp8 NaN among them
-                const kv_u32x4 keep = ok ? bytes_between(span.begin - j0, span.end - j0) : kv_u32x4{0u, 0u, 0u, 0u};
+                kv_u32x4 keep = first_bytes(ok ? span.end - j0 : 0);
+                if (span.begin > tb) keep &= ~first_bytes(span.begin - j0);
 #pragma unroll
                 for (int t = 0; t < DT; ++t) vr[t] &= keep;
             }
@@ -466,9 +464,10 @@ __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv_pre
             const int d = e % D, tc = e / D;
             if (!whole) {
                 // bytes that none of the rows sees may be anything, fp8 NaN among them
+                const bool ok = NP == 2 && tc >= 2 ? pg.held[NP - 1] : pg.held[0];
                 const int j0 = tb + 16 * tc;
-                vr[i] &= (NP == 2 && tc >= 2 ? pg.held[NP - 1] : pg.held[0])
-                             ? bytes_between(span.begin - j0, span.end - j0) : kv_u32x4{0u, 0u, 0u, 0u};
+                vr[i] &= first_bytes(ok ? span.end - j0 : 0);
+                if (span.begin > tb) vr[i] &= ~first_bytes(span.begin - j0);
             }
             vs[(2 * tc) * D + d] = kv_unpack8<FORMAT>(vr[i][0], vr[i][1]);
             vs[(2 * tc + 1) * D + d] = kv_unpack8<FORMAT>(vr[i][2], vr[i][3]);
