@@ -680,9 +680,12 @@ typedef struct {
  * of a value), in float32:
  *   lo = min x,  s = the largest fp16 number not above (max x - lo) / 15
  *   codes = clamp(round((x - lo) / s), 0, 15), 0 where s is 0
- * A number thus carries at most half a step (plus 15 times what s was cut by,
- * under 2^-10 of it, at the top of the range); what was written before stays,
- * also at later places of the page. A call takes up to 2^24 pieces of 32
+ * A number is thus off by at most half a step or, at the top of the range, 15
+ * times what s was cut by, and by the rounding of lo + s * code to fp16. The cut
+ * is under 2^-10 of s, or under 2^-24 where s is subnormal (a range below
+ * 15 * 2^-14): there a top number loses up to 15 * 2^-24, and a range below
+ * 15 * 2^-24 is stored as its smallest number alone. What was written before
+ * stays, also at later places of the page. A call takes up to 2^24 pieces of 32
  * consecutive tokens (that max_tokens from any place can touch) times heads.
  * NaN is stored as 0, an infinity as +-65504.
  *
@@ -724,17 +727,19 @@ awq_status awq_kv_read(const awq_kv_cache* cache, const awq_kv_seqs* seqs,
  * `window` of them (j > p - window). A query that sees no position gets
  * o = 0 and lse = -infinity. Logits, softmax statistics and sums are fp32;
  * the weights enter the second product as two fp16 numbers (a weight cut to
- * fp16 and what that left), within 2^-20 of themselves. A query with a NaN
- * that sees a position gets NaN (o and lse); no other row is touched by it,
- * or by an infinity. A position that no query of its sequence sees may hold
- * anything, and so may the scales of a page of such positions. With
- * AWQ_KV_INT4 the products' numbers are the cached ones, those awq_kv_read
- * gives.
+ * fp16 and what that left), within 2^-20 of themselves or 2^-34 of the row's
+ * largest, whichever is more (over an 8-bit cache the largest times its page's
+ * scale). A query with a NaN that sees a position gets NaN (o and lse); no other
+ * row is touched by it, or by an infinity. A position that no query of its
+ * sequence sees may hold anything, and so may the scales of a page of such
+ * positions. With AWQ_KV_INT4 the products' numbers are the cached ones, those
+ * awq_kv_read gives.
  *
  *   q_f16        device, fp16 [n_tokens, n_heads, head_dim], channels
  *                contiguous, 16-byte aligned, strides in halves, multiples
  *                of 8
- *   n_heads      a multiple of n_kv_heads
+ *   n_heads      a multiple of n_kv_heads; more than 32767 kv heads may be
+ *                refused where max_tokens * r is 17 to 32
  *   scale        finite
  *   causal       0 or 1; window 0 (none) or > 0 (causal only)
  *   out_f16      device, fp16 [n_tokens, n_heads, head_dim] (output, same
@@ -822,7 +827,10 @@ awq_status awq_rmsnorm(const void* x_f16, int64_t x_stride,
  *                        rotated numbers times 0.1 ln(factor) + 1. The pair
  *                        that turns n times is number
  *                        R ln(L / (2 pi n)) / (2 ln base); the ramp's ends are
- *                        rounded outwards to whole pairs.
+ *                        rounded outwards to whole pairs and kept at 0 or more
+ *                        (the first), R - 1 or less (the last). A ramp that
+ *                        ends at or before its start goes from one pair to the
+ *                        next: the pairs up to the start keep f_i.
  *   AWQ_ROPE_WAVELENGTH  f_i / factor at L / wavelength <= low, f_i at >= high,
  *                        linear in that quotient between
  *

@@ -121,8 +121,16 @@ constexpr int join_floats(int rows, int threads) { return kJoin + rows + threads
 // the splits in order (deterministic; nobody waits on anybody).
 // ALONE: each thread joins the parts of its own outputs, eight parts' loads in
 // flight, without LDS and barriers, in less code (which a block reaches once, and
-// cold: 0.3 us a kilobyte). 1 x 1000 tokens of 32 heads over the 4-bit cache, four
-// parts, 9.8 -> 8.3 us; 1 x 8000 of 8, 32 parts, 12.5 -> 11.7; 64 parts the same.
+// cold: 0.3 us a kilobyte). Over the 4-bit cache, 128 channels, in a graph (us, in
+// brackets by the join below): 1 x 512 to 4000 tokens of 32 heads, 2 to 8 parts,
+// 7.6 (9.0), 8.2 (9.6), 10.5 (12.0); 1 x 8000 of 8 heads, 32 parts, 1 / 8 query rows
+// 11.5 (11.7) / 11.7 (12.9); 128 parts of one head of 32768, 1 / 8 / 16 rows
+// 16.7 (13.4) / 16.8 (19.4) / 25.5 (27.1). So one row of 64 parts and more, 32
+// threads at work on them one batch after the other, is slower by 1 to 3.5 us: one
+// sequence of four kv heads or fewer that share no queries. A second instance for
+// that alone was not made. The 8-bit decode kernel still takes the join below; this
+// one measured 7.8 (9.1) for 1 x 1000 of 32 heads, 11.2 (12.1) for 1 x 8000 of 8 with
+// 4 rows, 34.9 (31.8) for 1 x 131072 of 4 with one.
 template <int D, int ROWS, int NT, bool ALONE = false, class Offset>
 __device__ inline void finish_rows(const KvAttentionArgs& a, const KvSeq& sq, const Rows& rw, const Offset& offset,
                                    const float* so, int so_stride, const float* sm, const float* sl, float* scratch,

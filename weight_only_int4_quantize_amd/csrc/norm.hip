@@ -10,7 +10,10 @@
 // from h itself.
 //
 // Bound by HBM: 2 bytes an element of x, r, the sum and y (4096 x 8192, 268 MB:
-// 51 us, 5.3 TB/s, a copy's rate), few rows by a launch's length.
+// 51 us, 5.3 TB/s, a copy's rate; to int8 by rows or to e4m3 by groups of 128, 236 MB,
+// 45-47 in a graph), few rows by a launch's length. Rows narrower than 512 leave
+// lanes of their wave idle: 327680 x 128 67 us, where a copy takes 32; x 256, half as
+// many, 37.
 #include "awq_internal.h"
 
 namespace awq {
@@ -280,8 +283,9 @@ awq_status launch_p(const NormArgs& a, hipStream_t stream) {
     return last_launch_status();
 }
 // As many threads to a row as it has pieces of eight, up to 1024: measured with a
-// residual and its sum (us, in brackets with a quarter as many threads and four
-// pieces each): 1 x 4096 2.8 (4.4), 1 x 8192 3.3 (4.7), 64 x 8192 e4m3 4.4 (6.0),
+// residual and its sum, calls back to back as this rule was made (in a graph 1 x 4096
+// takes 2.7, 64 x 8192 e4m3 3.9; us, in brackets with a quarter as many threads and
+// four pieces each): 1 x 4096 2.8 (4.4), 1 x 8192 3.3 (4.7), 64 x 8192 e4m3 4.4 (6.0),
 // 256 x 4096 3.7 (5.4), 4096 x 8192 50.7 (54.2). Between, 256 threads are some 8%
 // better (1024 x 4096 7.8 against 8.5): not worth instances of their own.
 template <int FORMAT>
