@@ -332,12 +332,17 @@ struct Plan {
 // pays for two or more pieces.
 // Over the 4-bit cache, 17 to 32 rows are one block's, which unpacks the keys and
 // values once for both sixteens, where the sequences' kv heads are two to a CU, or
-// enough for few parts to join and long. Measured, 8 query heads a kv head, 8 kv
-// heads of 128, 4 tokens (us, in brackets as two blocks of 16 rows): 64 x 4096 87
-// (109), 64 x 64 9.0 (11.0), 8 x 32768 92 (120), 8 x 8192 29.5 (33.5), 2 x 131072
-// 93 (115); but 2 x 32768 37.7 (35.5), 1 x 131072 63 (64), one kv head 1 x 262144 59
-// (41), 16 x 2000 21.7 (21.1), 1 x 1000 11.2 (8.8). With 192 channels and more it
-// leaves one wave per SIMD: 64 x 4096 152 (171), but 16 x 4096 54 (48).
+// enough for few parts to join and long. Measured in a graph, 8 query heads a kv
+// head, 8 kv heads of 128, 4 tokens (us, as two blocks of 16 rows, as one):
+//   taken     64 x 64 11.1, 9.1; 64 x 4096 102, 78; 16 x 4096 30.3, 26.9; 8 x 8192
+//             30.5, 27.3; 4 x 16384 30.5, 29.1; 8 x 32768 105, 78; 2 x 65536 55, 50;
+//             2 x 131072 104, 84; 16 kv heads 1 x 65536 53, 49; one 16 x 65536 55, 50
+//   not       16 x 2000 19.3, 19.7; 2 x 32768 31.8, 34.4; 1 x 65536 35.2, 42.3;
+//             1 x 131072 56.2, 58.7; 1 x 1000 8.8, 11.2; one kv head 1 x 262144 40, 59;
+//             and, where it would gain, 32 x 1000 17.7, 16.6
+// (another card, calls back to back: 64 x 4096 109, 87; 2 x 131072 115, 93). With
+// 192 channels and more it leaves one wave per SIMD: 64 x 4096 171, 152, but 16 x
+// 4096 48, 54.
 inline Plan plan_for(int format, int head_dim, int n_seqs, int kv_heads, int ratio, int64_t max_tokens, int64_t max_len,
                      bool have_workspace) {
     Plan p;
