@@ -55,8 +55,9 @@ __device__ inline half8_t from_n(half8_t v, int n) {
 // 390 MB, 86-87 us, 4.5 TB/s (the kernel's loads alone 5.5; the VALU busy 66% of
 // the time, the matrix cores 20%); 131072 and 131072 tokens 60 us, 5.2 TB/s.
 // 1 x 1000 tokens of 32 heads 7.7-8.2 us, a row of latencies. One kv head leaves
-// CUs idle: 1 x 262144 29 us (39 MB, 7.5 at a copy's rate), at most 128 blocks. Not faster: six,
-// eight or sixteen waves a block, two tiles in flight, splits of 512 positions.
+// CUs idle: 1 x 262144 29 us (39 MB, 7.5 at a copy's rate), at most 128 blocks.
+// Not faster: six, eight or sixteen waves a block, two tiles in flight, splits of
+// 512 positions.
 template <int D, int NP, int SETS>
 __global__ __launch_bounds__(kDecodeWaves* kWave, SETS == 2 ? 2 : D <= 96 ? 4 : D <= 128 ? 3 : 2) void
 kv4_decode_kernel(KvAttentionArgs a, Split sp, int n_splits, int row_tiles) {
@@ -362,9 +363,10 @@ kv4_decode_kernel(KvAttentionArgs a, Split sp, int n_splits, int row_tiles) {
 // Bound by the matrix cores and the VALU, neither of them full (52% and 58%
 // busy): 2 x 2048 tokens of 4096 (the second sequence's 1707 of 2560), 32 heads on 8
 // of 128, 242-249 us on different cards, 607-623 TFLOP/s, or 905-930 with the
-// weights' second parts, where a large matrix product reaches 1226. With one part, rounded, 200 us, and an error of 2.9e-4 in place of
-// 2.1e-4. Not faster: the next tile's logits before this one's softmax, the
-// instructions dealt out in a fixed order, raised wave priorities, eight waves.
+// weights' second parts, where a large matrix product reaches 1226. With one part,
+// rounded, 200 us, and an error of 2.9e-4 in place of 2.1e-4. Not faster: the next
+// tile's logits before this one's softmax, the instructions dealt out in a fixed
+// order, raised wave priorities, eight waves.
 template <int D, int NP>
 __global__ __launch_bounds__(kPrefillWaves* kWave, D <= 128 ? 2 : 1) void kv4_prefill_kernel(KvAttentionArgs a, Split sp,
                                                                                            int n_splits) {
